@@ -36,7 +36,8 @@ EXPORTS = ("kvq_status_str", "kvq_cache_bytes", "kvq_packed_bytes_per_token", "k
            "kvq_cache_status", "kvq_debug_decode_unset_wait", "kvq_debug_decode_timed", "kvq_decode_step",
            "kvq_step_staging_bytes", "kvq_decode_step_host", "kvq_draw_rotation_signs", "kvq_draw_qjl_matrix",
            "kvq_partial_floats", "kvq_decode_partials", "kvq_combine_partials",
-           "kvq_cache_bytes_paged", "kvq_cache_init_paged")
+           "kvq_cache_bytes_paged", "kvq_cache_init_paged", "kvq_extend_block_table", "kvq_slot_map",
+           "kvq_quantize_slots", "kvq_cache_set_lengths", "kvq_chunk_workspace_bytes", "kvq_chunk_attention")
 KVQ_STATUS_WAIT_TIMEOUT = 1
 
 
@@ -97,6 +98,12 @@ def load() -> ctypes.CDLL:
         "kvq_cache_init_paged": ([P(VP), P(kvq_cfg), I32, I32, I32, VP, VP, SZ, VP, VP, VP], I32),
         "kvq_decode_partials": ([VP, VP, I32, VP, VP, SZ, VP], I32),
         "kvq_combine_partials": ([VP, I32, I32, I32, I32, VP, VP], I32),
+        "kvq_extend_block_table": ([VP, VP, I32, VP, I32, VP, VP, I32, VP, VP, VP, VP], I32),
+        "kvq_slot_map": ([VP, VP, VP, I32, VP, I32, I32, I32, VP, VP, VP, VP], I32),
+        "kvq_quantize_slots": ([VP, VP, VP, I32, VP, I32, VP], I32),
+        "kvq_cache_set_lengths": ([VP, VP, VP], I32),
+        "kvq_chunk_workspace_bytes": ([VP, I32, I32, P(SZ)], I32),
+        "kvq_chunk_attention": ([VP, VP, I32, I32, VP, VP, VP, VP, SZ, VP], I32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -333,6 +340,114 @@ def kvq_decode_step_host(handle, K: torch.Tensor, V: torch.Tensor, q: torch.Tens
     return out
 
 
+# ---- ragged serving path
+
+def _ints(fn: str, dtype, **tensors):
+    """Contiguous CUDA tensors of one integer type on one device, the current one (the calls launch there)."""
+    _on_device(fn, **tensors)
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.dtype != dtype:
+            raise TypeError(f"{fn}: {name} must be {dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{fn}: {name} must be contiguous")
+        _current(fn, **{name: t})
+
+
+def _current(fn: str, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{fn}: {name} is on {t.device}, not on the current device")
+
+
+def kvq_extend_block_table(held: torch.Tensor, n_new: torch.Tensor, free_pages: torch.Tensor, block_table: torch.Tensor,
+                           seq_start: torch.Tensor, ctx_lens: torch.Tensor, taken: torch.Tensor, cursor=None, stream=None):
+    """Give pages to n_new [batch] new tokens of requests holding held [batch]: writes block_table [batch,
+    pages_per_seq] from free_pages [n_free] (starting at cursor [1]), seq_start [batch + 1], ctx_lens [batch]
+    and taken [2] (pages given, requests refused). All int32 CUDA tensors."""
+    fn = "kvq_extend_block_table"
+    _ints(fn, torch.int32, held=held, n_new=n_new, free_pages=free_pages, block_table=block_table, seq_start=seq_start,
+          ctx_lens=ctx_lens, taken=taken, cursor=cursor)
+    B = held.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != B or n_new.numel() != B or seq_start.numel() != B + 1 \
+            or ctx_lens.numel() != B or taken.numel() != 2 or (cursor is not None and cursor.numel() != 1):
+        raise ValueError(f"{fn}: held, n_new, ctx_lens [batch], seq_start [batch + 1], block_table [batch, pages_per_seq], "
+                         "taken [2], cursor [1]")
+    _check(fn, load().kvq_extend_block_table(_ptr(held), _ptr(n_new), B, _ptr(free_pages), free_pages.numel(), _ptr(cursor),
+                                             _ptr(block_table), block_table.shape[1], _ptr(seq_start), _ptr(ctx_lens),
+                                             _ptr(taken), _stream(stream)))
+
+
+def kvq_slot_map(held: torch.Tensor, seq_start: torch.Tensor, ctx_lens: torch.Tensor, block_table: torch.Tensor, n_pages: int,
+                 seq_ids, positions, slots: torch.Tensor, stream=None):
+    """Request, position (int32 [n_tokens], either may be None) and page slot (int64 [n_tokens], -1: none) of
+    every new token."""
+    fn = "kvq_slot_map"
+    _ints(fn, torch.int32, held=held, seq_start=seq_start, ctx_lens=ctx_lens, block_table=block_table, seq_ids=seq_ids,
+          positions=positions)
+    _ints(fn, torch.int64, slots=slots)
+    B, n = held.numel(), slots.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != B or seq_start.numel() != B + 1 or ctx_lens.numel() != B \
+            or any(t is not None and t.numel() != n for t in (seq_ids, positions)):
+        raise ValueError(f"{fn}: held, ctx_lens [batch], seq_start [batch + 1], block_table [batch, pages_per_seq], "
+                         "seq_ids, positions, slots [n_tokens]")
+    _check(fn, load().kvq_slot_map(_ptr(held), _ptr(seq_start), _ptr(ctx_lens), B, _ptr(block_table), block_table.shape[1],
+                                   n_pages, n, _ptr(seq_ids), _ptr(positions), _ptr(slots), _stream(stream)))
+
+
+def kvq_quantize_slots(handle, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, stream=None):
+    """Code K, V [n_tokens, n_kv_heads, head_dim] into page slots int64 [n_tokens] (negative: skipped)."""
+    fn = "kvq_quantize_slots"
+    _on_device(fn, K=K, V=V)
+    _ints(fn, torch.int64, slots=slots)
+    if K.dtype not in DTYPES or V.dtype != K.dtype:
+        raise TypeError("K and V must both be float32 or bfloat16")
+    if not (K.is_contiguous() and V.is_contiguous()):
+        raise ValueError("K and V must be contiguous")
+    if K.dim() != 3 or K.shape != V.shape or slots.numel() != K.shape[0]:
+        raise ValueError("K and V must be [n_tokens, n_kv_heads, head_dim] and slots [n_tokens]")
+    _current(fn, K=K, V=V)
+    _check(fn, load().kvq_quantize_slots(handle, _ptr(K), _ptr(V), DTYPES[K.dtype], _ptr(slots), K.shape[0],
+                                         _stream(stream)))
+
+
+def kvq_cache_set_lengths(handle, lens, batch: int, stream=None):
+    """Set the lengths of all sequences (batch host integers)."""
+    a = np.ascontiguousarray(lens)
+    if a.shape != (batch,) or a.dtype.kind not in "iu" or (a.size and (a.max() > 2**31 - 1 or a.min() < -2**31)):
+        raise ValueError("lens must hold one integer per sequence")
+    a = a.astype(np.int32)
+    _check("kvq_cache_set_lengths", load().kvq_cache_set_lengths(handle, a.ctypes.data_as(ctypes.c_void_p), _stream(stream)))
+
+
+def kvq_chunk_workspace_bytes(handle, dtype, n_tokens: int) -> int:
+    out = ctypes.c_size_t()
+    _check("kvq_chunk_workspace_bytes",
+           load().kvq_chunk_workspace_bytes(handle, DTYPES[dtype], n_tokens, ctypes.byref(out)))
+    return out.value
+
+
+def kvq_chunk_attention(handle, q: torch.Tensor, seq_start: torch.Tensor, ctx_lens, out: torch.Tensor,
+                        workspace: torch.Tensor, stream=None):
+    """Attention of new tokens' queries q [n_tokens, n_q_heads, head_dim], request b's in rows seq_start[b] ..
+    seq_start[b + 1] - 1, over the packed cache of ctx_lens [batch] tokens (None: the cache's lengths). out is
+    like q."""
+    fn = "kvq_chunk_attention"
+    _on_device(fn, q=q, out=out, workspace=workspace)
+    _ints(fn, torch.int32, seq_start=seq_start, ctx_lens=ctx_lens)
+    if q.dtype not in DTYPES or out.dtype != q.dtype:
+        raise TypeError("q and out must both be float32 or bfloat16")
+    if not (q.is_contiguous() and out.is_contiguous() and workspace.is_contiguous()):
+        raise ValueError("q, out and workspace must be contiguous")
+    if q.dim() != 3 or out.shape != q.shape:
+        raise ValueError("q and out must be [n_tokens, n_q_heads, head_dim]")
+    _current(fn, q=q, out=out, workspace=workspace)
+    _check(fn, load().kvq_chunk_attention(handle, _ptr(q), DTYPES[q.dtype], q.shape[0], _ptr(seq_start), _ptr(ctx_lens),
+                                          _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                          _stream(stream)))
+
+
 def kvq_decode_attention_static(handle, q: torch.Tensor, out: torch.Tensor, stream=None):
     """Decode attention without a workspace (partials in the library's fixed device array)."""
     _on_device("kvq_decode_attention_static", q=q, out=out)
@@ -528,6 +643,44 @@ class KvqCache:
             raise ValueError(f"decode_partials: partials must be {(self.batch, self.cfg.n_q_heads, n)}")
         kvq_decode_partials(self.handle, q, partials, self.workspace, stream)
         return partials
+
+    def quantize_slots(self, K, V, slots, stream=None):
+        """Code a token-major batch K, V [n_tokens, n_kv_heads, head_dim] into page slots (kvq_quantize_slots)."""
+        if K.dim() != 3 or tuple(K.shape[1:]) != (self.cfg.n_kv_heads, self.cfg.head_dim) or K.shape != V.shape:
+            raise ValueError(f"quantize_slots: K, V must be [n_tokens, {self.cfg.n_kv_heads}, {self.cfg.head_dim}]")
+        kvq_quantize_slots(self.handle, K, V, slots, stream)
+
+    def set_lengths(self, lens, stream=None):
+        """Set every sequence's length (kvq_cache_set_lengths)."""
+        kvq_cache_set_lengths(self.handle, lens, self.batch, stream)
+
+    def chunk_attention(self, q, seq_start, ctx_lens=None, out=None, workspace=None, stream=None):
+        """Attention of a ragged batch of new tokens (kvq_chunk_attention); returns out, like q. Without a
+        workspace the cache keeps one per stream, grown to the largest call there; a captured call takes one
+        from the graph's own memory, so that no two graphs share it."""
+        if q.dim() != 3 or tuple(q.shape[1:]) != (self.cfg.n_q_heads, self.cfg.head_dim):
+            raise ValueError(f"chunk_attention: q must be [n_tokens, {self.cfg.n_q_heads}, {self.cfg.head_dim}]")
+        if seq_start.numel() != self.batch + 1 or (ctx_lens is not None and ctx_lens.numel() != self.batch):
+            raise ValueError(f"chunk_attention: seq_start [{self.batch + 1}] and ctx_lens [{self.batch}]")
+        if q.dtype not in DTYPES:
+            raise TypeError("q must be float32 or bfloat16")
+        if out is None:
+            out = torch.empty_like(q)
+        if workspace is None:
+            workspace = self._chunk_workspace(kvq_chunk_workspace_bytes(self.handle, q.dtype, q.shape[0]), q.device, stream)
+        kvq_chunk_attention(self.handle, q, seq_start, ctx_lens, out, workspace, stream)
+        return out
+
+    def _chunk_workspace(self, need, device, stream):
+        stream = torch.cuda.current_stream() if stream is None else stream
+        with torch.cuda.stream(stream):  # memory of that stream: a workspace it outgrows is reused in its order
+            if torch.cuda.is_current_stream_capturing():
+                return torch.empty(need, dtype=torch.uint8, device=device)
+            kept = self.__dict__.setdefault("chunk_workspaces", {})
+            have = kept.get(stream.cuda_stream)
+            if have is None or have.numel() < need:
+                have = kept[stream.cuda_stream] = torch.empty(need, dtype=torch.uint8, device=device)
+            return have
 
     def lengths(self):
         return kvq_cache_lengths(self.handle, self.batch)

@@ -1167,3 +1167,176 @@ extern "C" kvq_status kvq_decode_attention_static(const kvq_cache* c, const void
   if (st != KVQ_OK) return st;
   return kvq_decode_attention(c, q, dtype, out, scratch, kStaticScratchBytes, stream);
 }
+
+// ---- ragged serving path: block tables, slot maps, appends by slots, chunk attention ----------------
+
+namespace {
+// The cache kinds the ragged path handles: rotated codes, no bf16 window.
+bool ragged_supported(const kvq_cache* c) { return !c->is_fp4 && !has_window(c); }
+bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+ChunkLayout chunk_layout_of(const kvq_cache* c, int n_tokens) {
+  return chunk_layout(n_tokens, c->batch, c->cfg.n_q_heads, c->cfg.n_kv_heads, c->k.qjl, c->v.qjl, c->sms);
+}
+}  // namespace
+
+extern "C" {
+
+kvq_status kvq_extend_block_table(const int32_t* held, const int32_t* n_new, int32_t batch, const int32_t* free_pages,
+                                  int32_t n_free, const int32_t* cursor, int32_t* block_table, int32_t pages_per_seq,
+                                  int32_t* seq_start, int32_t* ctx_lens, int32_t* taken, void* stream) {
+  if (!held || !n_new || !block_table || !seq_start || !ctx_lens || !taken) return KVQ_ERR_INVALID_ARG;
+  if (batch < 1 || pages_per_seq < 1 || n_free < 0 || (n_free > 0 && !free_pages)) return KVQ_ERR_INVALID_ARG;
+  if ((long)pages_per_seq * kTile * kTilePair > (1l << 30)) return KVQ_ERR_INVALID_ARG;
+  const void* in[] = {held, n_new, free_pages, cursor};
+  const void* out[] = {block_table, seq_start, ctx_lens, taken};
+  for (const void* p : in)
+    if (!aligned_to(p, 4)) return KVQ_ERR_ALIGNMENT;
+  for (int i = 0; i < 4; ++i) {
+    if (!aligned_to(out[i], 4)) return KVQ_ERR_ALIGNMENT;
+    for (const void* p : in)
+      if (p == out[i]) return KVQ_ERR_INVALID_ARG;  // blocks read every input while others write
+    for (int j = 0; j < i; ++j)
+      if (out[j] == out[i]) return KVQ_ERR_INVALID_ARG;
+  }
+  return launch_extend_block_table(held, n_new, batch, free_pages, n_free, cursor, block_table, pages_per_seq, seq_start,
+                                   ctx_lens, taken, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+kvq_status kvq_slot_map(const int32_t* held, const int32_t* seq_start, const int32_t* ctx_lens, int32_t batch,
+                        const int32_t* block_table, int32_t pages_per_seq, int32_t n_pages, int32_t n_tokens,
+                        int32_t* seq_ids, int32_t* positions, int64_t* slots, void* stream) {
+  if (batch < 1 || pages_per_seq < 1 || n_pages < 1 || n_tokens < 0) return KVQ_ERR_INVALID_ARG;
+  if ((long)pages_per_seq * kTile * kTilePair > (1l << 30)) return KVQ_ERR_INVALID_ARG;
+  if (n_tokens == 0) return KVQ_OK;
+  if (!held || !seq_start || !ctx_lens || !block_table || !slots) return KVQ_ERR_INVALID_ARG;
+  const void* ints[] = {held, seq_start, ctx_lens, block_table, seq_ids, positions};
+  for (const void* p : ints)
+    if (!aligned_to(p, 4)) return KVQ_ERR_ALIGNMENT;
+  if (!aligned_to(slots, 8)) return KVQ_ERR_ALIGNMENT;
+  const void* out[] = {seq_ids, positions, slots};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < 4; ++j)
+      if (out[i] && out[i] == ints[j]) return KVQ_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (out[i] && out[i] == out[j]) return KVQ_ERR_INVALID_ARG;
+  }
+  return launch_slot_map(held, seq_start, ctx_lens, batch, block_table, pages_per_seq, n_pages, n_tokens, seq_ids,
+                         positions, reinterpret_cast<long long*>(slots), reinterpret_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+kvq_status kvq_cache_set_lengths(kvq_cache* c, const int32_t* lens, void* stream) {
+  if (!c || !lens) return KVQ_ERR_INVALID_ARG;
+  if (has_window(c)) return KVQ_ERR_UNSUPPORTED;  // the window's rows would not follow
+  for (int i = 0; i < c->batch; ++i) {
+    if (lens[i] < 0) return KVQ_ERR_INVALID_ARG;
+    if (lens[i] > c->capacity) return KVQ_ERR_CAPACITY;
+  }
+  if (!on_cache_device(c)) return KVQ_ERR_INVALID_ARG;
+  for (int first = 0; first < c->batch; first += kMaxSeqPerLaunch) {
+    LengthParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.lens = c->d_lens;
+    p.first = first;
+    p.n = std::min(kMaxSeqPerLaunch, c->batch - first);
+    std::memcpy(p.value, lens + first, sizeof(int32_t) * p.n);
+    if (launch_set_lengths(p, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return KVQ_ERR_CUDA;
+    std::copy(lens + first, lens + first + p.n, c->lens.begin() + first);
+  }
+  return KVQ_OK;
+}
+
+kvq_status kvq_quantize_slots(kvq_cache* c, const void* K, const void* V, kvq_dtype dtype, const int64_t* slots,
+                              int32_t n_tokens, void* stream) {
+  if (!c || n_tokens < 0) return KVQ_ERR_INVALID_ARG;
+  if (dtype != KVQ_F32 && dtype != KVQ_BF16) return KVQ_ERR_INVALID_ARG;
+  if (!c->table || !ragged_supported(c)) return KVQ_ERR_UNSUPPORTED;
+  if (n_tokens == 0) return KVQ_OK;
+  if (!K || !V || !slots) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(K) || !aligned16(V) || !aligned_to(slots, 8)) return KVQ_ERR_ALIGNMENT;
+  if (!on_cache_device(c)) return KVQ_ERR_INVALID_ARG;
+  SlotQuantizeParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.src[0] = K;
+  p.src[1] = V;
+  p.bf16 = dtype == KVQ_BF16;
+  p.n_tokens = n_tokens;
+  p.heads = c->cfg.n_kv_heads;
+  p.slots = reinterpret_cast<const long long*>(slots);
+  p.region[0] = c->d_k;
+  p.region[1] = c->d_v;
+  p.n_pages = c->n_pages;
+  p.side[0] = c->k;
+  p.side[1] = c->v;
+  p.signs = c->d_signs;
+  p.signs_stride = c->signs_stride;
+  p.St = c->d_St;
+  p.err = c->d_status;
+  return launch_quantize_slots(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+kvq_status kvq_chunk_workspace_bytes(const kvq_cache* c, kvq_dtype dtype, int32_t n_tokens, size_t* bytes) {
+  if (!c || !bytes || n_tokens < 0) return KVQ_ERR_INVALID_ARG;
+  if (dtype != KVQ_F32 && dtype != KVQ_BF16) return KVQ_ERR_INVALID_ARG;
+  if (!ragged_supported(c)) return KVQ_ERR_UNSUPPORTED;
+  if ((long)n_tokens * c->cfg.n_q_heads > (1l << 30)) return KVQ_ERR_INVALID_ARG;
+  *bytes = chunk_layout_of(c, n_tokens).total;
+  return KVQ_OK;
+}
+
+kvq_status kvq_chunk_attention(const kvq_cache* c, const void* q, kvq_dtype dtype, int32_t n_tokens,
+                               const int32_t* seq_start, const int32_t* ctx_lens, void* out, void* workspace,
+                               size_t ws_bytes, void* stream) {
+  if (!c || n_tokens < 0) return KVQ_ERR_INVALID_ARG;
+  if (dtype != KVQ_F32 && dtype != KVQ_BF16) return KVQ_ERR_INVALID_ARG;
+  if (!ragged_supported(c)) return KVQ_ERR_UNSUPPORTED;
+  if (n_tokens == 0) return KVQ_OK;
+  if (!q || !seq_start || !out || !workspace) return KVQ_ERR_INVALID_ARG;
+  if ((long)n_tokens * c->cfg.n_q_heads > (1l << 30)) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return KVQ_ERR_ALIGNMENT;
+  if (!aligned_to(seq_start, 4) || !aligned_to(ctx_lens, 4)) return KVQ_ERR_ALIGNMENT;
+  if (!on_cache_device(c)) return KVQ_ERR_INVALID_ARG;
+  const ChunkLayout L = chunk_layout_of(c, n_tokens);
+  if (ws_bytes < L.total) return KVQ_ERR_WORKSPACE;
+  ChunkParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.q = q;
+  p.out = out;
+  p.bf16 = dtype == KVQ_BF16;
+  p.n_tokens = n_tokens;
+  p.B = c->batch;
+  p.Hq = c->cfg.n_q_heads;
+  p.Hkv = c->cfg.n_kv_heads;
+  p.group = p.Hq / p.Hkv;
+  p.seq_start = seq_start;
+  p.ctx_lens = ctx_lens ? ctx_lens : c->d_lens;
+  p.capacity = c->capacity;
+  p.kreg = c->d_k;
+  p.vreg = c->d_v;
+  p.tiles_per_seq = c->tiles_per_seq;
+  p.table = c->table;
+  p.pages_per_seq = c->pages_per_seq;
+  p.n_pages = c->n_pages;
+  p.k = c->k;
+  p.v = c->v;
+  p.signs = c->d_signs;
+  p.signs_stride = c->signs_stride;
+  p.S = c->d_S;
+  p.St = c->d_St;
+  p.logit_scale = default_scale(c->cfg) * 1.4426950408889634f;
+  p.err = c->d_status;
+  char* w = static_cast<char*>(workspace);
+  p.rows = L.rows;
+  p.max_tiles = L.max_tiles;
+  p.ctas = L.ctas;
+  p.unit_start = reinterpret_cast<long long*>(w + L.unit_start);
+  p.tile_seq = reinterpret_cast<int*>(w + L.tile_seq);
+  p.tile_start = reinterpret_cast<int*>(w + L.tile_start);
+  p.head = reinterpret_cast<long long*>(w + L.head);
+  p.qprep = w + L.qprep;
+  p.part = reinterpret_cast<float*>(w + L.part);
+  return launch_chunk_attention(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,513 @@
+// Attention of a ragged batch of new tokens over the packed LM / LM_QJL / SIGN1 cache: host plan, query
+// prep, the fp32 segment kernel, and the merge. ("TurboQuant vs OSCAR vs EpiCache", section
+// "Quantization frontiers: TurboQuant and OSCAR": rotation, Lloyd-Max codes, QJL sketch; kernels
+// compatible with paged attention.)
+//
+// With R = H D / sqrt(d), a key k_t is held as n_t / sqrt(d) R^T (c[code] + kappa gamma_t S^T z_t), kappa =
+// sqrt(pi/2) / m. Rotating and sketching the query once (q~ = R q, s = kappa S q~) leaves
+//   logit_t = scale n_t / sqrt(d) (<q~, c[code_t]> + gamma_t <s, z_t>),
+// and the value sum is rotated back once per row:
+//   out = D H / d (sum_t w_t c[code_t] + kappa S^T sum_t w_t gamma_t z_t) / sum_t p_t,  w_t = p_t n_t.
+// Three launches: prep (plan and queries), segments (kvq_chunk.cuh), merge.
+#include <algorithm>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "kvq_chunk.cuh"
+#include "kvq_internal.h"
+#include "kvq_lm_common.cuh"
+#include "kvq_quantize_lm.cuh"
+
+namespace kvq {
+namespace {
+
+using namespace chunk;
+
+constexpr int kPrepThreads = 256;
+constexpr int kPrepRows = 32;     // query rows of a prep block: 4 per warp
+constexpr float kKappa = lmc::kSqrtHalfPi / kHeadDim;
+
+// Walsh-Hadamard transform of 128 coordinates, lane l holding 32 k + l (k < 4), unnormalised.
+__device__ __forceinline__ void fwht(float (&u)[4], int lane) {
+#pragma unroll
+  for (int b = 0; b < 5; ++b) {
+    const bool upper = (lane >> b) & 1;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float other = __shfl_xor_sync(0xffffffffu, u[k], 1 << b);
+      u[k] = upper ? other - u[k] : u[k] + other;
+    }
+  }
+  const float a0 = u[0] + u[1], a1 = u[0] - u[1], a2 = u[2] + u[3], a3 = u[2] - u[3];
+  u[0] = a0 + a2; u[2] = a0 - a2; u[1] = a1 + a3; u[3] = a1 - a3;
+}
+
+// One block's plan of the call: row tiles per request, their units, prefix sums of both.
+__device__ void plan(const ChunkParams& p) {
+  __shared__ long long s_warp[kPrepThreads / 32];
+  __shared__ long long s_run;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = p.rows / p.group;
+  auto scan = [&](long long v) {  // exclusive prefix of v over the block, carried in s_run
+    long long x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();
+    long long before = s_run;
+    for (int w = 0; w < warp; ++w) before += s_warp[w];
+    __syncthreads();
+    if (tid == kPrepThreads - 1) s_run = before + x;
+    __syncthreads();
+    return before + x - v;
+  };
+  if (tid == 0) s_run = 0;
+  __syncthreads();
+  for (int b0 = 0; b0 < p.B; b0 += kPrepThreads) {
+    const int b = b0 + tid;
+    int n = 0;
+    if (b < p.B) n = max(clamp_start(p, b + 1) - clamp_start(p, b), 0);
+    const long long at = scan((n + per - 1) / per);
+    // max_tiles holds every tile of a seq_start that does not decrease; another one is cut there
+    if (b < p.B) p.tile_start[b] = (int)min(at, (long long)p.max_tiles);
+  }
+  const int tiles = (int)min(s_run, (long long)p.max_tiles);
+  __syncthreads();
+  if (tid == 0) {
+    p.tile_start[p.B] = tiles;
+    s_run = 0;
+  }
+  __syncthreads();
+  for (int t0 = 0; t0 < tiles; t0 += kPrepThreads) {
+    const int t = t0 + tid;
+    long long units = 0;
+    if (t < tiles) {
+      int lo = 0, hi = p.B;  // the last request with tile_start <= t
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.tile_start[mid] <= t) lo = mid;
+        else hi = mid;
+      }
+      p.tile_seq[t] = lo;
+      const Rows r = tile_rows(p, lo, t - p.tile_start[lo]);
+      units = max(1, (r.limit + kPage - 1) / kPage);
+    }
+    const long long at = scan(units);
+    if (t < tiles) p.unit_start[t] = at;
+  }
+  if (tid == 0) {
+    p.unit_start[tiles] = s_run;
+    p.head[0] = tiles;
+    p.head[1] = s_run;
+  }
+}
+
+// Block 0 plans; the others rotate (and sketch) kPrepRows query rows each: fp32 [d (+ m)], the logit scale
+// and 1/sqrt(d) of the keys folded in.
+template <bool KQ>
+__global__ void __launch_bounds__(kPrepThreads) chunk_prep(const __grid_constant__ ChunkParams p) {
+  if (blockIdx.x == 0) {
+    plan(p);
+    return;
+  }
+  __shared__ float s_q[kPrepRows][kHeadDim];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const long long rows = (long long)p.n_tokens * p.Hq;
+  const long long row0 = (long long)(blockIdx.x - 1) * kPrepRows + 4 * warp;
+  constexpr int DK = KQ ? 2 * kHeadDim : kHeadDim;
+  float rot[4][4], sk[4][4];
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const long long row = row0 + v;
+    if (row < rows) {
+      const float* sg = p.signs + (int)(row % p.Hq) / p.group * p.signs_stride;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        rot[v][k] = qlm::load_elem(p.q, (size_t)row * kHeadDim + 32 * k + lane, p.bf16) * sg[32 * k + lane];
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) rot[v][k] = 0.f;
+    }
+    fwht(rot[v], lane);
+    // R q * scale / sqrt(d) = H D q * scale / d
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      rot[v][k] *= p.logit_scale * (1.f / kHeadDim);
+      if (KQ) s_q[4 * warp + v][32 * k + lane] = rot[v][k];
+      sk[v][k] = 0.f;
+    }
+  }
+  if (KQ) {  // kappa S q~, row j = 32 r + lane, from S^T [i][j]
+    __syncwarp();
+#pragma unroll 4
+    for (int i = 0; i < kHeadDim; ++i) {
+      float st[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) st[r] = __ldg(p.St + i * kHeadDim + 32 * r + lane);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const float x = s_q[4 * warp + v][i];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sk[v][r] = fmaf(st[r], x, sk[v][r]);
+      }
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const long long row = row0 + v;
+    if (row >= rows) break;
+    float* dst = static_cast<float*>(p.qprep) + (size_t)row * DK;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      dst[32 * k + lane] = rot[v][k];
+      if (KQ) dst[kHeadDim + 32 * k + lane] = sk[v][k] * kKappa;
+    }
+  }
+}
+
+// ---- fp32 segment kernel ------------------------------------------------------------------------------
+//
+// 64 rows x 64 tokens a step, 256 threads: thread (ty, tx) holds rows 4 ty .. + 3; of the logits tokens
+// 4 tx .. + 3, of the value sum dims 4 tx + 64 c .. + 3. Queries, the dequantised key (then value) page and
+// the weights lie k-major in shared memory, so every product step is two 16-byte loads (plus one per 64
+// value dims) for 16 (16 per 64 dims) FMAs. fp32 throughout.
+constexpr int kF32Rows = 64;
+
+__device__ __forceinline__ uint32_t plane_nibble(const unsigned char* plane, int order, int tok, int quad) {
+  // bits of token `tok` (of 32), coordinates 4 quad .. 4 quad + 3
+  if (order == kOrderOctet) {
+    const int t = quad & 3, h = (quad >> 2) & 1, m = quad >> 3;
+    const uint32_t w = reinterpret_cast<const uint32_t*>(plane)[(tok >> 3) * 32 + 8 * t + 2 * m + h] >> (tok & 7);
+    return (w & 1u) | ((w >> 7) & 2u) | ((w >> 14) & 4u) | ((w >> 21) & 8u);
+  }
+  const unsigned char byte = order == kOrderToken ? plane[tok * 16 + (quad >> 1)] : plane[(quad >> 1) * kTile + tok];
+  return (byte >> (4 * (quad & 1))) & 0xFu;
+}
+
+// Page `page` of one side as fp32, k-major dst: keys [dim][token], values [token][dim]. Sketch entries are
+// +-gamma; tokens at or behind `tokens` give zeros. scale[token] = norm.
+template <bool VALUES, bool QJL>
+__device__ __forceinline__ void dequant_f32(const ChunkParams& p, const SideLayout& L, const char* region, const Walk& w,
+                                            int page, int tokens, float* dst, float* scale) {
+  const int tid = threadIdx.x;
+  const int tok = tid & 63, part = tid >> 6;
+  const long ti = tile_index_read(p.table, p.pages_per_seq, p.n_pages, p.tiles_per_seq, p.Hkv, w.rows.b, w.hk, 2 * page, p.err);
+  const unsigned char* tb = reinterpret_cast<const unsigned char*>(region) + (size_t)(ti + (tok >> 5)) * L.tile_bytes;
+  const int slot = tok & 31;
+  constexpr int DIMS = QJL ? 2 * kHeadDim : kHeadDim;
+  const bool in = tok < tokens;
+  float gamma = 0.f;
+  if (QJL && in) gamma = __half2float(reinterpret_cast<const __half*>(tb + L.off_gamma)[slot]);
+  // a residual norm that is not finite (a coded infinity or NaN) makes NaN of the rows that attend to the
+  // token, through its scale, and must not reach the rows whose weight is 0 as 0 * NaN
+  const bool bad = VALUES && QJL && !isfinite(gamma);
+  if (bad) gamma = 0.f;
+  if (part == 0)
+    scale[tok] = bad ? NAN : in ? __half2float(reinterpret_cast<const __half*>(tb + L.off_norm)[slot]) : 0.f;
+  for (int quad = part; quad < DIMS / 4; quad += 4) {
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    if (in) {
+      if (quad < kHeadDim / 4) {
+        uint32_t bits[kMaxBits];
+#pragma unroll
+        for (int pp = 0; pp < kMaxBits; ++pp)
+          bits[pp] = pp < L.bits ? plane_nibble(tb + L.off_planes + pp * (kTile * 16), L.order, slot, quad) : 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          x[i] = L.cent[((bits[0] >> i) & 1u) | (((bits[1] >> i) & 1u) << 1) | (((bits[2] >> i) & 1u) << 2)];
+      } else {
+        const uint32_t z = plane_nibble(tb + L.off_sketch, L.order, slot, quad - kHeadDim / 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = (z >> i) & 1u ? gamma : -gamma;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dst[VALUES ? tok * DIMS + 4 * quad + i : (4 * quad + i) * 64 + tok] = x[i];
+  }
+}
+
+template <bool KQ, bool VQ>
+struct F32Smem {
+  static constexpr int DK = KQ ? 2 * kHeadDim : kHeadDim, DV = VQ ? 2 * kHeadDim : kHeadDim;
+  float q[DK][kF32Rows];
+  float kv[(DK > DV ? DK : DV) * 64];
+  float w[64][kF32Rows];
+  float kn[64], vn[64];
+};
+
+template <bool KQ, bool VQ>
+__global__ void __launch_bounds__(256) chunk_f32(const __grid_constant__ ChunkParams p) {
+  using Smem = F32Smem<KQ, VQ>;
+  constexpr int DK = Smem::DK, DV = Smem::DV, C = DV / 64;
+  extern __shared__ __align__(16) unsigned char smem[];
+  Smem& sm = *reinterpret_cast<Smem*>(smem);
+  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  Walk w;
+  w.init(p, blockIdx.x);
+  while (w.next(p)) {
+    const Rows r = w.rows;
+    const size_t qrow0 = (size_t)(r.start + r.first) * p.Hq + w.hk * p.group;
+    __syncthreads();
+    for (int i = tid; i < kF32Rows * DK; i += 256) {
+      const int row = i / DK, k = i % DK;
+      float v = 0.f;
+      if (row < r.count)
+        v = static_cast<const float*>(p.qprep)[(qrow0 + (size_t)(row / p.group) * p.Hq + row % p.group) * DK + k];
+      sm.q[k][row] = v;
+    }
+    float m[4], l[4], o[4][C][4];
+    int last[4];  // last position row i attends to
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+      const int row = 4 * ty + i;
+      last[i] = row < r.count ? min(r.pos0 + row / p.group, r.ctx - 1) : -1;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][c][j] = 0.f;
+    }
+    for (int k = w.k0; k < w.k1; ++k) {
+      const int tokens = min(kPage, r.limit - k * kPage);
+      if (tokens <= 0) break;  // a tile with no position at all
+      __syncthreads();
+      dequant_f32<false, KQ>(p, p.k, p.kreg, w, k, tokens, sm.kv, sm.kn);
+      __syncthreads();
+      float s[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 8
+      for (int d = 0; d < DK; ++d) {
+        const float4 a = *reinterpret_cast<const float4*>(&sm.q[d][4 * ty]);
+        const float4 b = *reinterpret_cast<const float4*>(&sm.kv[d * 64 + 4 * tx]);
+        const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[i][j] = fmaf(av[i], bv[j], s[i][j]);
+      }
+      float alpha[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int t = k * kPage + 4 * tx + j;
+          s[i][j] = t <= last[i] ? s[i][j] * sm.kn[4 * tx + j] : -INFINITY;
+          mx = fmaxf(mx, s[i][j]);
+        }
+#pragma unroll
+        for (int x = 8; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+        const float mn = fmaxf(m[i], mx), ref = mn == -INFINITY ? 0.f : mn;
+        alpha[i] = exp2f(m[i] - ref);
+        m[i] = mn;
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[i][j] = exp2f(s[i][j] - ref);
+          sum += s[i][j];
+        }
+#pragma unroll
+        for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        l[i] = fmaf(l[i], alpha[i], sum);
+      }
+      __syncthreads();  // every read of the key page is done
+      dequant_f32<true, VQ>(p, p.v, p.vreg, w, k, tokens, sm.kv, sm.vn);
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int t = k * kPage + 4 * tx + j;
+        const float n = sm.vn[4 * tx + j];
+        float4 wv;  // a masked weight is 0 whatever the token's norm
+        wv.x = t <= last[0] ? s[0][j] * n : 0.f;
+        wv.y = t <= last[1] ? s[1][j] * n : 0.f;
+        wv.z = t <= last[2] ? s[2][j] * n : 0.f;
+        wv.w = t <= last[3] ? s[3][j] * n : 0.f;
+        *reinterpret_cast<float4*>(&sm.w[4 * tx + j][4 * ty]) = wv;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[i][c][j] *= alpha[i];
+#pragma unroll 4
+      for (int t = 0; t < kPage; ++t) {
+        const float4 a = *reinterpret_cast<const float4*>(&sm.w[t][4 * ty]);
+        const float av[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          const float4 b = *reinterpret_cast<const float4*>(&sm.kv[t * DV + 64 * c + 4 * tx]);
+          const float bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[i][c][j] = fmaf(av[i], bv[j], o[i][c][j]);
+        }
+      }
+    }
+    float* st = segment_state(p, w.item, blockIdx.x, DV);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 4 * ty + i;
+      if (tx == 0) {
+        st[row] = m[i];
+        st[kF32Rows + row] = l[i];
+      }
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) st[(2 + 64 * c + 4 * tx + j) * kF32Rows + row] = o[i][c][j];
+    }
+  }
+}
+
+// ---- merge --------------------------------------------------------------------------------------------
+//
+// A block merges 32 rows of one item (kv-head, row tile): a warp 4 rows, lane l dims 32 k + l.
+constexpr int kMergeThreads = 256, kMergeRows = 32;
+
+template <bool VQ>
+__global__ void __launch_bounds__(kMergeThreads) chunk_merge(const __grid_constant__ ChunkParams p) {
+  constexpr int DV = VQ ? 2 * kHeadDim : kHeadDim;
+  __shared__ float s_z[VQ ? kMergeRows : 1][kHeadDim];
+  const int tiles = (int)p.head[0];
+  const int per = p.rows / kMergeRows;
+  const long long items = (long long)tiles * p.Hkv;
+  const long long item = blockIdx.x / per;
+  if (item >= items) return;
+  const int hk = (int)(item / tiles), tile = (int)(item % tiles);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row0 = (int)(blockIdx.x % per) * kMergeRows + 4 * warp;
+  const int b = p.tile_seq[tile];
+  const Rows r = tile_rows(p, b, tile - p.tile_start[b]);
+  const long long units = p.head[1], T = units * p.Hkv, G = cta_count(p, T);
+  const int c0 = cta_of(hk * units + p.unit_start[tile], T, G);
+  const int c1 = cta_of(hk * units + p.unit_start[tile + 1] - 1, T, G);
+  float acc[4][4], accz[4][4], l[4];
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    l[v] = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[v][k] = accz[v][k] = 0.f;
+    const int row = row0 + v;
+    if (row >= r.count) continue;
+    float m = -INFINITY, sum = 0.f;
+    for (int c = c0; c <= c1; ++c) {
+      const float* st = segment_state(p, item, c, DV);
+      m = fmaxf(m, st[row]);
+      sum += st[p.rows + row];
+    }
+    if (m == -INFINITY || sum != sum) {  // nothing attended, or a logit that is NaN (the maximum passes over it)
+      l[v] = sum;
+      continue;
+    }
+    for (int c = c0; c <= c1; ++c) {
+      const float* st = segment_state(p, item, c, DV);
+      const float f = exp2f(st[row] - m);
+      if (f == 0.f) continue;
+      l[v] = fmaf(f, st[p.rows + row], l[v]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        acc[v][k] = fmaf(f, st[(size_t)(2 + 32 * k + lane) * p.rows + row], acc[v][k]);
+        if (VQ) accz[v][k] = fmaf(f, st[(size_t)(2 + kHeadDim + 32 * k + lane) * p.rows + row], accz[v][k]);
+      }
+    }
+  }
+  if (VQ) {  // acc += kappa S^T accz
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s_z[VQ ? 4 * warp + v : 0][32 * k + lane] = accz[v][k] * kKappa;
+    __syncwarp();
+#pragma unroll 4
+    for (int j = 0; j < kHeadDim; ++j) {
+      float sj[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sj[k] = __ldg(p.S + j * kHeadDim + 32 * k + lane);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const float x = s_z[VQ ? 4 * warp + v : 0][j];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[v][k] = fmaf(sj[k], x, acc[v][k]);
+      }
+    }
+  }
+  const float* sg = p.signs + hk * p.signs_stride;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    fwht(acc[v], lane);
+    const int row = row0 + v;
+    if (row >= r.count) continue;
+    const float f = l[v] > 0.f ? 1.f / (kHeadDim * l[v]) : (l[v] == 0.f ? 0.f : l[v]);
+    const size_t at = ((size_t)(r.start + r.first + row / p.group) * p.Hq + hk * p.group + row % p.group) * kHeadDim;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float x = acc[v][k] * f * sg[32 * k + lane];
+      if (p.bf16) static_cast<__nv_bfloat16*>(p.out)[at + 32 * k + lane] = __float2bfloat16_rn(x);
+      else static_cast<float*>(p.out)[at + 32 * k + lane] = x;
+    }
+  }
+}
+
+template <bool KQ, bool VQ>
+cudaError_t launch_f32(const ChunkParams& p, cudaStream_t s) {
+  constexpr int smem = (int)sizeof(F32Smem<KQ, VQ>);
+  const cudaError_t e = cudaFuncSetAttribute(chunk_f32<KQ, VQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  chunk_f32<KQ, VQ><<<p.ctas, 256, smem, s>>>(p);
+  return launched();
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+
+ChunkLayout chunk_layout(int n_tokens, int batch, int Hq, int Hkv, bool k_qjl, bool v_qjl, int sms) {
+  ChunkLayout L;
+  L.rows = kF32Rows;
+  const int per = L.rows / (Hq / Hkv);
+  L.max_tiles = n_tokens / per + std::min(batch, n_tokens) + 1;
+  L.ctas = sms;
+  const size_t rows = (size_t)n_tokens * Hq, segments = (size_t)L.max_tiles * Hkv + L.ctas;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = up256(off + bytes);
+    return at;
+  };
+  L.head = take(2 * sizeof(long long));
+  L.unit_start = take(sizeof(long long) * ((size_t)L.max_tiles + 1));
+  L.tile_seq = take(sizeof(int) * (size_t)L.max_tiles);
+  L.tile_start = take(sizeof(int) * ((size_t)batch + 1));
+  L.qprep = take(rows * kHeadDim * (k_qjl ? 2 : 1) * sizeof(float));
+  L.part = take(sizeof(float) * segments * L.rows * (2 + kHeadDim * (v_qjl ? 2 : 1)));
+  L.total = off;
+  return L;
+}
+
+cudaError_t launch_chunk_attention(const ChunkParams& p, cudaStream_t s) {
+  const long long rows = (long long)p.n_tokens * p.Hq;
+  const unsigned prep = 1 + (unsigned)((rows + kPrepRows - 1) / kPrepRows);
+  if (p.k.qjl) chunk_prep<true><<<prep, kPrepThreads, 0, s>>>(p);
+  else chunk_prep<false><<<prep, kPrepThreads, 0, s>>>(p);
+  cudaError_t e = launched();
+  if (e != cudaSuccess) return e;
+  if (p.k.qjl) e = p.v.qjl ? launch_f32<true, true>(p, s) : launch_f32<true, false>(p, s);
+  else e = p.v.qjl ? launch_f32<false, true>(p, s) : launch_f32<false, false>(p, s);
+  if (e != cudaSuccess) return e;
+  const unsigned merge = (unsigned)((size_t)p.max_tiles * p.Hkv * (p.rows / kMergeRows));
+  if (p.v.qjl) chunk_merge<true><<<merge, kMergeThreads, 0, s>>>(p);
+  else chunk_merge<false><<<merge, kMergeThreads, 0, s>>>(p);
+  return launched();
+}
+
+}  // namespace kvq

@@ -1,0 +1,113 @@
+// Pieces shared by the chunk attention kernels: the work plan over ragged requests and the states its
+// segments leave behind.
+//
+// Rows. A kv-head of request b has n_b * group query rows, row r = token r / group, head r % group. Row
+// tiles of `rows` rows never cross a request; tile t of a kv-head belongs to request tile_seq[t], the
+// tiles of request b being tile_start[b] .. tile_start[b + 1] - 1.
+//
+// Units. Tile t attends to the positions below its limit, the last row's position + 1, in units of one
+// 64-token page; unit_start[t] is the prefix sum of max(1, ceil(limit / 64)). The units of all kv-heads
+// lie end to end (kv-head h's from h * head[1]), and CTA c of G = min(CTAs, T) takes the units floor(c T / G)
+// .. floor((c + 1) T / G) - 1 of the T: an even split whatever the lengths, without a host that knows them.
+// A CTA's run of units in one tile is a segment; segment number = item + CTA (item = h * tiles + t) is
+// distinct, since every step from one segment to the next raises the item or the CTA. A segment writes
+// its softmax state, column-major: m [rows], l [rows], o [value dims][rows]; one kernel then merges the
+// segments of every row, folds the value sketch and rotates back.
+#pragma once
+
+#include "kvq_internal.h"
+#include "kvq_tiles.cuh"
+
+namespace kvq {
+namespace chunk {
+
+constexpr int kPage = kTile * kTilePair;  // tokens of a unit
+
+struct Rows {        // one row tile
+  int b;             // request
+  int first;         // its first row's token within the request
+  int count;         // rows in use
+  int start;         // request's first token in the ragged batch
+  int pos0;          // position of the tile's first token (may be negative)
+  int ctx;           // tokens the request's cache holds
+  int limit;         // positions below this are attended by some row
+};
+
+__device__ __forceinline__ int clamp_start(const ChunkParams& p, int b) { return min(max(p.seq_start[b], 0), p.n_tokens); }
+
+__device__ __forceinline__ Rows tile_rows(const ChunkParams& p, int b, int tile) {
+  Rows r;
+  r.b = b;
+  r.start = clamp_start(p, b);
+  const int n = max(clamp_start(p, b + 1) - r.start, 0);
+  const int per = p.rows / p.group;  // tokens of a row tile
+  r.first = tile * per;
+  const int tokens = min(per, n - r.first);
+  r.count = tokens * p.group;
+  r.ctx = min(max(p.ctx_lens[b], 0), p.capacity);
+  r.pos0 = r.ctx - n + r.first;
+  r.limit = max(0, r.pos0 + tokens);
+  return r;
+}
+
+// CTAs that share T units (each has one at least), and the CTA that owns unit u: the largest c with
+// floor(c T / G) <= u.
+__device__ __forceinline__ long long cta_count(const ChunkParams& p, long long T) { return min((long long)p.ctas, T); }
+__device__ __forceinline__ long long cta_first(long long c, long long T, long long G) { return c * T / G; }
+__device__ __forceinline__ int cta_of(long long u, long long T, long long G) { return (int)(((u + 1) * G - 1) / T); }
+
+// Walks the segments of one CTA. Every thread (or one per warp) keeps its own copy.
+struct Walk {
+  long long u, end, units;  // next unit, end of the CTA's range, units of a kv-head
+  int tiles, tile, hk;
+  // current segment
+  long long item;
+  int k0, k1;      // its units within the tile: pages k0 .. k1 - 1
+  int whole;       // the segment is the whole tile
+  Rows rows;
+
+  __device__ __forceinline__ void init(const ChunkParams& p, int cta) {
+    tiles = (int)p.head[0];
+    units = p.head[1];
+    const long long T = units * p.Hkv;
+    const long long G = cta_count(p, T);
+    u = cta < G ? cta_first(cta, T, G) : 0;
+    end = cta < G ? cta_first(cta + 1, T, G) : 0;
+    hk = units > 0 ? (int)(u / units) : 0;
+    const long long r = u - hk * units;
+    int lo = 0, hi = tiles;  // the last tile with unit_start <= r
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p.unit_start[mid] <= r) lo = mid;
+      else hi = mid;
+    }
+    tile = lo;
+  }
+  __device__ __forceinline__ bool next(const ChunkParams& p) {
+    if (u >= end) return false;
+    if (tile == tiles) {
+      tile = 0;
+      ++hk;
+    }
+    const long long base = hk * units;
+    const long long t0 = base + p.unit_start[tile], t1 = base + p.unit_start[tile + 1];
+    const long long stop = min(t1, end);
+    k0 = (int)(u - t0);
+    k1 = (int)(stop - t0);
+    whole = u == t0 && stop == t1;
+    item = (long long)hk * tiles + tile;
+    const int b = p.tile_seq[tile];
+    rows = tile_rows(p, b, tile - p.tile_start[b]);
+    u = stop;
+    if (stop == t1) ++tile;
+    return true;
+  }
+};
+
+__device__ __forceinline__ float* segment_state(const ChunkParams& p, long long item, int cta, int dv) {
+  return p.part + (size_t)(item + cta) * p.rows * (2 + dv);
+}
+
+}  // namespace chunk
+
+}  // namespace kvq

@@ -1,0 +1,412 @@
+// The ragged serving path's bookkeeping and append: block tables and slot maps from request lengths,
+// and an append of a token-major batch into page slots ("TurboQuant vs OSCAR vs EpiCache", OSCAR:
+// fused kernels compatible with paged attention and the prefix cache).
+//
+// extend_block_table. Request b holds held_b tokens and takes new_b more. Its pages grow from
+// ceil(held_b / 64) to ceil((held_b + new_b) / 64); the new ones come from the free list in request
+// order, at the exclusive prefix sum of the counts. Bound by launch latency: the largest calls move a
+// few hundred KB. So one kernel and no exchange between blocks: every block sums the counts of all
+// requests before its own (batch / 1024 coalesced rounds), then writes its own requests' entries.
+//
+// slot_map. Token t of the ragged batch belongs to the request b with seq_start[b] <= t <
+// seq_start[b + 1] (binary search), has position held_b + t - seq_start[b], and goes to slot
+// 64 * table[b][position / 64] + position % 64. One thread per token; bound by the 16 bytes it writes.
+//
+// quantize_slots. The codec's steps 1-7 (kvq_quantize.cu) on vectors [token][kv-head][128], written to
+// slots[token]. A block codes TOK tokens of one (kv-head, side): warps code a token each, the sketch of
+// all TOK residuals is one product with S^T staged in shared memory (as in kvq_quantize_tile.cuh), and
+// the bits go out per run of slots in one octet: a whole octet of a key plane is stored, a part of one
+// is merged with atomics, since other tokens of the octet may belong to another block. The sketch
+// product on the CUDA cores bounds it (128 x 128 FMAs a vector), so small calls take TOK = 8, which
+// spreads them over four times as many blocks as TOK = 32, and large calls 32, which reads S^T a
+// quarter as often.
+#include <algorithm>
+
+#include <cuda_fp16.h>
+
+#include "kvq_async.cuh"
+#include "kvq_internal.h"
+#include "kvq_quantize_lm.cuh"
+#include "kvq_tiles.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr int kPage = kTile * kTilePair;
+constexpr int kTableThreads = 256;
+
+// Inclusive sum over the block of one value per thread (kTableThreads threads), and the block's total.
+__device__ __forceinline__ long long block_scan(long long v, long long* total) {
+  __shared__ long long s_warp[kTableThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  __syncthreads();  // the previous round's reads of s_warp are done
+  if (lane == 31) s_warp[warp] = v;
+  __syncthreads();
+  long long before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kTableThreads / 32; ++w) {
+    const long long u = s_warp[w];
+    before += w < warp ? u : 0;
+    all += u;
+  }
+  *total = all;
+  return v + before;
+}
+
+// Pages a request holds and needs; valid: its lengths fit the table.
+struct Request {
+  int held, n_new, p0, need;
+  bool valid;
+};
+__device__ __forceinline__ Request request(const int* held, const int* n_new, int b, int pages_per_seq) {
+  Request r;
+  r.held = held[b];
+  r.n_new = n_new[b];
+  r.valid = r.held >= 0 && r.n_new >= 0 && (long long)r.held + r.n_new <= (long long)pages_per_seq * kPage;
+  r.p0 = r.valid ? (int)(((long long)r.held + kPage - 1) / kPage) : 0;
+  r.need = r.valid ? (int)(((long long)r.held + r.n_new + kPage - 1) / kPage) - r.p0 : 0;
+  return r;
+}
+
+// Grid: one block per kTableThreads requests.
+__global__ void __launch_bounds__(kTableThreads)
+extend_block_table(const int* __restrict__ held, const int* __restrict__ n_new, int batch, const int* __restrict__ free_pages,
+                   int n_free, const int* __restrict__ cursor, int* __restrict__ table, int pages_per_seq,
+                   int* __restrict__ seq_start, int* __restrict__ ctx_lens, int* __restrict__ taken) {
+  __shared__ int s_first[kTableThreads], s_need[kTableThreads], s_p0[kTableThreads];
+  __shared__ int s_sum[2];
+  const int tid = threadIdx.x;
+  const int begin = blockIdx.x * kTableThreads;
+  const int first = cursor ? *cursor : 0;
+  const long long room = first >= 0 && first <= n_free ? n_free - first : -1;  // -1: no page can be given
+  long long pages = 0, tokens = 0;  // of the requests before this block's
+  for (int b0 = 0; b0 < begin; b0 += kTableThreads) {
+    const Request r = request(held, n_new, b0 + tid, pages_per_seq);
+    pages += r.need;
+    tokens += max(r.n_new, 0);
+  }
+  long long all_pages, all_tokens, own_pages, own_tokens;
+  block_scan(pages, &all_pages);
+  block_scan(tokens, &all_tokens);
+  const int b = begin + tid;
+  Request r{0, 0, 0, 0, true};
+  if (b < batch) r = request(held, n_new, b, pages_per_seq);
+  const long long end = all_pages + block_scan(r.need, &own_pages);
+  const long long tend = all_tokens + block_scan(max(r.n_new, 0), &own_tokens);
+  const bool granted = r.valid && (r.need == 0 || end <= room);
+  if (tid < 2) s_sum[tid] = 0;
+  s_first[tid] = (int)min(end - r.need, 0x7fffffffll);
+  s_need[tid] = granted ? r.need : 0;
+  s_p0[tid] = r.p0;
+  __syncthreads();
+  if (b < batch) {
+    if (b == 0) seq_start[0] = 0;
+    seq_start[b + 1] = (int)min(tend, 0x7fffffffll);
+    ctx_lens[b] = granted ? r.held + r.n_new : (int)min(max((long long)r.held, 0ll), (long long)pages_per_seq * kPage);
+  }
+  // entries: one warp per request
+  for (int i = tid >> 5; i < min(kTableThreads, batch - begin); i += kTableThreads / 32) {
+    const int n = s_need[i];
+    int* row = table + (long long)(begin + i) * pages_per_seq + s_p0[i];
+    for (int k = tid & 31; k < n; k += 32) row[k] = free_pages[first + s_first[i] + k];
+  }
+  // totals: the last block sees every request once more
+  if (blockIdx.x == gridDim.x - 1) {
+    long long run = 0;
+    int got = 0, refused = 0;
+    for (int b0 = 0; b0 < batch; b0 += kTableThreads) {
+      Request q{0, 0, 0, 0, true};
+      if (b0 + tid < batch) q = request(held, n_new, b0 + tid, pages_per_seq);
+      long long part;
+      const long long e = run + block_scan(q.need, &part);
+      run += part;
+      const bool ok = q.valid && (q.need == 0 || e <= room);
+      got += ok ? q.need : 0;
+      refused += ok ? 0 : 1;
+    }
+    atomicAdd(&s_sum[0], got);
+    atomicAdd(&s_sum[1], refused);
+    __syncthreads();
+    if (tid < 2) taken[tid] = s_sum[tid];
+  }
+}
+
+constexpr int kSlotThreads = 256;
+
+__global__ void __launch_bounds__(kSlotThreads)
+slot_map(const int* __restrict__ held, const int* __restrict__ seq_start, const int* __restrict__ ctx_lens, int batch,
+         const int* __restrict__ table, int pages_per_seq, int n_pages, int n_tokens, int* __restrict__ seq_ids,
+         int* __restrict__ positions, long long* __restrict__ slots) {
+  const int t = blockIdx.x * kSlotThreads + threadIdx.x;
+  if (t >= n_tokens || t >= seq_start[batch]) return;  // rows behind the last request stay as they are
+  int lo = 0, hi = batch;  // the last b with seq_start[b] <= t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (seq_start[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  const int start = seq_start[lo], n = seq_start[lo + 1] - start;
+  const long long pos = (long long)held[lo] + (t - start);
+  long long slot = -1;
+  if (pos >= 0 && pos < (long long)pages_per_seq * kPage && (long long)held[lo] + n == ctx_lens[lo]) {
+    const int page = table[(long long)lo * pages_per_seq + pos / kPage];
+    if (page >= 0 && page < n_pages) slot = (long long)page * kPage + pos % kPage;
+  }
+  if (seq_ids) seq_ids[t] = lo;
+  if (positions) positions[t] = (int)pos;
+  slots[t] = slot;
+}
+
+__global__ void set_lengths(const __grid_constant__ LengthParams p) {
+  const int i = threadIdx.x;
+  if (i < p.n) p.lens[p.first + i] = p.value[i];
+}
+
+// ---- append by slots --------------------------------------------------------------------------------
+
+constexpr int kAppWarps = 8;
+constexpr int kAppThreads = kAppWarps * 32;
+
+template <int TOK>
+struct AppSmem {
+  float rho[TOK][kHeadDim];
+  uint32_t planes[TOK][kMaxBits + 1][4];  // code planes, then the sign words
+  float n[TOK], gamma[TOK];
+  long long slot[TOK];  // -1: not written
+};
+
+template <int TOK>
+__global__ void __launch_bounds__(kAppThreads) quantize_slots(const __grid_constant__ SlotQuantizeParams p) {
+  constexpr int R = TOK / 8;            // sketch rows per lane: 32 / TOK warps share the 128 rows of 4 tokens
+  constexpr int kShare = 32 / TOK;
+  extern __shared__ __align__(16) unsigned char smem[];
+  AppSmem<TOK>& sm = *reinterpret_cast<AppSmem<TOK>*>(smem);
+  float* st_s = reinterpret_cast<float*>(smem + (sizeof(AppSmem<TOK>) + 15) / 16 * 16);
+  const int side = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const SideLayout& L = p.side[side];
+  const int nthr = (1 << L.bits) - 1;
+  const int chunks = (p.n_tokens + TOK - 1) / TOK;
+  const long long total = (long long)chunks * p.heads;
+  if (blockIdx.x >= total) return;
+  if (L.qjl) {
+    for (int c = tid; c < kHeadDim * kHeadDim / 4; c += kAppThreads) cp_async16(st_s + 4 * c, p.St + 4 * c);
+    cp_async_commit();
+  }
+  float thr[7];
+#pragma unroll
+  for (int i = 0; i < 7; ++i) thr[i] = i < nthr ? L.thr[i] : INFINITY;
+  const float cent_lane = L.cent[(lane & 7) <= nthr ? (lane & 7) : 0];
+  bool st_ready = false;
+
+  for (long long g = blockIdx.x; g < total; g += gridDim.x) {
+    const int h = (int)(g % p.heads), first = (int)(g / p.heads) * TOK;
+    const int count = min(TOK, p.n_tokens - first);
+    float sgn[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sgn[q] = p.signs[h * p.signs_stride + 32 * q + lane];
+    for (int i = warp; i < TOK; i += kAppWarps) {
+      long long slot = i < count ? p.slots[first + i] : -1;
+      if (slot >= (long long)p.n_pages * kPage) {
+        if (lane == 0) atomicOr(p.err, kStatusBadPage);
+        slot = -1;
+      }
+      if (lane == 0) sm.slot[i] = slot < 0 ? -1 : slot;
+      float rho[4] = {0.f, 0.f, 0.f, 0.f};
+      if (slot >= 0) {
+        const size_t base = ((size_t)(first + i) * p.heads + h) * kHeadDim;
+        float u[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) u[q] = qlm::load_elem(p.src[side], base + 32 * q + lane, p.bf16);
+        const float n = sqrtf(qlm::warp_sum(u[0] * u[0] + u[1] * u[1] + u[2] * u[2] + u[3] * u[3]));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) u[q] *= sgn[q];
+#pragma unroll
+        for (int b = 0; b < 5; ++b) {  // Walsh-Hadamard butterflies over index bits 0..4
+          const bool upper = (lane >> b) & 1;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float other = __shfl_xor_sync(0xffffffffu, u[q], 1 << b);
+            u[q] = upper ? other - u[q] : u[q] + other;
+          }
+        }
+        const float a0 = u[0] + u[1], a1 = u[0] - u[1], a2 = u[2] + u[3], a3 = u[2] - u[3];
+        u[0] = a0 + a2; u[2] = a0 - a2; u[1] = a1 + a3; u[3] = a1 - a3;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) u[q] = (n > 0.f) ? u[q] / n : 0.f;
+        int code[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          int c = 0;
+#pragma unroll
+          for (int j = 0; j < 7; ++j) c += (u[q] >= thr[j]) ? 1 : 0;
+          code[q] = c;
+          rho[q] = u[q] - __shfl_sync(0xffffffffu, cent_lane, c);
+        }
+#pragma unroll
+        for (int pp = 0; pp < kMaxBits; ++pp)
+          if (pp < L.bits) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t w = __ballot_sync(0xffffffffu, (code[q] >> pp) & 1);
+              if (lane == q) sm.planes[i][pp][q] = w;
+            }
+          }
+        if (lane == 0) sm.n[i] = n;
+        if (L.qjl) {
+          const float gam = sqrtf(qlm::warp_sum(rho[0] * rho[0] + rho[1] * rho[1] + rho[2] * rho[2] + rho[3] * rho[3]));
+          if (lane == 0) sm.gamma[i] = gam;
+        }
+      }
+      if (L.qjl)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sm.rho[i][32 * q + lane] = rho[q];
+    }
+    if (L.qjl && !st_ready) {
+      cp_async_wait<0>();
+      st_ready = true;
+    }
+    __syncthreads();
+
+    if (L.qjl) {  // projections of 4 tokens onto rows 32 (R * share + r) + lane
+      const int quad = warp / kShare, share = warp % kShare;
+      float acc[4][R];
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[v][r] = 0.f;
+      const float* r0 = sm.rho[4 * quad];
+      const float* sc = st_s + 32 * R * share + lane;
+#pragma unroll 4
+      for (int i = 0; i < kHeadDim; i += 4) {
+        float4 rv[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) rv[v] = *reinterpret_cast<const float4*>(r0 + v * kHeadDim + i);
+#pragma unroll
+        for (int ii = 0; ii < 4; ++ii) {
+          float sv[R];
+#pragma unroll
+          for (int r = 0; r < R; ++r) sv[r] = sc[(i + ii) * kHeadDim + 32 * r];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const float x = ii == 0 ? rv[v].x : ii == 1 ? rv[v].y : ii == 2 ? rv[v].z : rv[v].w;
+#pragma unroll
+            for (int r = 0; r < R; ++r) acc[v][r] = fmaf(sv[r], x, acc[v][r]);
+          }
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const uint32_t w = __ballot_sync(0xffffffffu, acc[v][r] >= 0.f);
+          if (lane == r) sm.planes[4 * quad + v][kMaxBits][R * share + r] = w;
+        }
+      __syncthreads();
+    }
+
+    const int nplanes = L.bits + (L.qjl ? 1 : 0);
+    auto tile_base = [&](long long slot) {
+      return p.region[side] + (size_t)((slot / kPage * p.heads + h) * 2 + (slot % kPage) / kTile) * L.tile_bytes;
+    };
+    for (int pp = warp; pp < nplanes; pp += kAppWarps) {
+      const int src = pp < L.bits ? pp : kMaxBits;
+      const int off = pp < L.bits ? L.off_planes + pp * (kTile * 16) : L.off_sketch;
+      if (L.order == kOrderOctet) {
+        // lane = word 8t + 2m + hh of an octet: byte i is coordinate 32m + 16hh + 4t + i, bit j token j.
+        // Tokens of one octet that follow one another in the batch leave together.
+        const int wt = lane >> 3, wm = (lane >> 1) & 3, wh = lane & 1;
+        uint32_t word = 0, mask = 0;
+        long long octet = -1;
+        for (int i = 0; i <= TOK; ++i) {
+          const long long slot = i < TOK ? sm.slot[i] : -1;
+          const long long o = slot < 0 ? -1 : slot >> 3;
+          if (o != octet) {
+            if (octet >= 0) {
+              uint32_t* dst = reinterpret_cast<uint32_t*>(tile_base(octet << 3) + off) + (octet & 3) * 32 + lane;
+              if (mask == 0xffffffffu) {
+                *dst = word;
+              } else {
+                atomicAnd(dst, ~(mask & ~word));
+                atomicOr(dst, word);
+              }
+            }
+            octet = o;
+            word = mask = 0;
+          }
+          if (slot >= 0) {
+            const int j = (int)(slot & 7);
+            const uint32_t nib = (sm.planes[i][src][wm] >> (16 * wh + 4 * wt)) & 0xFu;
+            word = (word & ~(0x01010101u << j)) | (qlm::spread_nibble(nib) << j);
+            mask |= 0x01010101u << j;
+          }
+        }
+      } else {
+        for (int i = lane / 16; i < TOK; i += 2) {  // byte k of the row: two tokens a step
+          const long long slot = sm.slot[i];
+          if (slot < 0) continue;
+          const int k = lane & 15;
+          const char byte = (char)((sm.planes[i][src][k >> 2] >> (8 * (k & 3))) & 0xFFu);
+          char* tb = tile_base(slot) + off;
+          const int t = (int)(slot % kTile);
+          if (L.order == kOrderToken) tb[t * 16 + k] = byte;
+          else tb[k * kTile + t] = byte;
+        }
+      }
+    }
+    for (int i = tid; i < 2 * TOK; i += kAppThreads) {
+      const int tok = i % TOK;
+      const long long slot = sm.slot[tok];
+      if (slot < 0) continue;
+      char* tb = tile_base(slot) + (slot % kTile) * 2;
+      if (i < TOK) *reinterpret_cast<__half*>(tb + L.off_norm) = __float2half_rn(sm.n[tok]);
+      else if (L.qjl) *reinterpret_cast<__half*>(tb + L.off_gamma) = __float2half_rn(sm.gamma[tok]);
+    }
+    __syncthreads();  // the next tokens reuse the shared buffers
+  }
+}
+
+template <int TOK>
+cudaError_t launch_slots(const SlotQuantizeParams& p, cudaStream_t s) {
+  const bool sketch = p.side[0].qjl || p.side[1].qjl;
+  const size_t smem = (sizeof(AppSmem<TOK>) + 15) / 16 * 16 + (sketch ? sizeof(float) * kHeadDim * kHeadDim : 0);
+  cudaError_t e = cudaFuncSetAttribute(quantize_slots<TOK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const long long blocks = (long long)((p.n_tokens + TOK - 1) / TOK) * p.heads;
+  quantize_slots<TOK><<<dim3((unsigned)std::min<long long>(blocks, 148 * 4), 2), kAppThreads, smem, s>>>(p);
+  return launched();
+}
+
+}  // namespace
+
+cudaError_t launch_extend_block_table(const int* held, const int* n_new, int batch, const int* free_pages, int n_free,
+                                      const int* cursor, int* table, int pages_per_seq, int* seq_start, int* ctx_lens,
+                                      int* taken, cudaStream_t s) {
+  extend_block_table<<<(batch + kTableThreads - 1) / kTableThreads, kTableThreads, 0, s>>>(
+      held, n_new, batch, free_pages, n_free, cursor, table, pages_per_seq, seq_start, ctx_lens, taken);
+  return launched();
+}
+
+cudaError_t launch_slot_map(const int* held, const int* seq_start, const int* ctx_lens, int batch, const int* table,
+                            int pages_per_seq, int n_pages, int n_tokens, int* seq_ids, int* positions, long long* slots,
+                            cudaStream_t s) {
+  slot_map<<<(n_tokens + kSlotThreads - 1) / kSlotThreads, kSlotThreads, 0, s>>>(
+      held, seq_start, ctx_lens, batch, table, pages_per_seq, n_pages, n_tokens, seq_ids, positions, slots);
+  return launched();
+}
+
+cudaError_t launch_set_lengths(const LengthParams& p, cudaStream_t s) {
+  set_lengths<<<1, kMaxSeqPerLaunch, 0, s>>>(p);
+  return launched();
+}
+
+cudaError_t launch_quantize_slots(const SlotQuantizeParams& p, cudaStream_t s) {
+  const long long groups = (long long)((p.n_tokens + 31) / 32) * p.heads;
+  return groups >= 148 ? launch_slots<32>(p, s) : launch_slots<8>(p, s);
+}
+
+}  // namespace kvq

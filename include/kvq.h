@@ -212,6 +212,78 @@ kvq_status kvq_decode_partials(const kvq_cache* c, const void* q, kvq_dtype dtyp
 kvq_status kvq_combine_partials(const float* partials, int32_t n_parts, int32_t batch, int32_t n_q_heads,
                                 int32_t dv, float* out, void* stream);
 
+/* ---- Ragged serving path: one step over requests of different lengths, planned on the GPU ----------
+ * ("TurboQuant vs OSCAR vs EpiCache", OSCAR: fused kernels compatible with paged attention and the
+ * prefix cache.) A step gives pages to the new tokens of every request (kvq_extend_block_table), finds
+ * their slots (kvq_slot_map), codes them into the pages (kvq_quantize_slots) and attends with all of
+ * them at once (kvq_chunk_attention), each request with its own number of new tokens: a prompt, a part
+ * of one, a few speculated tokens, a single one, none. Lengths stay on the device, so a step needs no
+ * host synchronisation and can be captured into a graph. Ragged arrays are token-major: request b owns
+ * rows seq_start[b] .. seq_start[b + 1] - 1. Device arrays of int32 (int64) need 4 (8) byte alignment.
+ *
+ * kvq_extend_block_table: request b holds held[b] tokens (device, [batch]) and takes n_new[b] more
+ * (device, [batch]). Writes, all on the device:
+ *   block_table [batch][pages_per_seq]: entries ceil(held/64) .. ceil((held + n_new)/64) - 1 of each
+ *     request, from free_pages [n_free] in request order, starting at index *cursor (NULL: 0). Other
+ *     entries are left as they are;
+ *   seq_start [batch + 1]: exclusive prefix sums of n_new (negative counts as 0);
+ *   ctx_lens [batch]: held + n_new, or held for a refused request;
+ *   taken [2]: pages given out by this call, and requests refused. (A caller that keeps a cursor adds
+ *     taken[0] to it.)
+ * A request is refused, and gets no page, when held or n_new is negative, when held + n_new exceeds
+ * 64 pages_per_seq, or when the pages of the requests up to it exceed the free ones; a request that
+ * needs no page is never refused for want of them. A cursor outside [0, n_free] leaves no free page.
+ * The entries of free_pages are not checked (calls that read the table check them). Outputs may be
+ * neither inputs nor each other (KVQ_ERR_INVALID_ARG), nor overlap them. No cache needed; runs on the
+ * current device. */
+kvq_status kvq_extend_block_table(const int32_t* held, const int32_t* n_new, int32_t batch, const int32_t* free_pages,
+                                  int32_t n_free, const int32_t* cursor, int32_t* block_table, int32_t pages_per_seq,
+                                  int32_t* seq_start, int32_t* ctx_lens, int32_t* taken, void* stream);
+
+/* For every new token t < min(n_tokens, seq_start[batch]), in request b: seq_ids[t] = b, positions[t] =
+ * held[b] + t - seq_start[b] and slots[t] = 64 page + positions[t] % 64, page = block_table[b][position
+ * / 64]; the slot is -1 when the request was refused (ctx_lens[b] is not held[b] + its new tokens), or
+ * when the entry is not a page of a pool of n_pages, or the position is outside the table. seq_ids and
+ * positions (int32 [n_tokens]) may be NULL. Rows from seq_start[batch] on are left as they are. seq_start
+ * must not decrease. Outputs as above; n_tokens == 0 is a no-op. */
+kvq_status kvq_slot_map(const int32_t* held, const int32_t* seq_start, const int32_t* ctx_lens, int32_t batch,
+                        const int32_t* block_table, int32_t pages_per_seq, int32_t n_pages, int32_t n_tokens,
+                        int32_t* seq_ids, int32_t* positions, int64_t* slots, void* stream);
+
+/* Quantize a token-major batch K, V [n_tokens, n_kv_heads, head_dim] (f32 or bf16) into slots[t] (device
+ * int64) of a paged cache: the same codes, norms and sketch bits as kvq_quantize. A negative slot is
+ * skipped; one past the pool sets KVQ_STATUS_BAD_PAGE and is skipped. The slots of a call are distinct:
+ * a slot named twice ends up with unspecified content (its neighbours keep theirs). The cache's lengths
+ * do not change: give them to kvq_chunk_attention, or set them with kvq_cache_set_lengths. Caches that
+ * are not paged, or with a window, KIVI or FP4 codes: KVQ_ERR_UNSUPPORTED. n_tokens == 0: no-op. */
+kvq_status kvq_quantize_slots(kvq_cache* c, const void* K, const void* V, kvq_dtype dtype, const int64_t* slots,
+                              int32_t n_tokens, void* stream);
+
+/* Set every sequence's length (host array of `batch`), on the host and, on `stream`, on the device:
+ * after an append by slots, to start a sequence on pages it shares with another, or to reuse a finished
+ * sequence's place (length 0). The tokens below the length are what the pages hold. KVQ_ERR_INVALID_ARG
+ * for a negative length, KVQ_ERR_CAPACITY for one above the capacity (nothing written); window and KIVI
+ * caches: KVQ_ERR_UNSUPPORTED. */
+kvq_status kvq_cache_set_lengths(kvq_cache* c, const int32_t* lens, void* stream);
+
+/* Attention of a chunk of new tokens over the packed cache. q [n_tokens, n_q_heads, head_dim] (f32 or
+ * bf16) holds the new tokens' queries, request b's in rows seq_start[b] .. seq_start[b + 1] - 1 (device
+ * int32 [batch + 1], not decreasing, seq_start[batch] <= n_tokens); its tokens are the last ones of the
+ * ctx_lens[b] (device int32 [batch]; NULL: the cache's own lengths) that its cache holds, so row i sits
+ * at position ctx_lens[b] - n_new + i and attends to every position up to its own: a prompt's chunk
+ * appended before the call sees itself causally. out [n_tokens, n_q_heads, head_dim] has q's type. A row
+ * with no position to attend to (ctx_lens[b] < n_new) gets zeros; rows before seq_start[0] or behind the
+ * last request are left as they are. ctx_lens is cut to [0, capacity]. Logits and softmax as for
+ * kvq_decode_attention (n_new = 1 for every request computes the same attention); computed in fp32.
+ * LM, LM_QJL and SIGN1 caches without a window, paged or not; others KVQ_ERR_UNSUPPORTED. n_tokens * n_q_heads may not
+ * exceed 2^30. A block-table entry outside the pool sets KVQ_STATUS_BAD_PAGE and reads page 0. The
+ * workspace (kvq_chunk_workspace_bytes for this type and n_tokens) is in use until the call's work is
+ * done: calls that may overlap, and graphs that may replay at the same time, need one each. */
+kvq_status kvq_chunk_workspace_bytes(const kvq_cache* c, kvq_dtype dtype, int32_t n_tokens, size_t* bytes);
+kvq_status kvq_chunk_attention(const kvq_cache* c, const void* q, kvq_dtype dtype, int32_t n_tokens,
+                               const int32_t* seq_start, const int32_t* ctx_lens, void* out, void* workspace,
+                               size_t ws_bytes, void* stream);
+
 /* Device bytes of the staging buffer kvq_decode_step_host needs for inputs of type dtype: two
  * input slots (one step's K and V with n_new = 1 for all sequences, and q), then two output slots;
  * each region 256-byte aligned. */
