@@ -1174,8 +1174,8 @@ namespace {
 // The cache kinds the ragged path handles: rotated codes, no bf16 window.
 bool ragged_supported(const kvq_cache* c) { return !c->is_fp4 && !has_window(c); }
 bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-ChunkLayout chunk_layout_of(const kvq_cache* c, int n_tokens) {
-  return chunk_layout(n_tokens, c->batch, c->cfg.n_q_heads, c->cfg.n_kv_heads, c->k.qjl, c->v.qjl, c->sms);
+ChunkLayout chunk_layout_of(const kvq_cache* c, int n_tokens, bool bf16) {
+  return chunk_layout(n_tokens, c->batch, c->cfg.n_q_heads, c->cfg.n_kv_heads, c->k.qjl, c->v.qjl, bf16, c->sms);
 }
 }  // namespace
 
@@ -1281,7 +1281,7 @@ kvq_status kvq_chunk_workspace_bytes(const kvq_cache* c, kvq_dtype dtype, int32_
   if (dtype != KVQ_F32 && dtype != KVQ_BF16) return KVQ_ERR_INVALID_ARG;
   if (!ragged_supported(c)) return KVQ_ERR_UNSUPPORTED;
   if ((long)n_tokens * c->cfg.n_q_heads > (1l << 30)) return KVQ_ERR_INVALID_ARG;
-  *bytes = chunk_layout_of(c, n_tokens).total;
+  *bytes = chunk_layout_of(c, n_tokens, dtype == KVQ_BF16).total;
   return KVQ_OK;
 }
 
@@ -1297,13 +1297,14 @@ kvq_status kvq_chunk_attention(const kvq_cache* c, const void* q, kvq_dtype dtyp
   if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return KVQ_ERR_ALIGNMENT;
   if (!aligned_to(seq_start, 4) || !aligned_to(ctx_lens, 4)) return KVQ_ERR_ALIGNMENT;
   if (!on_cache_device(c)) return KVQ_ERR_INVALID_ARG;
-  const ChunkLayout L = chunk_layout_of(c, n_tokens);
+  const bool bf16 = dtype == KVQ_BF16;
+  const ChunkLayout L = chunk_layout_of(c, n_tokens, bf16);
   if (ws_bytes < L.total) return KVQ_ERR_WORKSPACE;
   ChunkParams p;
   std::memset(&p, 0, sizeof(p));
   p.q = q;
   p.out = out;
-  p.bf16 = dtype == KVQ_BF16;
+  p.bf16 = bf16;
   p.n_tokens = n_tokens;
   p.B = c->batch;
   p.Hq = c->cfg.n_q_heads;
@@ -1326,6 +1327,7 @@ kvq_status kvq_chunk_attention(const kvq_cache* c, const void* q, kvq_dtype dtyp
   p.St = c->d_St;
   p.logit_scale = default_scale(c->cfg) * 1.4426950408889634f;
   p.err = c->d_status;
+  p.wait_limit = kWaitLimitCycles;
   char* w = static_cast<char*>(workspace);
   p.rows = L.rows;
   p.max_tiles = L.max_tiles;
@@ -1335,6 +1337,7 @@ kvq_status kvq_chunk_attention(const kvq_cache* c, const void* q, kvq_dtype dtyp
   p.tile_start = reinterpret_cast<int*>(w + L.tile_start);
   p.head = reinterpret_cast<long long*>(w + L.head);
   p.qprep = w + L.qprep;
+  p.qscale = reinterpret_cast<float*>(w + L.qscale);
   p.part = reinterpret_cast<float*>(w + L.part);
   return launch_chunk_attention(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }

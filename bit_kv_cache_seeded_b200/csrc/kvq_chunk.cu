@@ -1,5 +1,5 @@
 // Attention of a ragged batch of new tokens over the packed LM / LM_QJL / SIGN1 cache: host plan, query
-// prep, the fp32 segment kernel, and the merge. ("TurboQuant vs OSCAR vs EpiCache", section
+// prep, the fp32 segment kernel, and the merge (bf16's segment kernel: kvq_chunk_umma.cu). ("TurboQuant vs OSCAR vs EpiCache", section
 // "Quantization frontiers: TurboQuant and OSCAR": rotation, Lloyd-Max codes, QJL sketch; kernels
 // compatible with paged attention.)
 //
@@ -106,8 +106,10 @@ __device__ void plan(const ChunkParams& p) {
   }
 }
 
-// Block 0 plans; the others rotate (and sketch) kPrepRows query rows each: fp32 [d (+ m)], the logit scale
-// and 1/sqrt(d) of the keys folded in.
+// Block 0 plans; the others rotate (and sketch) kPrepRows query rows each, the logit scale and 1/sqrt(d) of
+// the keys folded in. fp32 queries: rows of fp32 [d (+ m)]. bf16 queries: rows of fp16 for the tensor-core
+// kernel, in its order and with its scales, divided by a power of two (kept in qscale) that brings the row's
+// largest entry to [2^9, 2^10): half a step is 2^-11 of an entry down to 2^-23 of the largest.
 template <bool KQ>
 __global__ void __launch_bounds__(kPrepThreads) chunk_prep(const __grid_constant__ ChunkParams p) {
   if (blockIdx.x == 0) {
@@ -160,12 +162,35 @@ __global__ void __launch_bounds__(kPrepThreads) chunk_prep(const __grid_constant
   for (int v = 0; v < 4; ++v) {
     const long long row = row0 + v;
     if (row >= rows) break;
-    float* dst = static_cast<float*>(p.qprep) + (size_t)row * DK;
+    if (!p.bf16) {
+      float* dst = static_cast<float*>(p.qprep) + (size_t)row * DK;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        dst[32 * k + lane] = rot[v][k];
+        if (KQ) dst[kHeadDim + 32 * k + lane] = sk[v][k] * kKappa;
+      }
+      continue;
+    }
+    float mx = 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      dst[32 * k + lane] = rot[v][k];
-      if (KQ) dst[kHeadDim + 32 * k + lane] = sk[v][k] * kKappa;
+      rot[v][k] *= kCodeScale;
+      sk[v][k] *= kKappa * kSketchScale;
+      mx = fmaxf(mx, fmaxf(fabsf(rot[v][k]), fabsf(sk[v][k])));
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    int e = 0;
+    if (mx > 0.f && mx < INFINITY) e = min(max(ilogbf(mx) - 9, -126), 126);
+    const float inv = exp2f((float)-e);
+    __half* dst = static_cast<__half*>(p.qprep) + (size_t)row * DK;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int pos = query_pos(p.k.order, k, lane);
+      dst[pos] = __float2half_rn(rot[v][k] * inv);
+      if (KQ) dst[kHeadDim + pos] = __float2half_rn(sk[v][k] * inv);
+    }
+    if (lane == 0) p.qscale[row] = exp2f((float)e);
   }
 }
 
@@ -354,18 +379,15 @@ __global__ void __launch_bounds__(256) chunk_f32(const __grid_constant__ ChunkPa
         }
       }
     }
-    float* st = segment_state(p, w.item, blockIdx.x, DV);
+    float* ml = segment_ml(p, w.item, blockIdx.x, DV);
+    float* so = segment_o(p, w.item, blockIdx.x, DV);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int row = 4 * ty + i;
-      if (tx == 0) {
-        st[row] = m[i];
-        st[kF32Rows + row] = l[i];
-      }
+      if (tx == 0) *reinterpret_cast<float2*>(ml + 2 * row) = make_float2(m[i], l[i]);
 #pragma unroll
       for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) st[(2 + 64 * c + 4 * tx + j) * kF32Rows + row] = o[i][c][j];
+        *reinterpret_cast<float4*>(so + row * DV + 64 * c + 4 * tx) = make_float4(o[i][c][0], o[i][c][1], o[i][c][2], o[i][c][3]);
     }
   }
 }
@@ -402,31 +424,33 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge(const __grid_consta
     if (row >= r.count) continue;
     float m = -INFINITY, sum = 0.f;
     for (int c = c0; c <= c1; ++c) {
-      const float* st = segment_state(p, item, c, DV);
-      m = fmaxf(m, st[row]);
-      sum += st[p.rows + row];
+      const float2 s = *reinterpret_cast<const float2*>(segment_ml(p, item, c, DV) + 2 * row);
+      m = fmaxf(m, s.x);
+      sum += s.y;
     }
     if (m == -INFINITY || sum != sum) {  // nothing attended, or a logit that is NaN (the maximum passes over it)
       l[v] = sum;
       continue;
     }
     for (int c = c0; c <= c1; ++c) {
-      const float* st = segment_state(p, item, c, DV);
-      const float f = exp2f(st[row] - m);
+      const float2 s = *reinterpret_cast<const float2*>(segment_ml(p, item, c, DV) + 2 * row);
+      const float* o = segment_o(p, item, c, DV) + (size_t)row * DV;
+      const float f = exp2f(s.x - m);
       if (f == 0.f) continue;
-      l[v] = fmaf(f, st[p.rows + row], l[v]);
+      l[v] = fmaf(f, s.y, l[v]);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        acc[v][k] = fmaf(f, st[(size_t)(2 + 32 * k + lane) * p.rows + row], acc[v][k]);
-        if (VQ) accz[v][k] = fmaf(f, st[(size_t)(2 + kHeadDim + 32 * k + lane) * p.rows + row], accz[v][k]);
+        acc[v][k] = fmaf(f, o[32 * k + lane], acc[v][k]);
+        if (VQ) accz[v][k] = fmaf(f, o[kHeadDim + 32 * k + lane], accz[v][k]);
       }
     }
   }
   if (VQ) {  // acc += kappa S^T accz
+    const float zs = kKappa * (p.bf16 ? kSketchScale / kCodeScale : 1.f);
 #pragma unroll
     for (int v = 0; v < 4; ++v)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) s_z[VQ ? 4 * warp + v : 0][32 * k + lane] = accz[v][k] * kKappa;
+      for (int k = 0; k < 4; ++k) s_z[VQ ? 4 * warp + v : 0][32 * k + lane] = accz[v][k] * zs;
     __syncwarp();
 #pragma unroll 4
     for (int j = 0; j < kHeadDim; ++j) {
@@ -447,7 +471,7 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge(const __grid_consta
     fwht(acc[v], lane);
     const int row = row0 + v;
     if (row >= r.count) continue;
-    const float f = l[v] > 0.f ? 1.f / (kHeadDim * l[v]) : (l[v] == 0.f ? 0.f : l[v]);
+    const float f = l[v] > 0.f ? (p.bf16 ? kCodeScale : 1.f) / (kHeadDim * l[v]) : (l[v] == 0.f ? 0.f : l[v]);
     const size_t at = ((size_t)(r.start + r.first + row / p.group) * p.Hq + hk * p.group + row % p.group) * kHeadDim;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -471,9 +495,9 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
-ChunkLayout chunk_layout(int n_tokens, int batch, int Hq, int Hkv, bool k_qjl, bool v_qjl, int sms) {
+ChunkLayout chunk_layout(int n_tokens, int batch, int Hq, int Hkv, bool k_qjl, bool v_qjl, bool bf16, int sms) {
   ChunkLayout L;
-  L.rows = kF32Rows;
+  L.rows = bf16 ? chunk_umma_rows(v_qjl) : kF32Rows;
   const int per = L.rows / (Hq / Hkv);
   L.max_tiles = n_tokens / per + std::min(batch, n_tokens) + 1;
   L.ctas = sms;
@@ -488,7 +512,8 @@ ChunkLayout chunk_layout(int n_tokens, int batch, int Hq, int Hkv, bool k_qjl, b
   L.unit_start = take(sizeof(long long) * ((size_t)L.max_tiles + 1));
   L.tile_seq = take(sizeof(int) * (size_t)L.max_tiles);
   L.tile_start = take(sizeof(int) * ((size_t)batch + 1));
-  L.qprep = take(rows * kHeadDim * (k_qjl ? 2 : 1) * sizeof(float));
+  L.qprep = take(rows * kHeadDim * (k_qjl ? 2 : 1) * (bf16 ? sizeof(__half) : sizeof(float)));
+  L.qscale = take(bf16 ? sizeof(float) * rows : 0);
   L.part = take(sizeof(float) * segments * L.rows * (2 + kHeadDim * (v_qjl ? 2 : 1)));
   L.total = off;
   return L;
@@ -501,7 +526,8 @@ cudaError_t launch_chunk_attention(const ChunkParams& p, cudaStream_t s) {
   else chunk_prep<false><<<prep, kPrepThreads, 0, s>>>(p);
   cudaError_t e = launched();
   if (e != cudaSuccess) return e;
-  if (p.k.qjl) e = p.v.qjl ? launch_f32<true, true>(p, s) : launch_f32<true, false>(p, s);
+  if (p.bf16) e = launch_chunk_umma(p, s);
+  else if (p.k.qjl) e = p.v.qjl ? launch_f32<true, true>(p, s) : launch_f32<true, false>(p, s);
   else e = p.v.qjl ? launch_f32<false, true>(p, s) : launch_f32<false, false>(p, s);
   if (e != cudaSuccess) return e;
   const unsigned merge = (unsigned)((size_t)p.max_tiles * p.Hkv * (p.rows / kMergeRows));

@@ -10,9 +10,9 @@
 // lie end to end (kv-head h's from h * head[1]), and CTA c of G = min(CTAs, T) takes the units floor(c T / G)
 // .. floor((c + 1) T / G) - 1 of the T: an even split whatever the lengths, without a host that knows them.
 // A CTA's run of units in one tile is a segment; segment number = item + CTA (item = h * tiles + t) is
-// distinct, since every step from one segment to the next raises the item or the CTA. A segment writes
-// its softmax state, column-major: m [rows], l [rows], o [value dims][rows]; one kernel then merges the
-// segments of every row, folds the value sketch and rotates back.
+// distinct, since every step from one segment to the next raises the item or the CTA. A segment writes its
+// softmax state, (m, l) [rows][2] and o [rows][value dims]; one kernel then merges the segments of every row,
+// folds the value sketch and rotates back.
 #pragma once
 
 #include "kvq_internal.h"
@@ -104,10 +104,26 @@ struct Walk {
   }
 };
 
-__device__ __forceinline__ float* segment_state(const ChunkParams& p, long long item, int cta, int dv) {
+__device__ __forceinline__ float* segment_ml(const ChunkParams& p, long long item, int cta, int dv) {
   return p.part + (size_t)(item + cta) * p.rows * (2 + dv);
 }
+__device__ __forceinline__ float* segment_o(const ChunkParams& p, long long item, int cta, int dv) {
+  return segment_ml(p, item, cta, dv) + 2 * p.rows;
+}
+
+// Where the tensor-core kernel keeps coordinate 32 k + lane of a query (or of its sketch), so that the keys'
+// order in a tile need not change (see there).
+__device__ __forceinline__ int query_pos(int order, int k, int lane) {
+  if (order == kOrderOctet) return 32 * ((lane >> 2) & 3) + 8 * k + 4 * (lane >> 4) + (lane & 3);
+  const int byte = 4 * (k & 1) + (lane >> 3);  // of 8 in half a row
+  return 64 * (k >> 1) + 8 * (lane & 7) + byte;
+}
+constexpr float kCodeScale = 8.f, kSketchScale = 16.f;  // its operands hold 1/8 of a code, 1/16 of a sketch entry
 
 }  // namespace chunk
+
+// The bf16 path's segment kernel (kvq_chunk_umma.cu), and the query rows of its tile.
+int chunk_umma_rows(bool v_qjl);
+cudaError_t launch_chunk_umma(const ChunkParams& p, cudaStream_t s);
 
 }  // namespace kvq

@@ -1,0 +1,539 @@
+// Chunk attention's segment kernel on 5th-generation tensor cores (tcgen05, kind::f16, fp32 sums), for bf16
+// queries. Work plan and the states it leaves: kvq_chunk.cuh.
+//
+// A CTA walks its segments page by page (64 tokens). Per page and tile of 128 query rows
+//   S [128 x 64]  = Q [128 x DK] . K^T          (A, B from shared memory; DK = 128, + 128 of the key sketch)
+//   O [128 x DV] += P [128 x 64] . V            (A from tensor memory; DV = 128, + 128 of the value sketch)
+// with K and V dequantised from the packed page into fp16: entries n c / 8 (a code times the token's norm)
+// and +-n gamma / 16 (a sign bit); the powers of two keep every fp16 norm's entries in range, and the
+// queries and the merge carry their inverses. NT row tiles share a page's dequantisation: two where tensor
+// memory holds their sums (O takes 2 x 128 columns, S 2 x 2 x 64), one with a value sketch (O 256).
+//
+// Warps: 4 per row tile for the softmax (thread = row), 4 that dequantise keys (and fetch the queries of a
+// segment), 4 for values, 2 that issue the products (S, and P V one page behind; one thread issues an MMA
+// about every 50 cycles, so the two kinds run on two warps). K and V pages are staged twice, S twice per
+// tile, so that dequantisation, S, softmax and P V of neighbouring pages overlap. P overwrites the first
+// 32 columns of its S.
+//
+// Operands lie in shared memory as 128-byte-swizzled K-major rows: row r of an atom of 64 K-elements is 128
+// bytes, its 16-byte chunk c at chunk c ^ (r % 8). A dequantising thread makes 8 elements of a row at a time
+// and stores them as one chunk; 8 neighbouring threads fill 8 different chunks (no bank conflicts). Keys in
+// octet order give a thread coordinates 32 m + 16 h + 4 t + i of 8 tokens; the queries are stored in that
+// order (query_pos), since the product does not mind which way its K-elements are numbered.
+//
+// Softmax weights are p = 2^(x - m + 7), m the row's maximum but for steps under 2^8, by which it may lag
+// before O is rescaled: p stays under 2^15 in fp16, and a weight is dropped only below 2^-31 of the largest.
+// A value whose norm is not finite enters as zeros (0 p would be NaN in every row); the rows that attend
+// to it get a NaN sum from the page's mask instead.
+#include <cuda_fp16.h>
+
+#include "kvq_async.cuh"
+#include "kvq_chunk.cuh"
+#include "kvq_tcgen05.cuh"
+
+namespace kvq {
+namespace {
+
+using namespace chunk;
+
+constexpr int kStages = 2;
+constexpr int kTileRows = 128;
+constexpr float kLag = 8.f, kShift = 7.f;
+constexpr uint32_t kColS = 256, kTmemCols = 512;
+
+template <bool KQ, bool VQ>
+struct Cfg {
+  static constexpr int NT = VQ ? 1 : 2;
+  static constexpr int DK = KQ ? 256 : 128, DV = VQ ? 256 : 128;
+  static constexpr int kWarpK = 4 * NT, kWarpV = kWarpK + 4, kWarpS = kWarpV + 4, kWarpO = kWarpS + 1;
+  static constexpr int kThreads = 32 * (kWarpO + 1);
+  static constexpr int kQTile = kTileRows * DK * 2, kKStage = kPage * DK * 2, kVStage = kPage * DV * 2;
+  static constexpr int kOffK = NT * kQTile, kOffV = kOffK + kStages * kKStage, kOffEnd = kOffV + kStages * kVStage;
+};
+
+template <int NT>
+struct Bars {
+  uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages];
+  uint64_t sfull[NT][2], pready[NT][2], pvdone[NT][2];
+  uint64_t qfull, qempty, done[2];
+  unsigned char vbad[kStages][8];  // tokens of the page whose value norm is not finite, a bit each
+  uint32_t tmem;
+  int fail;
+};
+
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
+         ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t half_bits(float x) { return (uint32_t)__half_as_ushort(__float2half_rn(x)); }
+__device__ __forceinline__ float half_of(uint32_t bits) { return __half2float(__ushort_as_half((unsigned short)bits)); }
+
+// Four code words (one per plane) of 32 elements, element (byte i, bit s): prepared once, then the fp16 pairs
+// of bytes 0, 1 and 2, 3 for a bit s. Two bits: the code picks one of 4 halves. Three: the lower two bits,
+// inverted below zero, pick one of 4 magnitudes. The sign's word has bytes 1 and 2 exchanged, which puts the
+// bits of a pair 16 apart.
+__device__ __forceinline__ uint32_t sign_word(uint32_t w) { return __byte_perm(~w, 0, 0x3120); }
+
+template <int BITS>
+struct Codes {
+  uint32_t even, odd, neg;
+  __device__ __forceinline__ void set(const uint32_t (&w)[kMaxBits]) {
+    if (BITS == 1) neg = sign_word(w[0]);
+    if (BITS >= 2) {
+      const uint32_t flip = BITS == 3 ? ~w[2] : 0u;
+      const uint32_t a = w[0] ^ flip, b = w[1] ^ flip;
+      even = (a & 0x55555555u) | ((b & 0x55555555u) << 1);
+      odd = ((a >> 1) & 0x55555555u) | (b & 0xAAAAAAAAu);
+      if (BITS == 3) neg = sign_word(w[2]);
+    }
+  }
+  // lo, hi: the 4 halves (one bit: lo holds the magnitude twice)
+  __device__ __forceinline__ void get(int s, uint32_t lo, uint32_t hi, uint32_t& p01, uint32_t& p23) const {
+    if (BITS == 1) {
+      p01 = p23 = lo;
+    } else {
+      const uint32_t y = ((s & 1 ? odd : even) >> (s & 6)) & 0x03030303u;
+      const uint32_t sel = y * 0x22u + 0x10101010u;
+      p01 = __byte_perm(lo, hi, sel);
+      p23 = __byte_perm(lo, hi, sel >> 16);
+    }
+    if (BITS != 2) {
+      p01 ^= (neg << (15 - s)) & 0x80008000u;
+      p23 ^= (neg << (7 - s)) & 0x80008000u;
+    }
+  }
+};
+
+__device__ __forceinline__ void code_halves(const SideLayout& L, uint32_t& lo, uint32_t& hi) {
+  if (L.bits == 1) {
+    lo = hi = half_bits(L.cent[1] * 0.125f) * 0x10001u;
+  } else {
+    const int at = L.bits == 3 ? 4 : 0;
+    lo = half_bits(L.cent[at] * 0.125f) | half_bits(L.cent[at + 1] * 0.125f) << 16;
+    hi = half_bits(L.cent[at + 2] * 0.125f) | half_bits(L.cent[at + 3] * 0.125f) << 16;
+  }
+}
+
+// A thread's share of one side's page: 8 bytes of every plane, and 8 tokens' norms (keys in token order: one).
+struct PageRegs {
+  uint2 plane[kMaxBits], sketch;
+  uint4 norm, gamma;
+};
+
+template <bool QJL>
+__device__ __forceinline__ void load_page(PageRegs& r, const SideLayout& L, const unsigned char* tile, int off8, int slot) {
+#pragma unroll
+  for (int p = 0; p < kMaxBits; ++p)
+    if (p < L.bits) r.plane[p] = __ldg(reinterpret_cast<const uint2*>(tile + L.off_planes + p * (kTile * 16) + off8));
+  if (QJL) r.sketch = __ldg(reinterpret_cast<const uint2*>(tile + L.off_sketch + off8));
+  r.norm = __ldg(reinterpret_cast<const uint4*>(tile + L.off_norm + 2 * slot));
+  if (QJL) r.gamma = __ldg(reinterpret_cast<const uint4*>(tile + L.off_gamma + 2 * slot));
+}
+
+__device__ __forceinline__ uint32_t half_at(const uint4& v, int i) {  // i-th of 8
+  const uint32_t w = (i >> 1) == 0 ? v.x : (i >> 1) == 1 ? v.y : (i >> 1) == 2 ? v.z : v.w;
+  return i & 1 ? w >> 16 : w & 0xFFFFu;
+}
+
+// 8 bits s of the words: 8 elements each (4 of each word), scaled by scale(s, pair) and stored as one chunk at
+// dst(s); their signs times sgn(s, pair) at dst(s) + sketch_off.
+template <int BITS, bool QJL, typename Scale, typename Sgn, typename Dst>
+__device__ __forceinline__ void expand(const PageRegs& r, uint32_t lo, uint32_t hi, Scale scale, Sgn sgn, Dst dst, int sketch_off) {
+  Codes<BITS> a, b;
+  uint32_t wa[kMaxBits], wb[kMaxBits];
+#pragma unroll
+  for (int p = 0; p < kMaxBits; ++p) {
+    wa[p] = r.plane[p].x;
+    wb[p] = r.plane[p].y;
+  }
+  a.set(wa);
+  b.set(wb);
+  const uint32_t za = QJL ? sign_word(r.sketch.x) : 0u, zb = QJL ? sign_word(r.sketch.y) : 0u;
+#pragma unroll
+  for (int s = 0; s < 8; ++s) {
+    uint32_t v[4];
+    a.get(s, lo, hi, v[0], v[1]);
+    b.get(s, lo, hi, v[2], v[3]);
+    unsigned char* d = dst(s);
+    *reinterpret_cast<uint4*>(d) =
+        make_uint4(mul2(v[0], scale(s, 0)), mul2(v[1], scale(s, 1)), mul2(v[2], scale(s, 2)), mul2(v[3], scale(s, 3)));
+    if (QJL)
+      *reinterpret_cast<uint4*>(d + sketch_off) =
+          make_uint4(sgn(s, 0) ^ ((za << (15 - s)) & 0x80008000u), sgn(s, 1) ^ ((za << (7 - s)) & 0x80008000u),
+                     sgn(s, 2) ^ ((zb << (15 - s)) & 0x80008000u), sgn(s, 3) ^ ((zb << (7 - s)) & 0x80008000u));
+  }
+}
+
+template <bool QJL, typename Scale, typename Sgn, typename Dst>
+__device__ __forceinline__ void expand_bits(int bits, const PageRegs& r, uint32_t lo, uint32_t hi, Scale scale, Sgn sgn, Dst dst,
+                                            int sketch_off) {
+  if (bits == 2) expand<2, QJL>(r, lo, hi, scale, sgn, dst, sketch_off);
+  else if (bits == 3) expand<3, QJL>(r, lo, hi, scale, sgn, dst, sketch_off);
+  else expand<1, QJL>(r, lo, hi, scale, sgn, dst, sketch_off);
+}
+
+__device__ __forceinline__ int segment_pages(const Walk& w) { return max(0, min(w.k1, (w.rows.limit + kPage - 1) / kPage) - w.k0); }
+
+template <bool KQ, bool VQ>
+__global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __grid_constant__ ChunkParams p) {
+  using C = Cfg<KQ, VQ>;
+  constexpr int NT = C::NT, DK = C::DK, DV = C::DV;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  __shared__ __align__(8) Bars<NT> bars;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_addr(&bars.kfull[i]), 128);
+      mbar_init(smem_addr(&bars.kempty[i]), 1);
+      mbar_init(smem_addr(&bars.vfull[i]), 128);
+      mbar_init(smem_addr(&bars.vempty[i]), 1);
+    }
+    for (int t = 0; t < NT; ++t)
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(smem_addr(&bars.sfull[t][b]), 1);
+        mbar_init(smem_addr(&bars.pready[t][b]), 128);
+        mbar_init(smem_addr(&bars.pvdone[t][b]), 1);
+      }
+    mbar_init(smem_addr(&bars.qfull), 128);
+    mbar_init(smem_addr(&bars.qempty), 1);
+    mbar_init(smem_addr(&bars.done[0]), 1);
+    mbar_init(smem_addr(&bars.done[1]), 1);
+    mbar_init_fence();
+    bars.fail = 0;
+  }
+  if (warp == 0) tc::alloc(smem_addr(&bars.tmem), kTmemCols);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = bars.tmem;
+  const uint32_t sm = smem_addr(smem);
+  // a wait that gives up ends every later one at once; the loops are bounded by the plan
+  auto wait = [&](uint64_t& bar, uint32_t parity) {
+    const uint32_t a = smem_addr(&bar);
+    if (mbar_try(a, parity) || *(volatile int*)&bars.fail) return;
+    if (!mbar_wait_spin(a, parity, p.wait_limit)) {
+      bars.fail = 1;
+      atomicOr(p.err, 1);
+    }
+  };
+  Walk w;
+  w.init(p, blockIdx.x);
+
+  if (warp < C::kWarpK) {  // ---- softmax: thread = row
+    const int t = warp >> 2, row = tid;  // row of the NT * 128
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t tO = tmem + lanes + t * DV, tS = tmem + lanes + kColS + t * 128;
+    int n = 0, nv = 0;  // pages this tile, and the CTA, has seen
+    while (w.next(p)) {
+      const Rows r = w.rows;
+      const int np = segment_pages(w);
+      const bool used = t * kTileRows < r.count && np > 0;
+      const bool work = warp * 32 < r.count;
+      const int last = row < r.count ? min(r.pos0 + row / p.group, r.ctx - 1) : -1;
+      float qs = 1.f;
+      if (row < r.count)
+        qs = p.qscale[(size_t)(r.start + r.first + row / p.group) * p.Hq + w.hk * p.group + row % p.group];
+      float m = -INFINITY, ref = 0.f, l = 0.f;
+      for (int j = 0; used && j < np; ++j, ++n) {
+        const int b = n & 1, st = (nv + j) % kStages;
+        wait(bars.sfull[t][b], (n >> 1) & 1);
+        tc::fence_after();
+        if (work) {
+          uint32_t s[kPage];
+          uint32_t(&s0)[32] = *reinterpret_cast<uint32_t(*)[32]>(s);
+          uint32_t(&s1)[32] = *reinterpret_cast<uint32_t(*)[32]>(s + 32);
+          tc::tmem_ld32(tS + 64 * b, s0);
+          tc::tmem_ld32(tS + 64 * b + 32, s1);
+          tc::wait_ld();
+          const int reach = last - (w.k0 + j) * kPage;  // the page's tokens 0 .. reach are attended
+          if (!__all_sync(0xffffffffu, reach >= kPage - 1)) {
+#pragma unroll
+            for (int i = 0; i < kPage; ++i) s[i] = i <= reach ? s[i] : 0xff800000u;
+          }
+          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < kPage; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], __uint_as_float(s[i]));
+          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * qs;
+          const bool grow = mx > m + kLag || (m == -INFINITY && mx > m);
+          if (__any_sync(0xffffffffu, grow)) {
+            const float alpha = grow ? ex2f(m - mx) : 1.f;
+            if (grow) {
+              m = mx;
+              ref = mx - kShift;
+            }
+            l *= alpha;
+            if (j > 0) {
+              wait(bars.pvdone[t][(n - 1) & 1], ((n - 1) >> 1) & 1);
+              tc::fence_after();
+#pragma unroll 1
+              for (int c = 0; c < DV; c += 16) {
+                uint32_t o[16];
+                tc::tmem_ld16(tO + c, o);
+                tc::wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                tc::tmem_st16(tO + c, o);
+              }
+              tc::wait_st();
+            }
+          }
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          uint32_t ph[kPage / 2];
+#pragma unroll
+          for (int i = 0; i < kPage / 2; ++i) {
+            const float a = ex2f(fmaf(__uint_as_float(s[2 * i]), qs, -ref));
+            const float c = ex2f(fmaf(__uint_as_float(s[2 * i + 1]), qs, -ref));
+            sum[i & 3] += a + c;
+            const __half2 h = __floats2half2_rn(a, c);
+            ph[i] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tc::tmem_st32(tS + 64 * b, ph);
+          wait(bars.vfull[st], ((nv + j) / kStages) & 1);
+          const unsigned long long bad = *reinterpret_cast<const volatile unsigned long long*>(bars.vbad[st]);
+          if (bad != 0 && reach >= 0 && (bad & (~0ull >> (63 - min(reach, 63)))) != 0) l = NAN;
+          tc::wait_st();
+        }
+        tc::fence_before();
+        mbar_arrive(smem_addr(&bars.pready[t][b]));
+      }
+      nv += np;
+      // the segment's state
+      if (used) {
+        wait(bars.pvdone[t][(n - 1) & 1], ((n - 1) >> 1) & 1);
+        tc::fence_after();
+      }
+      if (work) {
+        float* ml = segment_ml(p, w.item, blockIdx.x, DV) + 2 * row;
+        float* so = segment_o(p, w.item, blockIdx.x, DV) + (size_t)row * DV;
+        if (row < r.count) *reinterpret_cast<float2*>(ml) = make_float2(m == -INFINITY ? m : ref, l);
+#pragma unroll 1
+        for (int c = 0; c < DV; c += 16) {
+          uint32_t o[16];
+          if (used) {
+            tc::tmem_ld16(tO + c, o);
+            tc::wait_ld();
+          }
+          if (row < r.count)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+              *reinterpret_cast<uint4*>(so + c + i) =
+                  used ? make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]) : make_uint4(0, 0, 0, 0);
+        }
+      }
+      tc::fence_before();
+    }
+  } else if (warp < C::kWarpV) {  // ---- keys, and the queries of each segment
+    const int th = tid - 32 * C::kWarpK;
+    const bool octet = p.k.order == kOrderOctet;
+    // octet order: tokens 8 o .. + 7, coordinates of words 2 g, 2 g + 1; token order: token th / 2, half a row
+    const int o = th >> 4, g = th & 15;
+    const int tile = octet ? o >> 2 : th >> 6;
+    const int off8 = octet ? (o & 3) * 128 + g * 8 : ((th >> 1) & 31) * 16 + (th & 1) * 8;
+    const int slot = octet ? 8 * (o & 3) : ((th >> 1) & 31) & ~7;
+    uint32_t lo, hi;
+    code_halves(p.k, lo, hi);
+    auto fetch = [&](PageRegs& r, int page) {
+      const long ti = tile_index_read(p.table, p.pages_per_seq, p.n_pages, p.tiles_per_seq, p.Hkv, w.rows.b, w.hk, 2 * page, p.err);
+      load_page<KQ>(r, p.k, reinterpret_cast<const unsigned char*>(p.kreg) + (size_t)(ti + tile) * p.k.tile_bytes, off8, slot);
+    };
+    int n = 0, seg = 0;
+    PageRegs regs;
+    while (w.next(p)) {
+      const Rows r = w.rows;
+      const int np = segment_pages(w);
+      if (np == 0) continue;
+      fetch(regs, w.k0);
+      if (seg > 0) wait(bars.qempty, (seg - 1) & 1);
+      ++seg;
+      constexpr int kChunks = DK / 8;
+      const size_t qrow0 = (size_t)(r.start + r.first) * p.Hq + w.hk * p.group;
+#pragma unroll 8
+      for (int i = th; i < NT * kTileRows * kChunks; i += 128) {
+        const int row = i / kChunks, ch = i % kChunks;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (row < r.count)
+          v = *(reinterpret_cast<const uint4*>(static_cast<const __half*>(p.qprep) +
+                                               (qrow0 + (size_t)(row / p.group) * p.Hq + row % p.group) * DK) + ch);
+        const int rr = row & (kTileRows - 1);
+        *reinterpret_cast<uint4*>(smem + (row / kTileRows) * C::kQTile + (ch >> 3) * (kTileRows * 128) + rr * 128 +
+                                  (((ch & 7) ^ (rr & 7)) << 4)) = v;
+      }
+      fence_proxy_async();
+      mbar_arrive(smem_addr(&bars.qfull));
+      for (int j = 0; j < np; ++j, ++n) {
+        const int st = n % kStages;
+        if (n >= kStages) wait(bars.kempty[st], (n / kStages - 1) & 1);
+        unsigned char* base = smem + C::kOffK + st * C::kKStage;
+        const PageRegs cur = regs;
+        if (j + 1 < np) fetch(regs, w.k0 + j + 1);
+        constexpr int kSketch = 2 * kPage * 128;  // past the two atoms of the codes
+        if (octet) {
+          uint32_t nn[8], ng[8];
+#pragma unroll
+          for (int s = 0; s < 8; ++s) {
+            const uint32_t h = half_at(cur.norm, s);
+            nn[s] = h * 0x10001u;
+            if (KQ) ng[s] = half_bits(half_of(h) * half_of(half_at(cur.gamma, s)) * 0.0625f) * 0x10001u;
+          }
+          unsigned char* d0 = base + (g >> 3) * (kPage * 128) + o * 1024;
+          expand_bits<KQ>(p.k.bits, cur, lo, hi, [&](int s, int) { return nn[s]; }, [&](int s, int) { return ng[s]; },
+                          [&](int s) { return d0 + s * 128 + (((g & 7) ^ s) << 4); }, kSketch);
+        } else {
+          const int tok = th >> 1, i = tok & 7;
+          const uint32_t h = half_at(cur.norm, i), nn = h * 0x10001u;
+          const uint32_t ng = KQ ? half_bits(half_of(h) * half_of(half_at(cur.gamma, i)) * 0.0625f) * 0x10001u : 0u;
+          unsigned char* d0 = base + (th & 1) * (kPage * 128) + tok * 128;
+          expand_bits<KQ>(p.k.bits, cur, lo, hi, [&](int, int) { return nn; }, [&](int, int) { return ng; },
+                          [&](int s) { return d0 + ((s ^ i) << 4); }, kSketch);
+        }
+        fence_proxy_async();
+        mbar_arrive(smem_addr(&bars.kfull[st]));
+      }
+    }
+  } else if (warp < C::kWarpS) {  // ---- values: dims 8 k .. + 7 of tokens 8 c .. + 7
+    const int th = tid - 32 * C::kWarpV;
+    const int c = th & 7, k = th >> 3;
+    uint32_t lo, hi;
+    code_halves(p.v, lo, hi);
+    auto fetch = [&](PageRegs& r, int page) {
+      const long ti = tile_index_read(p.table, p.pages_per_seq, p.n_pages, p.tiles_per_seq, p.Hkv, w.rows.b, w.hk, 2 * page, p.err);
+      load_page<VQ>(r, p.v, reinterpret_cast<const unsigned char*>(p.vreg) + (size_t)(ti + (c >> 2)) * p.v.tile_bytes,
+                    k * kTile + 8 * (c & 3), 8 * (c & 3));
+    };
+    int n = 0;
+    PageRegs regs;
+    while (w.next(p)) {
+      const int np = segment_pages(w);
+      if (np == 0) continue;
+      fetch(regs, w.k0);
+      for (int j = 0; j < np; ++j, ++n) {
+        const int st = n % kStages;
+        if (n >= kStages) wait(bars.vempty[st], (n / kStages - 1) & 1);
+        const PageRegs cur = regs;
+        const int tokens = w.rows.limit - (w.k0 + j) * kPage - 8 * c;  // of this thread's 8
+        if (j + 1 < np) fetch(regs, w.k0 + j + 1);
+        uint32_t nn[4], ng[4], bad = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t nh[2], gh[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            nh[e] = 2 * i + e < tokens ? half_at(cur.norm, 2 * i + e) : 0u;
+            gh[e] = VQ && 2 * i + e < tokens ? half_at(cur.gamma, 2 * i + e) : 0u;
+            if ((nh[e] & 0x7C00u) == 0x7C00u || (gh[e] & 0x7C00u) == 0x7C00u) {
+              bad |= 1u << (2 * i + e);
+              nh[e] = gh[e] = 0u;
+            }
+          }
+          nn[i] = nh[0] | nh[1] << 16;
+          ng[i] = half_bits(half_of(nh[0]) * half_of(gh[0]) * 0.0625f) | half_bits(half_of(nh[1]) * half_of(gh[1]) * 0.0625f) << 16;
+        }
+        if (k == 0) bars.vbad[st][c] = (unsigned char)bad;
+        unsigned char* d0 = smem + C::kOffV + st * C::kVStage + k * 1024;
+        expand_bits<VQ>(p.v.bits, cur, lo, hi, [&](int, int i) { return nn[i]; }, [&](int, int i) { return ng[i]; },
+                        [&](int s) { return d0 + s * 128 + ((c ^ s) << 4); }, kHeadDim * 128);
+        fence_proxy_async();
+        mbar_arrive(smem_addr(&bars.vfull[st]));
+      }
+    }
+  } else if (warp == C::kWarpS) {  // ---- S = Q K^T
+    if (lane == 0) {
+      constexpr uint32_t id = tc::idesc_f16(0, 0, 0, kTileRows, kPage);
+      int n = 0, seg = 0, nt[NT] = {};
+      while (w.next(p)) {
+        const int np = segment_pages(w);
+        if (np == 0) continue;
+        wait(bars.qfull, seg & 1);
+        ++seg;
+        for (int j = 0; j < np; ++j, ++n) {
+          const int st = n % kStages;
+          wait(bars.kfull[st], (n / kStages) & 1);
+          const uint64_t kd = desc_sw128(sm + C::kOffK + st * C::kKStage);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            if (t * kTileRows >= w.rows.count) continue;
+            const int b = nt[t] & 1;
+            if (nt[t] >= 2) wait(bars.pvdone[t][b], ((nt[t] >> 1) - 1) & 1);  // P of two pages before is read
+            tc::fence_after();
+            const uint64_t qd = desc_sw128(sm + t * C::kQTile);
+#pragma unroll
+            for (int i = 0; i < DK / 16; ++i)
+              tc::umma_f16(tmem + kColS + t * 128 + b * 64, qd + (((i >> 2) * (kTileRows * 128) + (i & 3) * 32) >> 4),
+                           kd + (((i >> 2) * (kPage * 128) + (i & 3) * 32) >> 4), id, i > 0);
+            tc::commit(smem_addr(&bars.sfull[t][b]));
+            ++nt[t];
+          }
+          tc::commit(smem_addr(&bars.kempty[st]));
+        }
+        tc::commit(smem_addr(&bars.qempty));
+      }
+      tc::commit(smem_addr(&bars.done[0]));
+      mbar_wait(smem_addr(&bars.done[0]), 0, p.wait_limit);
+    }
+  } else {  // ---- O += P V
+    if (lane == 0) {
+      constexpr uint32_t id = tc::idesc_f16(0, 0, 0, kTileRows, DV);
+      int n = 0, nt[NT] = {};
+      while (w.next(p)) {
+        const int np = segment_pages(w);
+        for (int j = 0; j < np; ++j, ++n) {
+          const int st = n % kStages;
+          wait(bars.vfull[st], (n / kStages) & 1);
+          const uint64_t vd = desc_sw128(sm + C::kOffV + st * C::kVStage);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            if (t * kTileRows >= w.rows.count) continue;
+            const int b = nt[t] & 1;
+            wait(bars.pready[t][b], (nt[t] >> 1) & 1);
+            tc::fence_after();
+#pragma unroll
+            for (int i = 0; i < kPage / 16; ++i)
+              tc::umma_f16_ta(tmem + t * DV, tmem + kColS + t * 128 + b * 64 + 8 * i, vd + ((i * 32) >> 4), id, j > 0 || i > 0);
+            tc::commit(smem_addr(&bars.pvdone[t][b]));
+            ++nt[t];
+          }
+          tc::commit(smem_addr(&bars.vempty[st]));
+        }
+      }
+      tc::commit(smem_addr(&bars.done[1]));
+      mbar_wait(smem_addr(&bars.done[1]), 0, p.wait_limit);
+    }
+  }
+  __syncwarp();
+  tc::fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc::fence_after();
+    tc::dealloc(tmem, kTmemCols);
+  }
+}
+
+template <bool KQ, bool VQ>
+cudaError_t launch(const ChunkParams& p, cudaStream_t s) {
+  constexpr int smem = Cfg<KQ, VQ>::kOffEnd;
+  const cudaError_t e = cudaFuncSetAttribute(chunk_umma<KQ, VQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  chunk_umma<KQ, VQ><<<p.ctas, Cfg<KQ, VQ>::kThreads, smem, s>>>(p);
+  return launched();
+}
+
+}  // namespace
+
+int chunk_umma_rows(bool v_qjl) { return kTileRows * (v_qjl ? Cfg<true, true>::NT : Cfg<true, false>::NT); }
+
+cudaError_t launch_chunk_umma(const ChunkParams& p, cudaStream_t s) {
+  if (p.k.qjl) return p.v.qjl ? launch<true, true>(p, s) : launch<true, false>(p, s);
+  return p.v.qjl ? launch<false, true>(p, s) : launch<false, false>(p, s);
+}
+
+}  // namespace kvq

@@ -203,6 +203,7 @@ struct ChunkParams {
   const float* St;
   float logit_scale;        // softmax_scale * log2(e)
   int* err;
+  long long wait_limit;
   // workspace
   int rows;                 // query rows of a row tile
   int max_tiles;            // row tiles of one kv-head the workspace holds
@@ -212,13 +213,14 @@ struct ChunkParams {
   int* tile_start;          // [B + 1]
   long long* head;          // row tiles of a kv-head, units of a kv-head
   void* qprep;              // rotated (and sketched) queries
+  float* qscale;            // [n_tokens * Hq] (bf16)
   float* part;              // softmax states of the segments
 };
 
 // Byte offsets of a chunk call's workspace.
 struct ChunkLayout {
   int rows, max_tiles, ctas;
-  size_t unit_start, tile_seq, tile_start, head, qprep, part, total;
+  size_t unit_start, tile_seq, tile_start, head, qprep, qscale, part, total;
 };
 
 // Reads cudaGetLastError() right after a kernel launch and, when it is cudaSuccess, adds one to
@@ -281,7 +283,7 @@ cudaError_t launch_slot_map(const int* held, const int* seq_start, const int* ct
                             cudaStream_t s);
 cudaError_t launch_set_lengths(const LengthParams& p, cudaStream_t s);
 cudaError_t launch_quantize_slots(const SlotQuantizeParams& p, cudaStream_t s);
-ChunkLayout chunk_layout(int n_tokens, int batch, int Hq, int Hkv, bool k_qjl, bool v_qjl, int sms);
+ChunkLayout chunk_layout(int n_tokens, int batch, int Hq, int Hkv, bool k_qjl, bool v_qjl, bool bf16, int sms);
 cudaError_t launch_chunk_attention(const ChunkParams& p, cudaStream_t s);
 cudaError_t launch_decode_mla_mma(const MlaParams& p, cudaStream_t s);
 
