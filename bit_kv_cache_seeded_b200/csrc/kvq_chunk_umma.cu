@@ -77,38 +77,42 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t half_bits(float x) { return (uint32_t)__half_as_ushort(__float2half_rn(x)); }
 __device__ __forceinline__ float half_of(uint32_t bits) { return __half2float(__ushort_as_half((unsigned short)bits)); }
 
-// Four code words (one per plane) of 32 elements, element (byte i, bit s): prepared once, then the fp16 pairs
-// of bytes 0, 1 and 2, 3 for a bit s. Two bits: the code picks one of 4 halves. Three: the lower two bits,
-// inverted below zero, pick one of 4 magnitudes. The sign's word has bytes 1 and 2 exchanged, which puts the
-// bits of a pair 16 apart.
-__device__ __forceinline__ uint32_t sign_word(uint32_t w) { return __byte_perm(~w, 0, 0x3120); }
+// The code words (one per plane) of 32 elements, element (byte i, bit s): prepared once, then the fp16 pairs of
+// bytes 0, 1 and 2, 3 for s = 0 .. 7 in turn, which shifts the words along. Two bits: the code picks one of 4
+// halves. Three: the lower two bits, inverted below zero, pick one of 4 magnitudes. A sign word is rotated so
+// that bit s of bytes 0 and 1 comes to bits 15 and 31 after s steps, that of bytes 2 and 3 eight later.
+__device__ __forceinline__ uint32_t rotr(uint32_t w, int n) { return __funnelshift_r(w, w, n); }
+__device__ __forceinline__ uint32_t sign_word(uint32_t w) { return rotr(__byte_perm(~w, 0, 0x3120), 17); }
+constexpr uint32_t kSigns = 0x80008000u;
 
 template <int BITS>
 struct Codes {
   uint32_t even, odd, neg;
-  __device__ __forceinline__ void set(const uint32_t (&w)[kMaxBits]) {
-    if (BITS == 1) neg = sign_word(w[0]);
+  __device__ __forceinline__ void set(uint32_t w0, uint32_t w1, uint32_t w2) {
+    if (BITS == 1) neg = sign_word(w0);
     if (BITS >= 2) {
-      const uint32_t flip = BITS == 3 ? ~w[2] : 0u;
-      const uint32_t a = w[0] ^ flip, b = w[1] ^ flip;
+      const uint32_t flip = BITS == 3 ? ~w2 : 0u;
+      const uint32_t a = w0 ^ flip, b = w1 ^ flip;
       even = (a & 0x55555555u) | ((b & 0x55555555u) << 1);
       odd = ((a >> 1) & 0x55555555u) | (b & 0xAAAAAAAAu);
-      if (BITS == 3) neg = sign_word(w[2]);
+      if (BITS == 3) neg = sign_word(w2);
     }
   }
-  // lo, hi: the 4 halves (one bit: lo holds the magnitude twice)
-  __device__ __forceinline__ void get(int s, uint32_t lo, uint32_t hi, uint32_t& p01, uint32_t& p23) const {
+  // the next s, of parity `parity`; lo, hi: the 4 halves (one bit: lo holds the magnitude twice)
+  __device__ __forceinline__ void next(int parity, uint32_t lo, uint32_t hi, uint32_t& p01, uint32_t& p23) {
     if (BITS == 1) {
       p01 = p23 = lo;
     } else {
-      const uint32_t y = ((s & 1 ? odd : even) >> (s & 6)) & 0x03030303u;
-      const uint32_t sel = y * 0x22u + 0x10101010u;
+      uint32_t& w = parity ? odd : even;
+      const uint32_t sel = (w & 0x03030303u) * 0x22u + 0x10101010u;
+      w >>= 2;
       p01 = __byte_perm(lo, hi, sel);
       p23 = __byte_perm(lo, hi, sel >> 16);
     }
     if (BITS != 2) {
-      p01 ^= (neg << (15 - s)) & 0x80008000u;
-      p23 ^= (neg << (7 - s)) & 0x80008000u;
+      p01 ^= neg & kSigns;
+      p23 ^= rotr(neg, 8) & kSigns;
+      neg = rotr(neg, 1);
     }
   }
 };
@@ -133,7 +137,7 @@ template <bool QJL>
 __device__ __forceinline__ void load_page(PageRegs& r, const SideLayout& L, const unsigned char* tile, int off8, int slot) {
 #pragma unroll
   for (int p = 0; p < kMaxBits; ++p)
-    if (p < L.bits) r.plane[p] = __ldg(reinterpret_cast<const uint2*>(tile + L.off_planes + p * (kTile * 16) + off8));
+    r.plane[p] = p >= L.bits ? make_uint2(0, 0) : __ldg(reinterpret_cast<const uint2*>(tile + L.off_planes + p * (kTile * 16) + off8));
   if (QJL) r.sketch = __ldg(reinterpret_cast<const uint2*>(tile + L.off_sketch + off8));
   r.norm = __ldg(reinterpret_cast<const uint4*>(tile + L.off_norm + 2 * slot));
   if (QJL) r.gamma = __ldg(reinterpret_cast<const uint4*>(tile + L.off_gamma + 2 * slot));
@@ -143,42 +147,60 @@ __device__ __forceinline__ uint32_t half_at(const uint4& v, int i) {  // i-th of
   const uint32_t w = (i >> 1) == 0 ? v.x : (i >> 1) == 1 ? v.y : (i >> 1) == 2 ? v.z : v.w;
   return i & 1 ? w >> 16 : w & 0xFFFFu;
 }
+__device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
 
-// 8 bits s of the words: 8 elements each (4 of each word), scaled by scale(s, pair) and stored as one chunk at
-// dst(s); their signs times sgn(s, pair) at dst(s) + sketch_off.
-template <int BITS, bool QJL, typename Scale, typename Sgn, typename Dst>
-__device__ __forceinline__ void expand(const PageRegs& r, uint32_t lo, uint32_t hi, Scale scale, Sgn sgn, Dst dst, int sketch_off) {
+// For s = 0 .. 7 the 8 elements (4 of each word) scaled by a norm, stored as one chunk at d + s * step + 16 (x ^ s),
+// and their signs times the sketch's magnitude sketch_off further. ROWS (keys): s is a token, nn[s / 2] holds
+// its norm in half s % 2, ng the magnitude. Otherwise (values) pair i of tokens has nn[i], ng[i].
+// The loop stays rolled: unrolled, the four roles' code misses the instruction cache (38% of all
+// stalls; a page took 4500 cycles to dequantise).
+template <int BITS, bool QJL, bool ROWS>
+__device__ __forceinline__ void expand(const PageRegs& r, uint32_t lo, uint32_t hi, const uint32_t (&nn)[4], const uint32_t (&ng)[4],
+                                       uint32_t d, int step, uint32_t x, int sketch_off) {
   Codes<BITS> a, b;
-  uint32_t wa[kMaxBits], wb[kMaxBits];
+  a.set(r.plane[0].x, r.plane[1].x, r.plane[2].x);
+  b.set(r.plane[0].y, r.plane[1].y, r.plane[2].y);
+  uint32_t za = QJL ? sign_word(r.sketch.x) : 0u, zb = QJL ? sign_word(r.sketch.y) : 0u;
+  uint32_t n[4] = {nn[0], nn[1], nn[2], nn[3]}, g[4] = {ng[0], ng[1], ng[2], ng[3]};
+#pragma unroll 1
+  for (int q = 0; q < 4; ++q) {
 #pragma unroll
-  for (int p = 0; p < kMaxBits; ++p) {
-    wa[p] = r.plane[p].x;
-    wb[p] = r.plane[p].y;
-  }
-  a.set(wa);
-  b.set(wb);
-  const uint32_t za = QJL ? sign_word(r.sketch.x) : 0u, zb = QJL ? sign_word(r.sketch.y) : 0u;
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t at = d + ((x ^ (2 * q + e)) << 4);
+      uint32_t v[4], m[4], h[4];
+      a.next(e, lo, hi, v[0], v[1]);
+      b.next(e, lo, hi, v[2], v[3]);
 #pragma unroll
-  for (int s = 0; s < 8; ++s) {
-    uint32_t v[4];
-    a.get(s, lo, hi, v[0], v[1]);
-    b.get(s, lo, hi, v[2], v[3]);
-    unsigned char* d = dst(s);
-    *reinterpret_cast<uint4*>(d) =
-        make_uint4(mul2(v[0], scale(s, 0)), mul2(v[1], scale(s, 1)), mul2(v[2], scale(s, 2)), mul2(v[3], scale(s, 3)));
-    if (QJL)
-      *reinterpret_cast<uint4*>(d + sketch_off) =
-          make_uint4(sgn(s, 0) ^ ((za << (15 - s)) & 0x80008000u), sgn(s, 1) ^ ((za << (7 - s)) & 0x80008000u),
-                     sgn(s, 2) ^ ((zb << (15 - s)) & 0x80008000u), sgn(s, 3) ^ ((zb << (7 - s)) & 0x80008000u));
+      for (int i = 0; i < 4; ++i) {
+        m[i] = ROWS ? __byte_perm(n[0], 0, e ? 0x3232 : 0x1010) : n[i];
+        h[i] = ROWS ? __byte_perm(g[0], 0, e ? 0x3232 : 0x1010) : g[i];
+      }
+      sts16(at, mul2(v[0], m[0]), mul2(v[1], m[1]), mul2(v[2], m[2]), mul2(v[3], m[3]));
+      if (QJL) {
+        sts16(at + sketch_off, h[0] ^ (za & kSigns), h[1] ^ (rotr(za, 8) & kSigns), h[2] ^ (zb & kSigns), h[3] ^ (rotr(zb, 8) & kSigns));
+        za = rotr(za, 1);
+        zb = rotr(zb, 1);
+      }
+      d += step;
+    }
+    if (ROWS) {
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        n[i] = n[i + 1];
+        g[i] = g[i + 1];
+      }
+    }
   }
 }
 
-template <bool QJL, typename Scale, typename Sgn, typename Dst>
-__device__ __forceinline__ void expand_bits(int bits, const PageRegs& r, uint32_t lo, uint32_t hi, Scale scale, Sgn sgn, Dst dst,
-                                            int sketch_off) {
-  if (bits == 2) expand<2, QJL>(r, lo, hi, scale, sgn, dst, sketch_off);
-  else if (bits == 3) expand<3, QJL>(r, lo, hi, scale, sgn, dst, sketch_off);
-  else expand<1, QJL>(r, lo, hi, scale, sgn, dst, sketch_off);
+template <bool QJL, bool ROWS>
+__device__ __forceinline__ void expand_bits(int bits, const PageRegs& r, uint32_t lo, uint32_t hi, const uint32_t (&nn)[4],
+                                            const uint32_t (&ng)[4], uint32_t d, int step, uint32_t x, int sketch_off) {
+  if (bits == 2) expand<2, QJL, ROWS>(r, lo, hi, nn, ng, d, step, x, sketch_off);
+  else if (bits == 3) expand<3, QJL, ROWS>(r, lo, hi, nn, ng, d, step, x, sketch_off);
+  else expand<1, QJL, ROWS>(r, lo, hi, nn, ng, d, step, x, sketch_off);
 }
 
 __device__ __forceinline__ int segment_pages(const Walk& w) { return max(0, min(w.k1, (w.rows.limit + kPage - 1) / kPage) - w.k0); }
@@ -248,20 +270,25 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
         wait(bars.sfull[t][b], (n >> 1) & 1);
         tc::fence_after();
         if (work) {
-          uint32_t s[kPage];
-          uint32_t(&s0)[32] = *reinterpret_cast<uint32_t(*)[32]>(s);
-          uint32_t(&s1)[32] = *reinterpret_cast<uint32_t(*)[32]>(s + 32);
-          tc::tmem_ld32(tS + 64 * b, s0);
-          tc::tmem_ld32(tS + 64 * b + 32, s1);
-          tc::wait_ld();
+          // two halves of 32 columns, read from tensor memory again for the second pass: a rolled loop (see expand)
           const int reach = last - (w.k0 + j) * kPage;  // the page's tokens 0 .. reach are attended
-          if (!__all_sync(0xffffffffu, reach >= kPage - 1)) {
+          const bool full = __all_sync(0xffffffffu, reach >= kPage - 1);
+          auto logits = [&](uint32_t (&s)[32], int c) {
+            tc::tmem_ld32(tS + 64 * b + c, s);
+            tc::wait_ld();
+            if (!full) {
 #pragma unroll
-            for (int i = 0; i < kPage; ++i) s[i] = i <= reach ? s[i] : 0xff800000u;
-          }
+              for (int i = 0; i < 32; ++i) s[i] = c + i <= reach ? s[i] : 0xff800000u;
+            }
+          };
           float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+          for (int c = 0; c < kPage; c += 32) {
+            uint32_t s[32];
+            logits(s, c);
 #pragma unroll
-          for (int i = 0; i < kPage; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], __uint_as_float(s[i]));
+            for (int i = 0; i < 32; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], __uint_as_float(s[i]));
+          }
           const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * qs;
           const bool grow = mx > m + kLag || (m == -INFINITY && mx > m);
           if (__any_sync(0xffffffffu, grow)) {
@@ -287,17 +314,21 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
             }
           }
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
-          uint32_t ph[kPage / 2];
+#pragma unroll 1
+          for (int c = 0; c < kPage; c += 32) {
+            uint32_t s[32], ph[16];
+            logits(s, c);
 #pragma unroll
-          for (int i = 0; i < kPage / 2; ++i) {
-            const float a = ex2f(fmaf(__uint_as_float(s[2 * i]), qs, -ref));
-            const float c = ex2f(fmaf(__uint_as_float(s[2 * i + 1]), qs, -ref));
-            sum[i & 3] += a + c;
-            const __half2 h = __floats2half2_rn(a, c);
-            ph[i] = *reinterpret_cast<const uint32_t*>(&h);
+            for (int i = 0; i < 16; ++i) {
+              const float a = ex2f(fmaf(__uint_as_float(s[2 * i]), qs, -ref));
+              const float d = ex2f(fmaf(__uint_as_float(s[2 * i + 1]), qs, -ref));
+              sum[i & 3] += a + d;
+              const __half2 h = __floats2half2_rn(a, d);
+              ph[i] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            tc::tmem_st16(tS + 64 * b + c / 2, ph);
           }
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          tc::tmem_st32(tS + 64 * b, ph);
           wait(bars.vfull[st], ((nv + j) / kStages) & 1);
           const unsigned long long bad = *reinterpret_cast<const volatile unsigned long long*>(bars.vbad[st]);
           if (bad != 0 && reach >= 0 && (bad & (~0ull >> (63 - min(reach, 63)))) != 0) l = NAN;
@@ -337,13 +368,17 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
     const bool octet = p.k.order == kOrderOctet;
     // octet order: tokens 8 o .. + 7, coordinates of words 2 g, 2 g + 1; token order: token th / 2, half a row
     const int o = th >> 4, g = th & 15;
-    const int tile = octet ? o >> 2 : th >> 6;
-    const int off8 = octet ? (o & 3) * 128 + g * 8 : ((th >> 1) & 31) * 16 + (th & 1) * 8;
-    const int slot = octet ? 8 * (o & 3) : ((th >> 1) & 31) & ~7;
+    const int tok = th >> 1;
+    const int tile = octet ? o >> 2 : tok >> 5;
+    const int off8 = octet ? (o & 3) * 128 + g * 8 : (tok & 31) * 16 + (th & 1) * 8;
+    const int slot = octet ? 8 * (o & 3) : tok & 24;
+    const uint32_t row_off = octet ? (g >> 3) * (kPage * 128) + o * 1024 : (th & 1) * (kPage * 128) + tok * 128;
     uint32_t lo, hi;
     code_halves(p.k, lo, hi);
-    auto fetch = [&](PageRegs& r, int page) {
-      const long ti = tile_index_read(p.table, p.pages_per_seq, p.n_pages, p.tiles_per_seq, p.Hkv, w.rows.b, w.hk, 2 * page, p.err);
+    auto find = [&](int page) {
+      return tile_index_read(p.table, p.pages_per_seq, p.n_pages, p.tiles_per_seq, p.Hkv, w.rows.b, w.hk, 2 * page, p.err);
+    };
+    auto fetch = [&](PageRegs& r, long ti) {
       load_page<KQ>(r, p.k, reinterpret_cast<const unsigned char*>(p.kreg) + (size_t)(ti + tile) * p.k.tile_bytes, off8, slot);
     };
     int n = 0, seg = 0;
@@ -352,7 +387,8 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
       const Rows r = w.rows;
       const int np = segment_pages(w);
       if (np == 0) continue;
-      fetch(regs, w.k0);
+      fetch(regs, find(w.k0));
+      long index = np > 1 ? find(w.k0 + 1) : 0;  // of the page after the one in regs
       if (seg > 0) wait(bars.qempty, (seg - 1) & 1);
       ++seg;
       constexpr int kChunks = DK / 8;
@@ -373,29 +409,27 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
       for (int j = 0; j < np; ++j, ++n) {
         const int st = n % kStages;
         if (n >= kStages) wait(bars.kempty[st], (n / kStages - 1) & 1);
-        unsigned char* base = smem + C::kOffK + st * C::kKStage;
+        const uint32_t base = sm + C::kOffK + st * C::kKStage;
         const PageRegs cur = regs;
-        if (j + 1 < np) fetch(regs, w.k0 + j + 1);
-        constexpr int kSketch = 2 * kPage * 128;  // past the two atoms of the codes
-        if (octet) {
-          uint32_t nn[8], ng[8];
+        if (j + 1 < np) fetch(regs, index);
+        if (j + 2 < np) index = find(w.k0 + j + 2);
+        uint32_t nn[4] = {cur.norm.x, cur.norm.y, cur.norm.z, cur.norm.w}, ng[4] = {};
+        if (KQ) {
+          const uint32_t gg[4] = {cur.gamma.x, cur.gamma.y, cur.gamma.z, cur.gamma.w};
 #pragma unroll
-          for (int s = 0; s < 8; ++s) {
-            const uint32_t h = half_at(cur.norm, s);
-            nn[s] = h * 0x10001u;
-            if (KQ) ng[s] = half_bits(half_of(h) * half_of(half_at(cur.gamma, s)) * 0.0625f) * 0x10001u;
-          }
-          unsigned char* d0 = base + (g >> 3) * (kPage * 128) + o * 1024;
-          expand_bits<KQ>(p.k.bits, cur, lo, hi, [&](int s, int) { return nn[s]; }, [&](int s, int) { return ng[s]; },
-                          [&](int s) { return d0 + s * 128 + (((g & 7) ^ s) << 4); }, kSketch);
-        } else {
-          const int tok = th >> 1, i = tok & 7;
-          const uint32_t h = half_at(cur.norm, i), nn = h * 0x10001u;
-          const uint32_t ng = KQ ? half_bits(half_of(h) * half_of(half_at(cur.gamma, i)) * 0.0625f) * 0x10001u : 0u;
-          unsigned char* d0 = base + (th & 1) * (kPage * 128) + tok * 128;
-          expand_bits<KQ>(p.k.bits, cur, lo, hi, [&](int, int) { return nn; }, [&](int, int) { return ng; },
-                          [&](int s) { return d0 + ((s ^ i) << 4); }, kSketch);
+          for (int i = 0; i < 4; ++i) ng[i] = mul2(mul2(nn[i], 0x2C002C00u), gg[i]);  // n / 16 * gamma
         }
+        if (!octet) {  // one token
+          const uint32_t nt = half_at(cur.norm, tok & 7) * 0x10001u;
+          const uint32_t gt = KQ ? half_at(make_uint4(ng[0], ng[1], ng[2], ng[3]), tok & 7) * 0x10001u : 0u;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            nn[i] = nt;
+            ng[i] = gt;
+          }
+        }
+        expand_bits<KQ, true>(p.k.bits, cur, lo, hi, nn, ng, base + row_off, octet ? 128 : 0, octet ? g & 7 : tok & 7,
+                              2 * kPage * 128);
         fence_proxy_async();
         mbar_arrive(smem_addr(&bars.kfull[st]));
       }
@@ -405,8 +439,10 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
     const int c = th & 7, k = th >> 3;
     uint32_t lo, hi;
     code_halves(p.v, lo, hi);
-    auto fetch = [&](PageRegs& r, int page) {
-      const long ti = tile_index_read(p.table, p.pages_per_seq, p.n_pages, p.tiles_per_seq, p.Hkv, w.rows.b, w.hk, 2 * page, p.err);
+    auto find = [&](int page) {
+      return tile_index_read(p.table, p.pages_per_seq, p.n_pages, p.tiles_per_seq, p.Hkv, w.rows.b, w.hk, 2 * page, p.err);
+    };
+    auto fetch = [&](PageRegs& r, long ti) {
       load_page<VQ>(r, p.v, reinterpret_cast<const unsigned char*>(p.vreg) + (size_t)(ti + (c >> 2)) * p.v.tile_bytes,
                     k * kTile + 8 * (c & 3), 8 * (c & 3));
     };
@@ -415,13 +451,15 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
     while (w.next(p)) {
       const int np = segment_pages(w);
       if (np == 0) continue;
-      fetch(regs, w.k0);
+      fetch(regs, find(w.k0));
+      long index = np > 1 ? find(w.k0 + 1) : 0;  // of the page after the one in regs
       for (int j = 0; j < np; ++j, ++n) {
         const int st = n % kStages;
         if (n >= kStages) wait(bars.vempty[st], (n / kStages - 1) & 1);
         const PageRegs cur = regs;
         const int tokens = w.rows.limit - (w.k0 + j) * kPage - 8 * c;  // of this thread's 8
-        if (j + 1 < np) fetch(regs, w.k0 + j + 1);
+        if (j + 1 < np) fetch(regs, index);
+        if (j + 2 < np) index = find(w.k0 + j + 2);
         uint32_t nn[4], ng[4], bad = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -439,9 +477,7 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
           ng[i] = half_bits(half_of(nh[0]) * half_of(gh[0]) * 0.0625f) | half_bits(half_of(nh[1]) * half_of(gh[1]) * 0.0625f) << 16;
         }
         if (k == 0) bars.vbad[st][c] = (unsigned char)bad;
-        unsigned char* d0 = smem + C::kOffV + st * C::kVStage + k * 1024;
-        expand_bits<VQ>(p.v.bits, cur, lo, hi, [&](int, int i) { return nn[i]; }, [&](int, int i) { return ng[i]; },
-                        [&](int s) { return d0 + s * 128 + ((c ^ s) << 4); }, kHeadDim * 128);
+        expand_bits<VQ, false>(p.v.bits, cur, lo, hi, nn, ng, sm + C::kOffV + st * C::kVStage + k * 1024, 128, c, kHeadDim * 128);
         fence_proxy_async();
         mbar_arrive(smem_addr(&bars.vfull[st]));
       }
