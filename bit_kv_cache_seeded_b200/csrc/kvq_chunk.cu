@@ -43,6 +43,53 @@ __device__ __forceinline__ void fwht(float (&u)[4], int lane) {
   u[0] = a0 + a2; u[2] = a0 - a2; u[1] = a1 + a3; u[3] = a1 - a3;
 }
 
+// C [32 x 128] = A [32 x 128] . M [128 x 128] on the tensor cores (mma.sync, tf32 operands, fp32 sums) for the
+// bf16 calls' two small products with the sketch matrix: S q~ per query row, S^T z per output row. tf32 rounds by
+// half a step of 2^-11 and keeps fp32's range, so the matrix needs no scaling. Warp w of 8 makes columns 16 w ..
+// + 15 and keeps its fragments of M in registers over the block's row groups. On the CUDA cores the products
+// took 2-3 times the rest of these kernels (prep of 131072 rows 207 us, merge of 55000 rows 110 us).
+constexpr int kPad = kHeadDim + 4;  // row stride of A: lane (g, t) reads bank 4 g + t
+
+struct TfFrags {
+  uint32_t b[2][16][2];
+};
+__device__ __forceinline__ uint32_t tf32(float x) {
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;\n" : "=r"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ void load_frags(TfFrags& f, const float* M, int warp, int lane) {
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        f.b[n][k][h] = tf32(__ldg(M + (8 * k + (lane & 3) + 4 * h) * kHeadDim + 16 * warp + 8 * n + (lane >> 2)));
+}
+__device__ __forceinline__ void tf32_product(const TfFrags& f, const float (*a)[kPad], float (*c)[kPad], int warp, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    float acc[2][4] = {};
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const uint32_t a0 = tf32(a[16 * m + g][8 * k + t]), a1 = tf32(a[16 * m + g + 8][8 * k + t]);
+      const uint32_t a2 = tf32(a[16 * m + g][8 * k + t + 4]), a3 = tf32(a[16 * m + g + 8][8 * k + t + 4]);
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+        asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+                     : "+f"(acc[n][0]), "+f"(acc[n][1]), "+f"(acc[n][2]), "+f"(acc[n][3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(f.b[n][k][0]), "r"(f.b[n][k][1]));
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<float2*>(&c[16 * m + g + 8 * h][16 * warp + 8 * n + 2 * t]) = make_float2(acc[n][2 * h], acc[n][2 * h + 1]);
+  }
+}
+
 // One block's plan of the call: row tiles per request, their units, prefix sums of both.
 __device__ void plan(const ChunkParams& p) {
   __shared__ long long s_warp[kPrepThreads / 32];
@@ -110,87 +157,101 @@ __device__ void plan(const ChunkParams& p) {
 // the keys folded in. fp32 queries: rows of fp32 [d (+ m)]. bf16 queries: rows of fp16 for the tensor-core
 // kernel, in its order and with its scales, divided by a power of two (kept in qscale) that brings the row's
 // largest entry to [2^9, 2^10): half a step is 2^-11 of an entry down to 2^-23 of the largest.
-template <bool KQ>
+template <bool KQ, bool BF16>
 __global__ void __launch_bounds__(kPrepThreads) chunk_prep(const __grid_constant__ ChunkParams p) {
   if (blockIdx.x == 0) {
     plan(p);
     return;
   }
-  __shared__ float s_q[kPrepRows][kHeadDim];
+  __shared__ float s_q[kPrepRows][kPad], s_k[KQ && BF16 ? kPrepRows : 1][kPad];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long rows = (long long)p.n_tokens * p.Hq;
-  const long long row0 = (long long)(blockIdx.x - 1) * kPrepRows + 4 * warp;
   constexpr int DK = KQ ? 2 * kHeadDim : kHeadDim;
-  float rot[4][4], sk[4][4];
+  TfFrags frags;
+  if (KQ && BF16) load_frags(frags, p.St, warp, lane);
+  for (long long group = blockIdx.x - 1; group * kPrepRows < rows; group += gridDim.x - 1) {
+    const long long row0 = group * kPrepRows + 4 * warp;
+    float rot[4][4], sk[4][4];
 #pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    const long long row = row0 + v;
-    if (row < rows) {
-      const float* sg = p.signs + (int)(row % p.Hq) / p.group * p.signs_stride;
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        rot[v][k] = qlm::load_elem(p.q, (size_t)row * kHeadDim + 32 * k + lane, p.bf16) * sg[32 * k + lane];
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) rot[v][k] = 0.f;
-    }
-    fwht(rot[v], lane);
-    // R q * scale / sqrt(d) = H D q * scale / d
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      rot[v][k] *= p.logit_scale * (1.f / kHeadDim);
-      if (KQ) s_q[4 * warp + v][32 * k + lane] = rot[v][k];
-      sk[v][k] = 0.f;
-    }
-  }
-  if (KQ) {  // kappa S q~, row j = 32 r + lane, from S^T [i][j]
-    __syncwarp();
-#pragma unroll 4
-    for (int i = 0; i < kHeadDim; ++i) {
-      float st[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) st[r] = __ldg(p.St + i * kHeadDim + 32 * r + lane);
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const float x = s_q[4 * warp + v][i];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) sk[v][r] = fmaf(st[r], x, sk[v][r]);
-      }
-    }
-  }
-#pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    const long long row = row0 + v;
-    if (row >= rows) break;
-    if (!p.bf16) {
-      float* dst = static_cast<float*>(p.qprep) + (size_t)row * DK;
+    for (int v = 0; v < 4; ++v) {
+      const long long row = row0 + v;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        dst[32 * k + lane] = rot[v][k];
-        if (KQ) dst[kHeadDim + 32 * k + lane] = sk[v][k] * kKappa;
+        rot[v][k] = row < rows ? qlm::load_elem(p.q, (size_t)row * kHeadDim + 32 * k + lane, BF16) : 0.f;
+        sk[v][k] = 0.f;
       }
-      continue;
-    }
-    float mx = 0.f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      rot[v][k] *= kCodeScale;
-      sk[v][k] *= kKappa * kSketchScale;
-      mx = fmaxf(mx, fmaxf(fabsf(rot[v][k]), fabsf(sk[v][k])));
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    int e = 0;
-    if (mx > 0.f && mx < INFINITY) e = min(max(ilogbf(mx) - 9, -126), 126);
-    const float inv = exp2f((float)-e);
-    __half* dst = static_cast<__half*>(p.qprep) + (size_t)row * DK;
+    for (int v = 0; v < 4; ++v) {
+      const float* sg = p.signs + (int)((row0 + v) % p.Hq) / p.group * p.signs_stride;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int pos = query_pos(p.k.order, k, lane);
-      dst[pos] = __float2half_rn(rot[v][k] * inv);
-      if (KQ) dst[kHeadDim + pos] = __float2half_rn(sk[v][k] * inv);
+      for (int k = 0; k < 4; ++k) rot[v][k] *= sg[32 * k + lane];
+      fwht(rot[v], lane);
+      // R q * scale / sqrt(d) = H D q * scale / d
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        rot[v][k] *= p.logit_scale * (1.f / kHeadDim);
+        if (KQ) s_q[4 * warp + v][32 * k + lane] = rot[v][k];
+      }
     }
-    if (lane == 0) p.qscale[row] = exp2f((float)e);
+    if (KQ && BF16) {  // S q~
+      __syncthreads();
+      tf32_product(frags, s_q, s_k, warp, lane);
+      __syncthreads();
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sk[v][k] = s_k[4 * warp + v][32 * k + lane];
+    } else if (KQ) {  // row j = 32 r + lane of S q~, from S^T [i][j]
+      __syncwarp();
+#pragma unroll 16
+      for (int i = 0; i < kHeadDim; ++i) {
+        float st[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) st[r] = __ldg(p.St + i * kHeadDim + 32 * r + lane);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float x = s_q[4 * warp + v][i];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) sk[v][r] = fmaf(st[r], x, sk[v][r]);
+        }
+      }
+      __syncwarp();
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const long long row = row0 + v;
+      if (row >= rows) break;
+      if (!BF16) {
+        float* dst = static_cast<float*>(p.qprep) + (size_t)row * DK;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          dst[32 * k + lane] = rot[v][k];
+          if (KQ) dst[kHeadDim + 32 * k + lane] = sk[v][k] * kKappa;
+        }
+        continue;
+      }
+      float mx = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        rot[v][k] *= kCodeScale;
+        sk[v][k] *= kKappa * kSketchScale;
+        mx = fmaxf(mx, fmaxf(fabsf(rot[v][k]), fabsf(sk[v][k])));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      int e = 0;
+      if (mx > 0.f && mx < INFINITY) e = min(max(ilogbf(mx) - 9, -126), 126);
+      const float inv = exp2f((float)-e);
+      __half* dst = static_cast<__half*>(p.qprep) + (size_t)row * DK;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int pos = query_pos(p.k.order, k, lane);
+        dst[pos] = __float2half_rn(rot[v][k] * inv);
+        if (KQ) dst[kHeadDim + pos] = __float2half_rn(sk[v][k] * inv);
+      }
+      if (lane == 0) p.qscale[row] = exp2f((float)e);
+    }
   }
 }
 
@@ -394,92 +455,124 @@ __global__ void __launch_bounds__(256) chunk_f32(const __grid_constant__ ChunkPa
 
 // ---- merge --------------------------------------------------------------------------------------------
 //
-// A block merges 32 rows of one item (kv-head, row tile): a warp 4 rows, lane l dims 32 k + l.
+// A block merges groups of 32 rows of one item (kv-head, row tile): a warp 4 rows, lane l dims 32 k + l.
 constexpr int kMergeThreads = 256, kMergeRows = 32;
 
-template <bool VQ>
+template <bool VQ, bool BF16>
 __global__ void __launch_bounds__(kMergeThreads) chunk_merge(const __grid_constant__ ChunkParams p) {
   constexpr int DV = VQ ? 2 * kHeadDim : kHeadDim;
-  __shared__ float s_z[VQ ? kMergeRows : 1][kHeadDim];
+  __shared__ float s_z[VQ ? kMergeRows : 1][kPad], s_c[VQ && BF16 ? kMergeRows : 1][kPad];
   const int tiles = (int)p.head[0];
   const int per = p.rows / kMergeRows;
   const long long items = (long long)tiles * p.Hkv;
-  const long long item = blockIdx.x / per;
-  if (item >= items) return;
-  const int hk = (int)(item / tiles), tile = (int)(item % tiles);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row0 = (int)(blockIdx.x % per) * kMergeRows + 4 * warp;
-  const int b = p.tile_seq[tile];
-  const Rows r = tile_rows(p, b, tile - p.tile_start[b]);
   const long long units = p.head[1], T = units * p.Hkv, G = cta_count(p, T);
-  const int c0 = cta_of(hk * units + p.unit_start[tile], T, G);
-  const int c1 = cta_of(hk * units + p.unit_start[tile + 1] - 1, T, G);
-  float acc[4][4], accz[4][4], l[4];
+  TfFrags frags;
+  if (VQ && BF16 && blockIdx.x < items * per) load_frags(frags, p.S, warp, lane);
+  for (long long group = blockIdx.x; group < items * per; group += gridDim.x) {
+    const long long item = group / per;
+    const int hk = (int)(item / tiles), tile = (int)(item % tiles);
+    const int group0 = (int)(group % per) * kMergeRows, row0 = group0 + 4 * warp;
+    const int b = p.tile_seq[tile];
+    const Rows r = tile_rows(p, b, tile - p.tile_start[b]);
+    if (group0 >= r.count) continue;
+    const int c0 = cta_of(hk * units + p.unit_start[tile], T, G);
+    const int c1 = cta_of(hk * units + p.unit_start[tile + 1] - 1, T, G);
+    float acc[4][4], accz[4][4], l[4];
 #pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    l[v] = 0.f;
+    for (int v = 0; v < 4; ++v) {
+      l[v] = 0.f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) acc[v][k] = accz[v][k] = 0.f;
-    const int row = row0 + v;
-    if (row >= r.count) continue;
-    float m = -INFINITY, sum = 0.f;
-    for (int c = c0; c <= c1; ++c) {
-      const float2 s = *reinterpret_cast<const float2*>(segment_ml(p, item, c, DV) + 2 * row);
-      m = fmaxf(m, s.x);
-      sum += s.y;
+      for (int k = 0; k < 4; ++k) acc[v][k] = accz[v][k] = 0.f;
+      const int row = row0 + v;
+      if (row >= r.count) continue;
+      float m = -INFINITY, sum = 0.f;
+      for (int c = c0; c <= c1; ++c) {
+        const float2 s = *reinterpret_cast<const float2*>(segment_ml(p, item, c, DV) + 2 * row);
+        m = fmaxf(m, s.x);
+        sum += s.y;
+      }
+      if (m == -INFINITY || sum != sum) {  // nothing attended, or a logit that is NaN (the maximum passes over it)
+        l[v] = sum;
+        continue;
+      }
+      for (int c = c0; c <= c1; ++c) {
+        const float2 s = *reinterpret_cast<const float2*>(segment_ml(p, item, c, DV) + 2 * row);
+        const float* o = segment_o(p, item, c, DV) + (size_t)row * DV;
+        const float f = exp2f(s.x - m);
+        if (f == 0.f) continue;
+        l[v] = fmaf(f, s.y, l[v]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          acc[v][k] = fmaf(f, o[32 * k + lane], acc[v][k]);
+          if (VQ) accz[v][k] = fmaf(f, o[kHeadDim + 32 * k + lane], accz[v][k]);
+        }
+      }
     }
-    if (m == -INFINITY || sum != sum) {  // nothing attended, or a logit that is NaN (the maximum passes over it)
-      l[v] = sum;
-      continue;
+    if (VQ) {  // acc += kappa S^T accz
+      const float zs = kKappa * (BF16 ? kSketchScale / kCodeScale : 1.f);
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s_z[4 * warp + v][32 * k + lane] = accz[v][k] * zs;
     }
-    for (int c = c0; c <= c1; ++c) {
-      const float2 s = *reinterpret_cast<const float2*>(segment_ml(p, item, c, DV) + 2 * row);
-      const float* o = segment_o(p, item, c, DV) + (size_t)row * DV;
-      const float f = exp2f(s.x - m);
-      if (f == 0.f) continue;
-      l[v] = fmaf(f, s.y, l[v]);
+    if (VQ && BF16) {
+      __syncthreads();
+      tf32_product(frags, s_z, s_c, warp, lane);
+      __syncthreads();
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[v][k] += s_c[4 * warp + v][32 * k + lane];
+    } else if (VQ) {
+      __syncwarp();
+#pragma unroll 16
+      for (int j = 0; j < kHeadDim; ++j) {
+        float sj[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sj[k] = __ldg(p.S + j * kHeadDim + 32 * k + lane);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float x = s_z[4 * warp + v][j];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[v][k] = fmaf(sj[k], x, acc[v][k]);
+        }
+      }
+      __syncwarp();
+    }
+    const float* sg = p.signs + hk * p.signs_stride;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      fwht(acc[v], lane);
+      const int row = row0 + v;
+      if (row >= r.count) continue;
+      const float f = l[v] > 0.f ? (BF16 ? kCodeScale : 1.f) / (kHeadDim * l[v]) : (l[v] == 0.f ? 0.f : l[v]);
+      const size_t at = ((size_t)(r.start + r.first + row / p.group) * p.Hq + hk * p.group + row % p.group) * kHeadDim;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        acc[v][k] = fmaf(f, o[32 * k + lane], acc[v][k]);
-        if (VQ) accz[v][k] = fmaf(f, o[kHeadDim + 32 * k + lane], accz[v][k]);
+        const float x = acc[v][k] * f * sg[32 * k + lane];
+        if (BF16) static_cast<__nv_bfloat16*>(p.out)[at + 32 * k + lane] = __float2bfloat16_rn(x);
+        else static_cast<float*>(p.out)[at + 32 * k + lane] = x;
       }
     }
   }
-  if (VQ) {  // acc += kappa S^T accz
-    const float zs = kKappa * (p.bf16 ? kSketchScale / kCodeScale : 1.f);
-#pragma unroll
-    for (int v = 0; v < 4; ++v)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) s_z[VQ ? 4 * warp + v : 0][32 * k + lane] = accz[v][k] * zs;
-    __syncwarp();
-#pragma unroll 4
-    for (int j = 0; j < kHeadDim; ++j) {
-      float sj[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) sj[k] = __ldg(p.S + j * kHeadDim + 32 * k + lane);
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const float x = s_z[VQ ? 4 * warp + v : 0][j];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) acc[v][k] = fmaf(sj[k], x, acc[v][k]);
-      }
-    }
-  }
-  const float* sg = p.signs + hk * p.signs_stride;
-#pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    fwht(acc[v], lane);
-    const int row = row0 + v;
-    if (row >= r.count) continue;
-    const float f = l[v] > 0.f ? (p.bf16 ? kCodeScale : 1.f) / (kHeadDim * l[v]) : (l[v] == 0.f ? 0.f : l[v]);
-    const size_t at = ((size_t)(r.start + r.first + row / p.group) * p.Hq + hk * p.group + row % p.group) * kHeadDim;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float x = acc[v][k] * f * sg[32 * k + lane];
-      if (p.bf16) static_cast<__nv_bfloat16*>(p.out)[at + 32 * k + lane] = __float2bfloat16_rn(x);
-      else static_cast<float*>(p.out)[at + 32 * k + lane] = x;
-    }
-  }
+}
+
+// Blocks that take groups of rows in turn: as many as fit at once, so that a block's fragments of the sketch
+// matrix serve many groups.
+constexpr long long kGroupBlocks = 148 * 3;
+
+template <bool KQ, bool BF16>
+cudaError_t launch_prep(const ChunkParams& p, cudaStream_t s) {
+  const long long groups = ((long long)p.n_tokens * p.Hq + kPrepRows - 1) / kPrepRows;
+  chunk_prep<KQ, BF16><<<1 + (unsigned)std::min(groups, kGroupBlocks), kPrepThreads, 0, s>>>(p);
+  return launched();
+}
+template <bool VQ, bool BF16>
+cudaError_t launch_merge(const ChunkParams& p, cudaStream_t s) {
+  const long long groups = (long long)p.max_tiles * p.Hkv * (p.rows / kMergeRows);
+  chunk_merge<VQ, BF16><<<(unsigned)std::min(groups, kGroupBlocks), kMergeThreads, 0, s>>>(p);
+  return launched();
 }
 
 template <bool KQ, bool VQ>
@@ -520,20 +613,16 @@ ChunkLayout chunk_layout(int n_tokens, int batch, int Hq, int Hkv, bool k_qjl, b
 }
 
 cudaError_t launch_chunk_attention(const ChunkParams& p, cudaStream_t s) {
-  const long long rows = (long long)p.n_tokens * p.Hq;
-  const unsigned prep = 1 + (unsigned)((rows + kPrepRows - 1) / kPrepRows);
-  if (p.k.qjl) chunk_prep<true><<<prep, kPrepThreads, 0, s>>>(p);
-  else chunk_prep<false><<<prep, kPrepThreads, 0, s>>>(p);
-  cudaError_t e = launched();
+  cudaError_t e;
+  if (p.bf16) e = p.k.qjl ? launch_prep<true, true>(p, s) : launch_prep<false, true>(p, s);
+  else e = p.k.qjl ? launch_prep<true, false>(p, s) : launch_prep<false, false>(p, s);
   if (e != cudaSuccess) return e;
   if (p.bf16) e = launch_chunk_umma(p, s);
   else if (p.k.qjl) e = p.v.qjl ? launch_f32<true, true>(p, s) : launch_f32<true, false>(p, s);
   else e = p.v.qjl ? launch_f32<false, true>(p, s) : launch_f32<false, false>(p, s);
   if (e != cudaSuccess) return e;
-  const unsigned merge = (unsigned)((size_t)p.max_tiles * p.Hkv * (p.rows / kMergeRows));
-  if (p.v.qjl) chunk_merge<true><<<merge, kMergeThreads, 0, s>>>(p);
-  else chunk_merge<false><<<merge, kMergeThreads, 0, s>>>(p);
-  return launched();
+  if (p.bf16) return p.v.qjl ? launch_merge<true, true>(p, s) : launch_merge<false, true>(p, s);
+  return p.v.qjl ? launch_merge<true, false>(p, s) : launch_merge<false, false>(p, s);
 }
 
 }  // namespace kvq

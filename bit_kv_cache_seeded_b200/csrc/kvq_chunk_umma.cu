@@ -9,8 +9,8 @@
 // queries and the merge carry their inverses. NT row tiles share a page's dequantisation: two where tensor
 // memory holds their sums (O takes 2 x 128 columns, S 2 x 2 x 64), one with a value sketch (O 256).
 //
-// Warps: 4 per row tile for the softmax (thread = row), 4 that dequantise keys (and fetch the queries of a
-// segment), 4 for values, 2 that issue the products (S, and P V one page behind; one thread issues an MMA
+// Warps: 4 per row tile for the softmax (thread = row), 4 or 8 that dequantise keys (and fetch the queries of
+// a segment), 4 or 8 for values, 2 that issue the products (S, and P V one page behind; one thread issues an MMA
 // about every 50 cycles, so the two kinds run on two warps). K and V pages are staged twice, S twice per
 // tile, so that dequantisation, S, softmax and P V of neighbouring pages overlap. P overwrites the first
 // 32 columns of its S.
@@ -45,7 +45,9 @@ template <bool KQ, bool VQ>
 struct Cfg {
   static constexpr int NT = VQ ? 1 : 2;
   static constexpr int DK = KQ ? 256 : 128, DV = VQ ? 256 : 128;
-  static constexpr int kWarpK = 4 * NT, kWarpV = kWarpK + 4, kWarpS = kWarpV + 4, kWarpO = kWarpS + 1;
+  // groups of 4 warps that dequantise a side, page n on group n % G: two where a sketch doubles the work
+  static constexpr int KG = KQ ? 2 : 1, VG = VQ ? 2 : 1;
+  static constexpr int kWarpK = 4 * NT, kWarpV = kWarpK + 4 * KG, kWarpS = kWarpV + 4 * VG, kWarpO = kWarpS + 1;
   static constexpr int kThreads = 32 * (kWarpO + 1);
   static constexpr int kQTile = kTileRows * DK * 2, kKStage = kPage * DK * 2, kVStage = kPage * DV * 2;
   static constexpr int kOffK = NT * kQTile, kOffV = kOffK + kStages * kKStage, kOffEnd = kOffV + kStages * kVStage;
@@ -205,6 +207,20 @@ __device__ __forceinline__ void expand_bits(int bits, const PageRegs& r, uint32_
 
 __device__ __forceinline__ int segment_pages(const Walk& w) { return max(0, min(w.k1, (w.rows.limit + kPage - 1) / kPage) - w.k0); }
 
+// A page's block-table entry (loaded a page before it is looked at: looking waits for the load), and its
+// first tile, page 0's for an entry that names none (kvq_tiles.cuh).
+__device__ __forceinline__ int page_entry(const ChunkParams& p, const Walk& w, int page) {
+  return p.table && page < p.pages_per_seq ? __ldcg(p.table + (long)w.rows.b * p.pages_per_seq + page) : 0;
+}
+__device__ __forceinline__ long page_tile(const ChunkParams& p, const Walk& w, int page, int entry) {
+  if (!p.table) return ((long)w.rows.b * p.Hkv + w.hk) * p.tiles_per_seq + 2 * page;
+  if (entry < 0 || entry >= p.n_pages) {
+    atomicOr(p.err, kStatusBadPage);
+    entry = 0;
+  }
+  return ((long)entry * p.Hkv + w.hk) * 2;
+}
+
 template <bool KQ, bool VQ>
 __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __grid_constant__ ChunkParams p) {
   using C = Cfg<KQ, VQ>;
@@ -225,7 +241,7 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
         mbar_init(smem_addr(&bars.pready[t][b]), 128);
         mbar_init(smem_addr(&bars.pvdone[t][b]), 1);
       }
-    mbar_init(smem_addr(&bars.qfull), 128);
+    mbar_init(smem_addr(&bars.qfull), 128 * C::KG);
     mbar_init(smem_addr(&bars.qempty), 1);
     mbar_init(smem_addr(&bars.done[0]), 1);
     mbar_init(smem_addr(&bars.done[1]), 1);
@@ -260,7 +276,8 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
       const int np = segment_pages(w);
       const bool used = t * kTileRows < r.count && np > 0;
       const bool work = warp * 32 < r.count;
-      const int last = row < r.count ? min(r.pos0 + row / p.group, r.ctx - 1) : -1;
+      // rows of no token count as unmasked: what they compute is not kept, and the others' mask may still be empty
+      const int last = row < r.count ? min(r.pos0 + row / p.group, r.ctx - 1) : 0x7fffffff;
       float qs = 1.f;
       if (row < r.count)
         qs = p.qscale[(size_t)(r.start + r.first + row / p.group) * p.Hq + w.hk * p.group + row % p.group];
@@ -364,7 +381,7 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
       tc::fence_before();
     }
   } else if (warp < C::kWarpV) {  // ---- keys, and the queries of each segment
-    const int th = tid - 32 * C::kWarpK;
+    const int all = tid - 32 * C::kWarpK, th = all & 127, grp = all >> 7;
     const bool octet = p.k.order == kOrderOctet;
     // octet order: tokens 8 o .. + 7, coordinates of words 2 g, 2 g + 1; token order: token th / 2, half a row
     const int o = th >> 4, g = th & 15;
@@ -375,9 +392,6 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
     const uint32_t row_off = octet ? (g >> 3) * (kPage * 128) + o * 1024 : (th & 1) * (kPage * 128) + tok * 128;
     uint32_t lo, hi;
     code_halves(p.k, lo, hi);
-    auto find = [&](int page) {
-      return tile_index_read(p.table, p.pages_per_seq, p.n_pages, p.tiles_per_seq, p.Hkv, w.rows.b, w.hk, 2 * page, p.err);
-    };
     auto fetch = [&](PageRegs& r, long ti) {
       load_page<KQ>(r, p.k, reinterpret_cast<const unsigned char*>(p.kreg) + (size_t)(ti + tile) * p.k.tile_bytes, off8, slot);
     };
@@ -387,14 +401,15 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
       const Rows r = w.rows;
       const int np = segment_pages(w);
       if (np == 0) continue;
-      fetch(regs, find(w.k0));
-      long index = np > 1 ? find(w.k0 + 1) : 0;  // of the page after the one in regs
+      const int first = (grp + C::KG - n % C::KG) % C::KG;  // this group's first page of the segment
+      if (first < np) fetch(regs, page_tile(p, w, w.k0 + first, page_entry(p, w, w.k0 + first)));
+      int entry = page_entry(p, w, w.k0 + first + C::KG);  // of the page after the one in regs
       if (seg > 0) wait(bars.qempty, (seg - 1) & 1);
       ++seg;
       constexpr int kChunks = DK / 8;
       const size_t qrow0 = (size_t)(r.start + r.first) * p.Hq + w.hk * p.group;
 #pragma unroll 8
-      for (int i = th; i < NT * kTileRows * kChunks; i += 128) {
+      for (int i = all; i < NT * kTileRows * kChunks; i += 128 * C::KG) {
         const int row = i / kChunks, ch = i % kChunks;
         uint4 v = make_uint4(0, 0, 0, 0);
         if (row < r.count)
@@ -406,13 +421,15 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
       }
       fence_proxy_async();
       mbar_arrive(smem_addr(&bars.qfull));
-      for (int j = 0; j < np; ++j, ++n) {
-        const int st = n % kStages;
-        if (n >= kStages) wait(bars.kempty[st], (n / kStages - 1) & 1);
+      for (int j = first; j < np; j += C::KG) {
+        const int nj = n + j, st = nj % kStages;
+        if (nj >= kStages) wait(bars.kempty[st], (nj / kStages - 1) & 1);
         const uint32_t base = sm + C::kOffK + st * C::kKStage;
         const PageRegs cur = regs;
-        if (j + 1 < np) fetch(regs, index);
-        if (j + 2 < np) index = find(w.k0 + j + 2);
+        if (j + C::KG < np) {
+          fetch(regs, page_tile(p, w, w.k0 + j + C::KG, entry));
+          entry = page_entry(p, w, w.k0 + j + 2 * C::KG);
+        }
         uint32_t nn[4] = {cur.norm.x, cur.norm.y, cur.norm.z, cur.norm.w}, ng[4] = {};
         if (KQ) {
           const uint32_t gg[4] = {cur.gamma.x, cur.gamma.y, cur.gamma.z, cur.gamma.w};
@@ -433,15 +450,13 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
         fence_proxy_async();
         mbar_arrive(smem_addr(&bars.kfull[st]));
       }
+      n += np;
     }
   } else if (warp < C::kWarpS) {  // ---- values: dims 8 k .. + 7 of tokens 8 c .. + 7
-    const int th = tid - 32 * C::kWarpV;
+    const int th = (tid - 32 * C::kWarpV) & 127, grp = (tid - 32 * C::kWarpV) >> 7;
     const int c = th & 7, k = th >> 3;
     uint32_t lo, hi;
     code_halves(p.v, lo, hi);
-    auto find = [&](int page) {
-      return tile_index_read(p.table, p.pages_per_seq, p.n_pages, p.tiles_per_seq, p.Hkv, w.rows.b, w.hk, 2 * page, p.err);
-    };
     auto fetch = [&](PageRegs& r, long ti) {
       load_page<VQ>(r, p.v, reinterpret_cast<const unsigned char*>(p.vreg) + (size_t)(ti + (c >> 2)) * p.v.tile_bytes,
                     k * kTile + 8 * (c & 3), 8 * (c & 3));
@@ -451,15 +466,18 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
     while (w.next(p)) {
       const int np = segment_pages(w);
       if (np == 0) continue;
-      fetch(regs, find(w.k0));
-      long index = np > 1 ? find(w.k0 + 1) : 0;  // of the page after the one in regs
-      for (int j = 0; j < np; ++j, ++n) {
-        const int st = n % kStages;
-        if (n >= kStages) wait(bars.vempty[st], (n / kStages - 1) & 1);
+      const int first = (grp + C::VG - n % C::VG) % C::VG;  // this group's first page of the segment
+      if (first < np) fetch(regs, page_tile(p, w, w.k0 + first, page_entry(p, w, w.k0 + first)));
+      int entry = page_entry(p, w, w.k0 + first + C::VG);  // of the page after the one in regs
+      for (int j = first; j < np; j += C::VG) {
+        const int nj = n + j, st = nj % kStages;
+        if (nj >= kStages) wait(bars.vempty[st], (nj / kStages - 1) & 1);
         const PageRegs cur = regs;
         const int tokens = w.rows.limit - (w.k0 + j) * kPage - 8 * c;  // of this thread's 8
-        if (j + 1 < np) fetch(regs, index);
-        if (j + 2 < np) index = find(w.k0 + j + 2);
+        if (j + C::VG < np) {
+          fetch(regs, page_tile(p, w, w.k0 + j + C::VG, entry));
+          entry = page_entry(p, w, w.k0 + j + 2 * C::VG);
+        }
         uint32_t nn[4], ng[4], bad = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -481,6 +499,7 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
         fence_proxy_async();
         mbar_arrive(smem_addr(&bars.vfull[st]));
       }
+      n += np;
     }
   } else if (warp == C::kWarpS) {  // ---- S = Q K^T
     if (lane == 0) {
