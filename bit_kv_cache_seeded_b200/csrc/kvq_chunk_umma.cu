@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
   constexpr int NT = C::NT, DK = C::DK, DV = C::DV;
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ __align__(8) Bars<NT> bars;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_addr(&bars.kfull[i]), 128);
@@ -501,68 +501,62 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
       }
       n += np;
     }
-  } else if (warp == C::kWarpS) {  // ---- S = Q K^T
-    if (lane == 0) {
-      constexpr uint32_t id = tc::idesc_f16(0, 0, 0, kTileRows, kPage);
-      int n = 0, seg = 0, nt[NT] = {};
-      while (w.next(p)) {
-        const int np = segment_pages(w);
-        if (np == 0) continue;
-        wait(bars.qfull, seg & 1);
-        ++seg;
-        for (int j = 0; j < np; ++j, ++n) {
-          const int st = n % kStages;
-          wait(bars.kfull[st], (n / kStages) & 1);
-          const uint64_t kd = desc_sw128(sm + C::kOffK + st * C::kKStage);
+  } else if (warp == C::kWarpS) {  // ---- S = Q K^T (the whole warp, so that control stays uniform)
+    constexpr uint32_t id = tc::idesc_f16(0, 0, 0, kTileRows, kPage);
+    int n = 0, seg = 0, nt[NT] = {};
+    while (w.next(p)) {
+      const int np = __shfl_sync(0xffffffffu, segment_pages(w), 0), count = __shfl_sync(0xffffffffu, w.rows.count, 0);
+      if (np == 0) continue;
+      wait(bars.qfull, seg & 1);
+      ++seg;
+      for (int j = 0; j < np; ++j, ++n) {
+        const int st = n % kStages;
+        wait(bars.kfull[st], (n / kStages) & 1);
+        const uint64_t kd = desc_sw128(sm + C::kOffK + st * C::kKStage);
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            if (t * kTileRows >= w.rows.count) continue;
-            const int b = nt[t] & 1;
-            if (nt[t] >= 2) wait(bars.pvdone[t][b], ((nt[t] >> 1) - 1) & 1);  // P of two pages before is read
-            tc::fence_after();
-            const uint64_t qd = desc_sw128(sm + t * C::kQTile);
+        for (int t = 0; t < NT; ++t) {
+          if (t * kTileRows >= count) continue;
+          const int b = nt[t] & 1;
+          if (nt[t] >= 2) wait(bars.pvdone[t][b], ((nt[t] >> 1) - 1) & 1);  // P of two pages before is read
+          tc::fence_after();
+          const uint64_t qd = desc_sw128(sm + t * C::kQTile);
 #pragma unroll
-            for (int i = 0; i < DK / 16; ++i)
-              tc::umma_f16(tmem + kColS + t * 128 + b * 64, qd + (((i >> 2) * (kTileRows * 128) + (i & 3) * 32) >> 4),
-                           kd + (((i >> 2) * (kPage * 128) + (i & 3) * 32) >> 4), id, i > 0);
-            tc::commit(smem_addr(&bars.sfull[t][b]));
-            ++nt[t];
-          }
-          tc::commit(smem_addr(&bars.kempty[st]));
+          for (int i = 0; i < DK / 64; ++i)
+            tc::umma_f16_x4(tmem + kColS + t * 128 + b * 64, qd + ((i * kTileRows * 128) >> 4), kd + ((i * kPage * 128) >> 4), id,
+                            i > 0);
+          tc::commit_elected(smem_addr(&bars.sfull[t][b]));
+          ++nt[t];
         }
-        tc::commit(smem_addr(&bars.qempty));
+        tc::commit_elected(smem_addr(&bars.kempty[st]));
       }
-      tc::commit(smem_addr(&bars.done[0]));
-      mbar_wait(smem_addr(&bars.done[0]), 0, p.wait_limit);
+      tc::commit_elected(smem_addr(&bars.qempty));
     }
+    tc::commit_elected(smem_addr(&bars.done[0]));
+    mbar_wait(smem_addr(&bars.done[0]), 0, p.wait_limit);
   } else {  // ---- O += P V
-    if (lane == 0) {
-      constexpr uint32_t id = tc::idesc_f16(0, 0, 0, kTileRows, DV);
-      int n = 0, nt[NT] = {};
-      while (w.next(p)) {
-        const int np = segment_pages(w);
-        for (int j = 0; j < np; ++j, ++n) {
-          const int st = n % kStages;
-          wait(bars.vfull[st], (n / kStages) & 1);
-          const uint64_t vd = desc_sw128(sm + C::kOffV + st * C::kVStage);
+    constexpr uint32_t id = tc::idesc_f16(0, 0, 0, kTileRows, DV);
+    int n = 0, nt[NT] = {};
+    while (w.next(p)) {
+      const int np = __shfl_sync(0xffffffffu, segment_pages(w), 0), count = __shfl_sync(0xffffffffu, w.rows.count, 0);
+      for (int j = 0; j < np; ++j, ++n) {
+        const int st = n % kStages;
+        wait(bars.vfull[st], (n / kStages) & 1);
+        const uint64_t vd = desc_sw128(sm + C::kOffV + st * C::kVStage);
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            if (t * kTileRows >= w.rows.count) continue;
-            const int b = nt[t] & 1;
-            wait(bars.pready[t][b], (nt[t] >> 1) & 1);
-            tc::fence_after();
-#pragma unroll
-            for (int i = 0; i < kPage / 16; ++i)
-              tc::umma_f16_ta(tmem + t * DV, tmem + kColS + t * 128 + b * 64 + 8 * i, vd + ((i * 32) >> 4), id, j > 0 || i > 0);
-            tc::commit(smem_addr(&bars.pvdone[t][b]));
-            ++nt[t];
-          }
-          tc::commit(smem_addr(&bars.vempty[st]));
+        for (int t = 0; t < NT; ++t) {
+          if (t * kTileRows >= count) continue;
+          const int b = nt[t] & 1;
+          wait(bars.pready[t][b], (nt[t] >> 1) & 1);
+          tc::fence_after();
+          tc::umma_f16_ta_x4(tmem + t * DV, tmem + kColS + t * 128 + b * 64, vd, id, j > 0);
+          tc::commit_elected(smem_addr(&bars.pvdone[t][b]));
+          ++nt[t];
         }
+        tc::commit_elected(smem_addr(&bars.vempty[st]));
       }
-      tc::commit(smem_addr(&bars.done[1]));
-      mbar_wait(smem_addr(&bars.done[1]), 0, p.wait_limit);
     }
+    tc::commit_elected(smem_addr(&bars.done[1]));
+    mbar_wait(smem_addr(&bars.done[1]), 0, p.wait_limit);
   }
   __syncwarp();
   tc::fence_before();
