@@ -72,6 +72,51 @@ __device__ __forceinline__ float ex2f(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
 }
+// Pairs of fp32 (one issue for two).
+struct F2 {
+  unsigned long long v;
+  __device__ __forceinline__ F2() {}
+  __device__ __forceinline__ F2(float a, float b) { asm("mov.b64 %0, {%1, %2};\n" : "=l"(v) : "f"(a), "f"(b)); }
+  __device__ __forceinline__ void get(float& a, float& b) const { asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(v)); }
+};
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// 2^x on the FMA pipe, for x < 126: x = k + f, k the nearest integer, 2^f by a cubic fitted to |f| <= 1/2 with
+// the least largest relative error (2^-13.7, under the weights' own rounding to fp16, 2^-11). Below 2^-126
+// stays 2^-126; a NaN stays one. The special-function unit makes 4 powers a cycle and quarter of an SM, which
+// bounds the softmax; a quarter of them is made here instead.
+__device__ __forceinline__ F2 ex2_fma(F2 x) {
+  float a, b;
+  x.get(a, b);
+  asm("max.NaN.f32 %0, %0, %1;\n" : "+f"(a) : "f"(-126.f));
+  asm("max.NaN.f32 %0, %0, %1;\n" : "+f"(b) : "f"(-126.f));
+  x = F2(a, b);
+  const F2 t = add(x, F2(12582912.f, 12582912.f));  // 1.5 * 2^23: k in the low bits
+  const F2 f = fma(add(t, F2(-12582912.f, -12582912.f)), F2(-1.f, -1.f), x);
+  F2 y = fma(f, F2(0.0551716648f, 0.0551716648f), F2(0.2426111251f, 0.2426111251f));
+  y = fma(f, y, F2(0.6932609677f, 0.6932609677f));
+  y = fma(f, y, F2(0.9999280572f, 0.9999280572f));
+  t.get(a, b);
+  return mul(y, F2(__int_as_float(__float_as_int(a) * (1 << 23) + 0x3f800000), __int_as_float(__float_as_int(b) * (1 << 23) + 0x3f800000)));
+}
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   const __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -298,15 +343,16 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
               for (int i = 0; i < 32; ++i) s[i] = c + i <= reach ? s[i] : 0xff800000u;
             }
           };
-          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          float mx2[2] = {-INFINITY, -INFINITY};
 #pragma unroll 1
           for (int c = 0; c < kPage; c += 32) {
             uint32_t s[32];
             logits(s, c);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], __uint_as_float(s[i]));
+            for (int i = 0; i < 16; ++i)
+              mx2[i & 1] = max3(mx2[i & 1], __uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
           }
-          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * qs;
+          const float mx = fmaxf(mx2[0], mx2[1]) * qs;
           const bool grow = mx > m + kLag || (m == -INFINITY && mx > m);
           if (__any_sync(0xffffffffu, grow)) {
             const float alpha = grow ? ex2f(m - mx) : 1.f;
@@ -330,22 +376,34 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
               tc::wait_st();
             }
           }
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          F2 sum[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
+          const F2 qs2(qs, qs), ref2(-ref, -ref);
 #pragma unroll 1
           for (int c = 0; c < kPage; c += 32) {
             uint32_t s[32], ph[16];
             logits(s, c);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float a = ex2f(fmaf(__uint_as_float(s[2 * i]), qs, -ref));
-              const float d = ex2f(fmaf(__uint_as_float(s[2 * i + 1]), qs, -ref));
-              sum[i & 3] += a + d;
+              F2 x = fma(F2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), qs2, ref2);
+              float a, d;
+              if ((i & 3) == 3) {
+                x = ex2_fma(x);
+                x.get(a, d);
+              } else {
+                x.get(a, d);
+                a = ex2f(a);
+                d = ex2f(d);
+                x = F2(a, d);
+              }
+              sum[i & 1] = add(sum[i & 1], x);
               const __half2 h = __floats2half2_rn(a, d);
               ph[i] = *reinterpret_cast<const uint32_t*>(&h);
             }
             tc::tmem_st16(tS + 64 * b + c / 2, ph);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          float la, lb;
+          add(sum[0], sum[1]).get(la, lb);
+          l += la + lb;
           wait(bars.vfull[st], ((nv + j) / kStages) & 1);
           const unsigned long long bad = *reinterpret_cast<const volatile unsigned long long*>(bars.vbad[st]);
           if (bad != 0 && reach >= 0 && (bad & (~0ull >> (63 - min(reach, 63)))) != 0) l = NAN;
@@ -363,7 +421,7 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
       if (work) {
         float* ml = segment_ml(p, w.item, blockIdx.x, DV) + 2 * row;
         float* so = segment_o(p, w.item, blockIdx.x, DV) + (size_t)row * DV;
-        if (row < r.count) *reinterpret_cast<float2*>(ml) = make_float2(m == -INFINITY ? m : ref, l);
+        if (row < r.count) *reinterpret_cast<float2*>(ml) = make_float2(m == -INFINITY ? m : ref, m == -INFINITY && l == l ? 0.f : l);
 #pragma unroll 1
         for (int c = 0; c < DV; c += 16) {
           uint32_t o[16];
