@@ -342,22 +342,23 @@ def kvq_decode_step_host(handle, K: torch.Tensor, V: torch.Tensor, q: torch.Tens
 
 # ---- ragged serving path
 
-def _ints(fn: str, dtype, **tensors):
-    """Contiguous CUDA tensors of one integer type on one device, the current one (the calls launch there)."""
-    _on_device(fn, **tensors)
+def _here(fn: str, dtype=None, **tensors):
+    """Contiguous CUDA tensors, of one type if dtype is given, on the current device (the calls launch there).
+    A call of the ragged path takes a few microseconds on the device: one pass over its tensors."""
+    here = -1
     for name, t in tensors.items():
         if t is None:
             continue
-        if t.dtype != dtype:
+        at = t.get_device()
+        if at < 0:
+            raise ValueError(f"{fn}: {name} must be a CUDA tensor")
+        if dtype is not None and t.dtype is not dtype:
             raise TypeError(f"{fn}: {name} must be {dtype}")
         if not t.is_contiguous():
             raise ValueError(f"{fn}: {name} must be contiguous")
-        _current(fn, **{name: t})
-
-
-def _current(fn: str, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device.index != torch.cuda.current_device():
+        if here < 0:
+            here = torch.cuda.current_device()
+        if at != here:
             raise ValueError(f"{fn}: {name} is on {t.device}, not on the current device")
 
 
@@ -367,16 +368,16 @@ def kvq_extend_block_table(held: torch.Tensor, n_new: torch.Tensor, free_pages: 
     pages_per_seq] from free_pages [n_free] (starting at cursor [1]), seq_start [batch + 1], ctx_lens [batch]
     and taken [2] (pages given, requests refused). All int32 CUDA tensors."""
     fn = "kvq_extend_block_table"
-    _ints(fn, torch.int32, held=held, n_new=n_new, free_pages=free_pages, block_table=block_table, seq_start=seq_start,
+    _here(fn, torch.int32, held=held, n_new=n_new, free_pages=free_pages, block_table=block_table, seq_start=seq_start,
           ctx_lens=ctx_lens, taken=taken, cursor=cursor)
-    B = held.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != B or n_new.numel() != B or seq_start.numel() != B + 1 \
+    B, shape = held.numel(), block_table.shape
+    if len(shape) != 2 or shape[0] != B or n_new.numel() != B or seq_start.numel() != B + 1 \
             or ctx_lens.numel() != B or taken.numel() != 2 or (cursor is not None and cursor.numel() != 1):
         raise ValueError(f"{fn}: held, n_new, ctx_lens [batch], seq_start [batch + 1], block_table [batch, pages_per_seq], "
                          "taken [2], cursor [1]")
-    _check(fn, load().kvq_extend_block_table(_ptr(held), _ptr(n_new), B, _ptr(free_pages), free_pages.numel(), _ptr(cursor),
-                                             _ptr(block_table), block_table.shape[1], _ptr(seq_start), _ptr(ctx_lens),
-                                             _ptr(taken), _stream(stream)))
+    _check(fn, load().kvq_extend_block_table(held.data_ptr(), n_new.data_ptr(), B, free_pages.data_ptr(), free_pages.numel(),
+                                             None if cursor is None else cursor.data_ptr(), block_table.data_ptr(), shape[1],
+                                             seq_start.data_ptr(), ctx_lens.data_ptr(), taken.data_ptr(), _stream(stream)))
 
 
 def kvq_slot_map(held: torch.Tensor, seq_start: torch.Tensor, ctx_lens: torch.Tensor, block_table: torch.Tensor, n_pages: int,
@@ -384,31 +385,29 @@ def kvq_slot_map(held: torch.Tensor, seq_start: torch.Tensor, ctx_lens: torch.Te
     """Request, position (int32 [n_tokens], either may be None) and page slot (int64 [n_tokens], -1: none) of
     every new token."""
     fn = "kvq_slot_map"
-    _ints(fn, torch.int32, held=held, seq_start=seq_start, ctx_lens=ctx_lens, block_table=block_table, seq_ids=seq_ids,
+    _here(fn, torch.int32, held=held, seq_start=seq_start, ctx_lens=ctx_lens, block_table=block_table, seq_ids=seq_ids,
           positions=positions)
-    _ints(fn, torch.int64, slots=slots)
-    B, n = held.numel(), slots.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != B or seq_start.numel() != B + 1 or ctx_lens.numel() != B \
-            or any(t is not None and t.numel() != n for t in (seq_ids, positions)):
+    _here(fn, torch.int64, slots=slots)
+    B, n, shape = held.numel(), slots.numel(), block_table.shape
+    if len(shape) != 2 or shape[0] != B or seq_start.numel() != B + 1 or ctx_lens.numel() != B \
+            or (seq_ids is not None and seq_ids.numel() != n) or (positions is not None and positions.numel() != n):
         raise ValueError(f"{fn}: held, ctx_lens [batch], seq_start [batch + 1], block_table [batch, pages_per_seq], "
                          "seq_ids, positions, slots [n_tokens]")
-    _check(fn, load().kvq_slot_map(_ptr(held), _ptr(seq_start), _ptr(ctx_lens), B, _ptr(block_table), block_table.shape[1],
-                                   n_pages, n, _ptr(seq_ids), _ptr(positions), _ptr(slots), _stream(stream)))
+    _check(fn, load().kvq_slot_map(held.data_ptr(), seq_start.data_ptr(), ctx_lens.data_ptr(), B, block_table.data_ptr(),
+                                   shape[1], n_pages, n, None if seq_ids is None else seq_ids.data_ptr(),
+                                   None if positions is None else positions.data_ptr(), slots.data_ptr(), _stream(stream)))
 
 
 def kvq_quantize_slots(handle, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, stream=None):
     """Code K, V [n_tokens, n_kv_heads, head_dim] into page slots int64 [n_tokens] (negative: skipped)."""
     fn = "kvq_quantize_slots"
-    _on_device(fn, K=K, V=V)
-    _ints(fn, torch.int64, slots=slots)
     if K.dtype not in DTYPES or V.dtype != K.dtype:
         raise TypeError("K and V must both be float32 or bfloat16")
-    if not (K.is_contiguous() and V.is_contiguous()):
-        raise ValueError("K and V must be contiguous")
+    _here(fn, K=K, V=V)
+    _here(fn, torch.int64, slots=slots)
     if K.dim() != 3 or K.shape != V.shape or slots.numel() != K.shape[0]:
         raise ValueError("K and V must be [n_tokens, n_kv_heads, head_dim] and slots [n_tokens]")
-    _current(fn, K=K, V=V)
-    _check(fn, load().kvq_quantize_slots(handle, _ptr(K), _ptr(V), DTYPES[K.dtype], _ptr(slots), K.shape[0],
+    _check(fn, load().kvq_quantize_slots(handle, K.data_ptr(), V.data_ptr(), DTYPES[K.dtype], slots.data_ptr(), K.shape[0],
                                          _stream(stream)))
 
 
@@ -434,17 +433,15 @@ def kvq_chunk_attention(handle, q: torch.Tensor, seq_start: torch.Tensor, ctx_le
     seq_start[b + 1] - 1, over the packed cache of ctx_lens [batch] tokens (None: the cache's lengths). out is
     like q."""
     fn = "kvq_chunk_attention"
-    _on_device(fn, q=q, out=out, workspace=workspace)
-    _ints(fn, torch.int32, seq_start=seq_start, ctx_lens=ctx_lens)
     if q.dtype not in DTYPES or out.dtype != q.dtype:
         raise TypeError("q and out must both be float32 or bfloat16")
-    if not (q.is_contiguous() and out.is_contiguous() and workspace.is_contiguous()):
-        raise ValueError("q, out and workspace must be contiguous")
+    _here(fn, q=q, out=out, workspace=workspace)
+    _here(fn, torch.int32, seq_start=seq_start, ctx_lens=ctx_lens)
     if q.dim() != 3 or out.shape != q.shape:
         raise ValueError("q and out must be [n_tokens, n_q_heads, head_dim]")
-    _current(fn, q=q, out=out, workspace=workspace)
-    _check(fn, load().kvq_chunk_attention(handle, _ptr(q), DTYPES[q.dtype], q.shape[0], _ptr(seq_start), _ptr(ctx_lens),
-                                          _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
+    _check(fn, load().kvq_chunk_attention(handle, q.data_ptr(), DTYPES[q.dtype], q.shape[0], seq_start.data_ptr(),
+                                          None if ctx_lens is None else ctx_lens.data_ptr(), out.data_ptr(),
+                                          workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                           _stream(stream)))
 
 
@@ -672,15 +669,17 @@ class KvqCache:
         return out
 
     def _chunk_workspace(self, need, device, stream):
-        stream = torch.cuda.current_stream() if stream is None else stream
-        with torch.cuda.stream(stream):  # memory of that stream: a workspace it outgrows is reused in its order
-            if torch.cuda.is_current_stream_capturing():
-                return torch.empty(need, dtype=torch.uint8, device=device)
-            kept = self.__dict__.setdefault("chunk_workspaces", {})
-            have = kept.get(stream.cuda_stream)
-            if have is None or have.numel() < need:
-                have = kept[stream.cuda_stream] = torch.empty(need, dtype=torch.uint8, device=device)
-            return have
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self._chunk_workspace(need, device, None)
+        # memory of the current stream: a workspace it outgrows is reused in its order
+        if torch.cuda.is_current_stream_capturing():
+            return torch.empty(need, dtype=torch.uint8, device=device)
+        kept, at = self.__dict__.setdefault("chunk_workspaces", {}), torch.cuda.current_stream().cuda_stream
+        have = kept.get(at)
+        if have is None or have.numel() < need:
+            have = kept[at] = torch.empty(need, dtype=torch.uint8, device=device)
+        return have
 
     def lengths(self):
         return kvq_cache_lengths(self.handle, self.batch)

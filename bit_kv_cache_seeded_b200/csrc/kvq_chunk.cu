@@ -478,34 +478,59 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge(const __grid_consta
     if (group0 >= r.count) continue;
     const int c0 = cta_of(hk * units + p.unit_start[tile], T, G);
     const int c1 = cta_of(hk * units + p.unit_start[tile + 1] - 1, T, G);
-    float acc[4][4], accz[4][4], l[4];
+    // the segments' maxima and sums first, a lane per segment; then their rows, four in flight
+    float acc[4][4], accz[4][4], l[4], m[4];
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
+      m[v] = -INFINITY;
       l[v] = 0.f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) acc[v][k] = accz[v][k] = 0.f;
-      const int row = row0 + v;
-      if (row >= r.count) continue;
-      float m = -INFINITY, sum = 0.f;
-      for (int c = c0; c <= c1; ++c) {
-        const float2 s = *reinterpret_cast<const float2*>(segment_ml(p, item, c, DV) + 2 * row);
-        m = fmaxf(m, s.x);
-        sum += s.y;
+    }
+    for (int c = c0 + lane; c <= c1; c += 32) {
+      const float2* ml = reinterpret_cast<const float2*>(segment_ml(p, item, c, DV)) + row0;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        if (row0 + v >= r.count) continue;
+        const float2 s = ml[v];
+        const float top = fmaxf(m[v], s.x);
+        // a NaN sum (a logit that is NaN: the maximum passes over it) stays, an empty part adds nothing
+        l[v] = top == -INFINITY ? l[v] + s.y : l[v] * exp2f(m[v] - top) + s.y * exp2f(s.x - top);
+        m[v] = top;
       }
-      if (m == -INFINITY || sum != sum) {  // nothing attended, or a logit that is NaN (the maximum passes over it)
-        l[v] = sum;
-        continue;
-      }
-      for (int c = c0; c <= c1; ++c) {
-        const float2 s = *reinterpret_cast<const float2*>(segment_ml(p, item, c, DV) + 2 * row);
-        const float* o = segment_o(p, item, c, DV) + (size_t)row * DV;
-        const float f = exp2f(s.x - m);
-        if (f == 0.f) continue;
-        l[v] = fmaf(f, s.y, l[v]);
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      float top = m[v];
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+      l[v] = top == -INFINITY ? l[v] : l[v] * exp2f(m[v] - top);
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) l[v] += __shfl_xor_sync(0xffffffffu, l[v], x);
+      m[v] = top;
+    }
+    for (int c = c0; c <= c1; ++c) {
+      const float2* ml = reinterpret_cast<const float2*>(segment_ml(p, item, c, DV)) + row0;
+      const float* so = segment_o(p, item, c, DV) + (size_t)row0 * DV + lane;
+      float o[4][4], z[4][4], f[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        f[v] = row0 + v < r.count ? ml[v].x : -INFINITY;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          acc[v][k] = fmaf(f, o[32 * k + lane], acc[v][k]);
-          if (VQ) accz[v][k] = fmaf(f, o[kHeadDim + 32 * k + lane], accz[v][k]);
+          o[v][k] = row0 + v < r.count ? so[v * DV + 32 * k] : 0.f;
+          z[v][k] = VQ && row0 + v < r.count ? so[v * DV + kHeadDim + 32 * k] : 0.f;
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        f[v] = m[v] == -INFINITY ? 0.f : exp2f(f[v] - m[v]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {  // a part without weight may hold anything
+          if (f[v] != 0.f) {
+            acc[v][k] = fmaf(f[v], o[v][k], acc[v][k]);
+            if (VQ) accz[v][k] = fmaf(f[v], z[v][k], accz[v][k]);
+          }
         }
       }
     }
@@ -546,7 +571,7 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge(const __grid_consta
       fwht(acc[v], lane);
       const int row = row0 + v;
       if (row >= r.count) continue;
-      const float f = l[v] > 0.f ? (BF16 ? kCodeScale : 1.f) / (kHeadDim * l[v]) : (l[v] == 0.f ? 0.f : l[v]);
+      const float f = l[v] > 0.f ? (BF16 ? kCodeScale : 1.f) / (kHeadDim * l[v]) : l[v];  // 0: nothing attended; or NaN
       const size_t at = ((size_t)(r.start + r.first + row / p.group) * p.Hq + hk * p.group + row % p.group) * kHeadDim;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {

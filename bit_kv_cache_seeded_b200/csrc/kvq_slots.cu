@@ -6,7 +6,7 @@
 // ceil(held_b / 64) to ceil((held_b + new_b) / 64); the new ones come from the free list in request
 // order, at the exclusive prefix sum of the counts. Bound by launch latency: the largest calls move a
 // few hundred KB. So one kernel and no exchange between blocks: every block sums the counts of all
-// requests before its own (batch / 1024 coalesced rounds), then writes its own requests' entries.
+// requests before its own (a coalesced round per 256), then writes its own requests' entries.
 //
 // slot_map. Token t of the ragged batch belongs to the request b with seq_start[b] <= t <
 // seq_start[b + 1] (binary search), has position held_b + t - seq_start[b], and goes to slot
@@ -73,47 +73,54 @@ __device__ __forceinline__ Request request(const int* held, const int* n_new, in
   return r;
 }
 
-// Grid: one block per kTableThreads requests.
+// Grid: one block per kOwn requests, a warp each: one block for 256 requests wrote its 23000 entries in 17.7 us, 32
+// blocks in 5.
+constexpr int kOwn = kTableThreads / 32;
+
 __global__ void __launch_bounds__(kTableThreads)
 extend_block_table(const int* __restrict__ held, const int* __restrict__ n_new, int batch, const int* __restrict__ free_pages,
                    int n_free, const int* __restrict__ cursor, int* __restrict__ table, int pages_per_seq,
                    int* __restrict__ seq_start, int* __restrict__ ctx_lens, int* __restrict__ taken) {
-  __shared__ int s_first[kTableThreads], s_need[kTableThreads], s_p0[kTableThreads];
+  __shared__ int s_first[kOwn], s_need[kOwn], s_p0[kOwn];
   __shared__ int s_sum[2];
   const int tid = threadIdx.x;
-  const int begin = blockIdx.x * kTableThreads;
+  const int begin = blockIdx.x * kOwn;
   const int first = cursor ? *cursor : 0;
   const long long room = first >= 0 && first <= n_free ? n_free - first : -1;  // -1: no page can be given
   long long pages = 0, tokens = 0;  // of the requests before this block's
-  for (int b0 = 0; b0 < begin; b0 += kTableThreads) {
-    const Request r = request(held, n_new, b0 + tid, pages_per_seq);
+  for (int b = tid; b < begin; b += kTableThreads) {
+    const Request r = request(held, n_new, b, pages_per_seq);
     pages += r.need;
     tokens += max(r.n_new, 0);
   }
+  const int b = begin + tid;
+  const bool own = tid < kOwn && b < batch;
+  Request r{0, 0, 0, 0, true};
+  if (own) r = request(held, n_new, b, pages_per_seq);
   long long all_pages, all_tokens, own_pages, own_tokens;
   block_scan(pages, &all_pages);
   block_scan(tokens, &all_tokens);
-  const int b = begin + tid;
-  Request r{0, 0, 0, 0, true};
-  if (b < batch) r = request(held, n_new, b, pages_per_seq);
   const long long end = all_pages + block_scan(r.need, &own_pages);
   const long long tend = all_tokens + block_scan(max(r.n_new, 0), &own_tokens);
   const bool granted = r.valid && (r.need == 0 || end <= room);
   if (tid < 2) s_sum[tid] = 0;
-  s_first[tid] = (int)min(end - r.need, 0x7fffffffll);
-  s_need[tid] = granted ? r.need : 0;
-  s_p0[tid] = r.p0;
+  if (tid < kOwn) {
+    s_first[tid] = (int)min(end - r.need, 0x7fffffffll);
+    s_need[tid] = granted ? r.need : 0;
+    s_p0[tid] = r.p0;
+  }
   __syncthreads();
-  if (b < batch) {
+  if (own) {
     if (b == 0) seq_start[0] = 0;
     seq_start[b + 1] = (int)min(tend, 0x7fffffffll);
     ctx_lens[b] = granted ? r.held + r.n_new : (int)min(max((long long)r.held, 0ll), (long long)pages_per_seq * kPage);
   }
-  // entries: one warp per request
-  for (int i = tid >> 5; i < min(kTableThreads, batch - begin); i += kTableThreads / 32) {
-    const int n = s_need[i];
+  const int i = tid >> 5, n = s_need[i];  // entries: one warp per request
+  if (n > 0) {
     int* row = table + (long long)(begin + i) * pages_per_seq + s_p0[i];
-    for (int k = tid & 31; k < n; k += 32) row[k] = free_pages[first + s_first[i] + k];
+    const int* from = free_pages + first + s_first[i];
+#pragma unroll 8
+    for (int k = tid & 31; k < n; k += 32) row[k] = from[k];
   }
   // totals: the last block sees every request once more
   if (blockIdx.x == gridDim.x - 1) {
@@ -386,7 +393,7 @@ cudaError_t launch_slots(const SlotQuantizeParams& p, cudaStream_t s) {
 cudaError_t launch_extend_block_table(const int* held, const int* n_new, int batch, const int* free_pages, int n_free,
                                       const int* cursor, int* table, int pages_per_seq, int* seq_start, int* ctx_lens,
                                       int* taken, cudaStream_t s) {
-  extend_block_table<<<(batch + kTableThreads - 1) / kTableThreads, kTableThreads, 0, s>>>(
+  extend_block_table<<<(batch + kOwn - 1) / kOwn, kTableThreads, 0, s>>>(
       held, n_new, batch, free_pages, n_free, cursor, table, pages_per_seq, seq_start, ctx_lens, taken);
   return launched();
 }
