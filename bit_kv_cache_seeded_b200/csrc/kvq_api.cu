@@ -461,6 +461,9 @@ kvq_status cache_init(kvq_cache** out, const kvq_cfg* cfg, int32_t batch, int32_
         hS[j * kHeadDim + i] = qjl_matrix[j * kHeadDim + i];
         hSt[(size_t)i * m + j] = qjl_matrix[j * kHeadDim + i];
       }
+    float top = 0.f;
+    for (size_t i = 0; i < m * kHeadDim; ++i) top = std::max(top, std::fabs(hS[i]));
+    c->s_exp = top > 0.f && std::isfinite(top) ? std::min(std::max(std::ilogb(top) - 9, -126), 118) : 0;
     // Synchronous copies: the tables are tiny and this keeps the staging buffer's lifetime
     // trivially safe.
     if (cudaMemcpy(c->d_signs, hs, sizeof(float) * n_signs, cudaMemcpyHostToDevice) != cudaSuccess ||
@@ -1325,6 +1328,7 @@ kvq_status kvq_chunk_attention(const kvq_cache* c, const void* q, kvq_dtype dtyp
   p.signs_stride = c->signs_stride;
   p.S = c->d_S;
   p.St = c->d_St;
+  p.s_exp = c->s_exp;
   p.logit_scale = default_scale(c->cfg) * 1.4426950408889634f;
   p.err = c->d_status;
   p.wait_limit = kWaitLimitCycles;

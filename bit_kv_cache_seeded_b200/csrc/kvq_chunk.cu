@@ -28,7 +28,8 @@ constexpr int kPrepThreads = 256;
 constexpr int kPrepRows = 32;     // query rows of a prep block: 4 per warp
 constexpr float kKappa = lmc::kSqrtHalfPi / kHeadDim;
 
-// Walsh-Hadamard transform of 128 coordinates, lane l holding 32 k + l (k < 4), unnormalised.
+// Walsh-Hadamard transform of 128 coordinates, lane l holding 4 l .. 4 l + 3 (so that a row is read and written
+// 16 or 8 bytes a lane), unnormalised.
 __device__ __forceinline__ void fwht(float (&u)[4], int lane) {
 #pragma unroll
   for (int b = 0; b < 5; ++b) {
@@ -43,42 +44,75 @@ __device__ __forceinline__ void fwht(float (&u)[4], int lane) {
   u[0] = a0 + a2; u[2] = a0 - a2; u[1] = a1 + a3; u[3] = a1 - a3;
 }
 
-// C [32 x 128] = A [32 x 128] . M [128 x 128] on the tensor cores (mma.sync, tf32 operands, fp32 sums) for the
-// bf16 calls' two small products with the sketch matrix: S q~ per query row, S^T z per output row. tf32 rounds by
-// half a step of 2^-11 and keeps fp32's range, so the matrix needs no scaling. Warp w of 8 makes columns 16 w ..
-// + 15 and keeps its fragments of M in registers over the block's row groups. On the CUDA cores the products
-// took 2-3 times the rest of these kernels (prep of 131072 rows 207 us, merge of 55000 rows 110 us).
-constexpr int kPad = kHeadDim + 4;  // row stride of A: lane (g, t) reads bank 4 g + t
-
-struct TfFrags {
-  uint32_t b[2][16][2];
-};
-__device__ __forceinline__ uint32_t tf32(float x) {
-  uint32_t r;
-  asm("cvt.rna.tf32.f32 %0, %1;\n" : "=r"(r) : "f"(x));
-  return r;
+__device__ __forceinline__ void load4(float (&u)[4], const void* row, bool bf16, int lane) {
+  if (bf16) {
+    const uint2 v = *(static_cast<const uint2*>(row) + lane);
+    u[0] = __uint_as_float(v.x << 16);
+    u[1] = __uint_as_float(v.x & 0xffff0000u);
+    u[2] = __uint_as_float(v.y << 16);
+    u[3] = __uint_as_float(v.y & 0xffff0000u);
+  } else {
+    const float4 v = *(static_cast<const float4*>(row) + lane);
+    u[0] = v.x; u[1] = v.y; u[2] = v.z; u[3] = v.w;
+  }
 }
-__device__ __forceinline__ void load_frags(TfFrags& f, const float* M, int warp, int lane) {
+__device__ __forceinline__ void store4(float* row, const float (&u)[4], int lane) {
+  *reinterpret_cast<float4*>(row + 4 * lane) = make_float4(u[0], u[1], u[2], u[3]);
+}
+template <typename T2>
+__device__ __forceinline__ uint2 pack4(T2 a, T2 b) {
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// C [32 x 128] = A [32 x 128] . M [128 x 128] on the tensor cores (mma.sync, fp16 operands, fp32 sums) for the
+// bf16 calls' two small products with the sketch matrix: S q~ per query row, S^T z per output row. A row of A
+// and all of M (its exponent is the cache's) are brought into fp16's range by powers of two; each rounding is half a step, 2^-11. Warp w of 8
+// makes columns 16 w .. + 15 and keeps its fragments of M in registers over the block's row groups. On the CUDA
+// cores the products took half of these kernels' time (prep of 131072 rows 207 us, merge of 55000 rows 110).
+constexpr int kPad = kHeadDim + 4;    // row stride of an fp32 row in shared memory
+constexpr int kPadH = kHeadDim + 8;   // of an fp16 row: the 8 rows that ldmatrix reads at once lie in distinct banks
+
+struct Frags {
+  uint32_t b[2][8][2];
+  float inv;  // 1 / the power of two that M was multiplied by
+};
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+// The power of two that a largest magnitude is divided by to come to [2^9, 2^10): from the exponent's bits, within
+// fp32's normal numbers (infinities and NaN give some power of two, and stay what they are).
+__device__ __forceinline__ int scale_exp(float mx) { return min(max((__float_as_int(mx) >> 23) - 136, -126), 119); }
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+__device__ __forceinline__ void load_frags(Frags& f, const float* M, int e, int warp, int lane) {
+  const float mul = pow2(-e);
+  f.inv = pow2(e);
 #pragma unroll
   for (int n = 0; n < 2; ++n)
 #pragma unroll
-    for (int k = 0; k < 16; ++k)
+    for (int k = 0; k < 8; ++k)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        f.b[n][k][h] = tf32(__ldg(M + (8 * k + (lane & 3) + 4 * h) * kHeadDim + 16 * warp + 8 * n + (lane >> 2)));
+      for (int h = 0; h < 2; ++h) {
+        const float* at = M + (16 * k + 2 * (lane & 3) + 8 * h) * kHeadDim + 16 * warp + 8 * n + (lane >> 2);
+        const __half2 v = __floats2half2_rn(__ldg(at) * mul, __ldg(at + kHeadDim) * mul);
+        f.b[n][k][h] = *reinterpret_cast<const uint32_t*>(&v);
+      }
 }
-__device__ __forceinline__ void tf32_product(const TfFrags& f, const float (*a)[kPad], float (*c)[kPad], int warp, int lane) {
+__device__ __forceinline__ void fp16_product(const Frags& f, const __half (*a)[kPadH], float (*c)[kPad], int warp, int lane) {
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
     float acc[2][4] = {};
+    const uint32_t row = (uint32_t)__cvta_generic_to_shared(&a[16 * m + (lane & 15)][8 * (lane >> 4)]);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const uint32_t a0 = tf32(a[16 * m + g][8 * k + t]), a1 = tf32(a[16 * m + g + 8][8 * k + t]);
-      const uint32_t a2 = tf32(a[16 * m + g][8 * k + t + 4]), a3 = tf32(a[16 * m + g + 8][8 * k + t + 4]);
+    for (int k = 0; k < 8; ++k) {
+      uint32_t a0, a1, a2, a3;
+      asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                   : "=r"(a0), "=r"(a1), "=r"(a2), "=r"(a3) : "r"(row + 32 * k) : "memory");
 #pragma unroll
       for (int n = 0; n < 2; ++n)
-        asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
                      : "+f"(acc[n][0]), "+f"(acc[n][1]), "+f"(acc[n][2]), "+f"(acc[n][3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(f.b[n][k][0]), "r"(f.b[n][k][1]));
     }
@@ -86,8 +120,17 @@ __device__ __forceinline__ void tf32_product(const TfFrags& f, const float (*a)[
     for (int n = 0; n < 2; ++n)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<float2*>(&c[16 * m + g + 8 * h][16 * warp + 8 * n + 2 * t]) = make_float2(acc[n][2 * h], acc[n][2 * h + 1]);
+        *reinterpret_cast<float2*>(&c[16 * m + g + 8 * h][16 * warp + 8 * n + 2 * t]) =
+            make_float2(acc[n][2 * h] * f.inv, acc[n][2 * h + 1] * f.inv);
   }
+}
+// One row of A, scaled by its own power of two, which it returns.
+__device__ __forceinline__ float store_row(__half* a, const float (&u)[4], int lane) {
+  const int e = scale_exp(warp_max(fmaxf(fmaxf(fabsf(u[0]), fabsf(u[1])), fmaxf(fabsf(u[2]), fabsf(u[3])))));
+  const float mul = pow2(-e);
+  *reinterpret_cast<uint2*>(a + 4 * lane) =
+      pack4(__floats2half2_rn(u[0] * mul, u[1] * mul), __floats2half2_rn(u[2] * mul, u[3] * mul));
+  return pow2(e);
 }
 
 // One block's plan of the call: row tiles per request, their units, prefix sums of both.
@@ -158,99 +201,118 @@ __device__ void plan(const ChunkParams& p) {
 // kernel, in its order and with its scales, divided by a power of two (kept in qscale) that brings the row's
 // largest entry to [2^9, 2^10): half a step is 2^-11 of an entry down to 2^-23 of the largest.
 template <bool KQ, bool BF16>
-__global__ void __launch_bounds__(kPrepThreads) chunk_prep(const __grid_constant__ ChunkParams p) {
+__global__ void __launch_bounds__(kPrepThreads, 2) chunk_prep(const __grid_constant__ ChunkParams p) {
   if (blockIdx.x == 0) {
     plan(p);
     return;
   }
-  __shared__ float s_q[kPrepRows][kPad], s_k[KQ && BF16 ? kPrepRows : 1][kPad];
+  __shared__ __align__(16) float s_q[KQ ? kPrepRows : 1][kPad];   // queries, and then (bf16) their sketches
+  __shared__ __align__(16) __half s_a[KQ && BF16 ? kPrepRows : 1][kPadH];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const long long rows = (long long)p.n_tokens * p.Hq;
+  const int rows = p.n_tokens * p.Hq;  // at most 2^30
   constexpr int DK = KQ ? 2 * kHeadDim : kHeadDim;
-  TfFrags frags;
-  if (KQ && BF16) load_frags(frags, p.St, warp, lane);
-  for (long long group = blockIdx.x - 1; group * kPrepRows < rows; group += gridDim.x - 1) {
-    const long long row0 = group * kPrepRows + 4 * warp;
+  Frags frags;
+  if (KQ && BF16) load_frags(frags, p.St, p.s_exp, warp, lane);
+  float next[4][4];  // the next group's queries, loaded a group ahead
+  auto fetch = [&](int group) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int row = group * kPrepRows + 4 * warp + v;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) next[v][k] = 0.f;
+      if (row < rows) load4(next[v], static_cast<const char*>(p.q) + (size_t)row * kHeadDim * (BF16 ? 2 : 4), BF16, lane);
+    }
+  };
+  fetch(blockIdx.x - 1);
+  for (int group = blockIdx.x - 1; group * kPrepRows < rows; group += gridDim.x - 1) {
+    const int row0 = group * kPrepRows + 4 * warp;
+    int head = row0 % p.Hq;
     float rot[4][4], sk[4][4];
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const long long row = row0 + v;
+    for (int v = 0; v < 4; ++v)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        rot[v][k] = row < rows ? qlm::load_elem(p.q, (size_t)row * kHeadDim + 32 * k + lane, BF16) : 0.f;
+        rot[v][k] = next[v][k];
         sk[v][k] = 0.f;
       }
-    }
+    fetch(group + gridDim.x - 1);
+    float back[4];  // powers of two of the product's rows
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const float* sg = p.signs + (int)((row0 + v) % p.Hq) / p.group * p.signs_stride;
+      float sg[4];
+      load4(sg, p.signs + head / p.group * p.signs_stride, false, lane);
+      if (++head == p.Hq) head = 0;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) rot[v][k] *= sg[32 * k + lane];
+      for (int k = 0; k < 4; ++k) rot[v][k] *= sg[k];
       fwht(rot[v], lane);
       // R q * scale / sqrt(d) = H D q * scale / d
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        rot[v][k] *= p.logit_scale * (1.f / kHeadDim);
-        if (KQ) s_q[4 * warp + v][32 * k + lane] = rot[v][k];
-      }
+      for (int k = 0; k < 4; ++k) rot[v][k] *= p.logit_scale * (1.f / kHeadDim);
+      if (KQ && BF16) back[v] = store_row(s_a[4 * warp + v], rot[v], lane);
+      else if (KQ) store4(s_q[4 * warp + v], rot[v], lane);
     }
     if (KQ && BF16) {  // S q~
       __syncthreads();
-      tf32_product(frags, s_q, s_k, warp, lane);
+      fp16_product(frags, s_a, s_q, warp, lane);
       __syncthreads();
 #pragma unroll
-      for (int v = 0; v < 4; ++v)
+      for (int v = 0; v < 4; ++v) {
+        load4(sk[v], s_q[4 * warp + v], false, lane);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) sk[v][k] = s_k[4 * warp + v][32 * k + lane];
-    } else if (KQ) {  // row j = 32 r + lane of S q~, from S^T [i][j]
+        for (int k = 0; k < 4; ++k) sk[v][k] *= back[v];
+      }
+    } else if (KQ) {  // rows j = 4 lane .. + 3 of S q~, from S^T [i][j]
       __syncwarp();
 #pragma unroll 16
       for (int i = 0; i < kHeadDim; ++i) {
-        float st[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) st[r] = __ldg(p.St + i * kHeadDim + 32 * r + lane);
+        const float4 st = __ldg(reinterpret_cast<const float4*>(p.St + i * kHeadDim) + lane);
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const float x = s_q[4 * warp + v][i];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) sk[v][r] = fmaf(st[r], x, sk[v][r]);
+          sk[v][0] = fmaf(st.x, x, sk[v][0]);
+          sk[v][1] = fmaf(st.y, x, sk[v][1]);
+          sk[v][2] = fmaf(st.z, x, sk[v][2]);
+          sk[v][3] = fmaf(st.w, x, sk[v][3]);
         }
       }
       __syncwarp();
     }
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const long long row = row0 + v;
+      const int row = row0 + v;
       if (row >= rows) break;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sk[v][k] *= kKappa;
       if (!BF16) {
         float* dst = static_cast<float*>(p.qprep) + (size_t)row * DK;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          dst[32 * k + lane] = rot[v][k];
-          if (KQ) dst[kHeadDim + 32 * k + lane] = sk[v][k] * kKappa;
-        }
+        store4(dst, rot[v], lane);
+        if (KQ) store4(dst + kHeadDim, sk[v], lane);
         continue;
       }
       float mx = 0.f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         rot[v][k] *= kCodeScale;
-        sk[v][k] *= kKappa * kSketchScale;
+        sk[v][k] *= kSketchScale;
         mx = fmaxf(mx, fmaxf(fabsf(rot[v][k]), fabsf(sk[v][k])));
       }
+      const int e = scale_exp(warp_max(mx));
+      const float inv = pow2(-e);
+      __half* dst = static_cast<__half*>(p.qprep) + (size_t)row * DK + query_pos(p.k.order, lane);
+      if (p.k.order == kOrderOctet) {
+        *reinterpret_cast<uint2*>(dst) = pack4(__floats2half2_rn(rot[v][0] * inv, rot[v][1] * inv),
+                                               __floats2half2_rn(rot[v][2] * inv, rot[v][3] * inv));
+        if (KQ)
+          *reinterpret_cast<uint2*>(dst + kHeadDim) = pack4(__floats2half2_rn(sk[v][0] * inv, sk[v][1] * inv),
+                                                            __floats2half2_rn(sk[v][2] * inv, sk[v][3] * inv));
+      } else {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      int e = 0;
-      if (mx > 0.f && mx < INFINITY) e = min(max(ilogbf(mx) - 9, -126), 126);
-      const float inv = exp2f((float)-e);
-      __half* dst = static_cast<__half*>(p.qprep) + (size_t)row * DK;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int pos = query_pos(p.k.order, k, lane);
-        dst[pos] = __float2half_rn(rot[v][k] * inv);
-        if (KQ) dst[kHeadDim + pos] = __float2half_rn(sk[v][k] * inv);
+        for (int k = 0; k < 4; ++k) {
+          dst[8 * k] = __float2half_rn(rot[v][k] * inv);
+          if (KQ) dst[kHeadDim + 8 * k] = __float2half_rn(sk[v][k] * inv);
+        }
       }
-      if (lane == 0) p.qscale[row] = exp2f((float)e);
+      if (lane == 0) p.qscale[row] = pow2(e);
     }
   }
 }
@@ -455,24 +517,25 @@ __global__ void __launch_bounds__(256) chunk_f32(const __grid_constant__ ChunkPa
 
 // ---- merge --------------------------------------------------------------------------------------------
 //
-// A block merges groups of 32 rows of one item (kv-head, row tile): a warp 4 rows, lane l dims 32 k + l.
+// A block merges groups of 32 rows of one item (kv-head, row tile): a warp 4 rows, lane l dims 4 l .. + 3.
 constexpr int kMergeThreads = 256, kMergeRows = 32;
 
 template <bool VQ, bool BF16>
-__global__ void __launch_bounds__(kMergeThreads) chunk_merge(const __grid_constant__ ChunkParams p) {
+__global__ void __launch_bounds__(kMergeThreads, VQ ? 2 : 3) chunk_merge(const __grid_constant__ ChunkParams p) {
   constexpr int DV = VQ ? 2 * kHeadDim : kHeadDim;
-  __shared__ float s_z[VQ ? kMergeRows : 1][kPad], s_c[VQ && BF16 ? kMergeRows : 1][kPad];
+  __shared__ __align__(16) float s_z[VQ ? kMergeRows : 1][kPad];   // sketch sums; bf16: their products
+  __shared__ __align__(16) __half s_a[VQ && BF16 ? kMergeRows : 1][kPadH];
   const int tiles = (int)p.head[0];
   const int per = p.rows / kMergeRows;
-  const long long items = (long long)tiles * p.Hkv;
+  const int groups = tiles * p.Hkv * per;  // a 32nd of the query rows, and what their tiles leave free
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long units = p.head[1], T = units * p.Hkv, G = cta_count(p, T);
-  TfFrags frags;
-  if (VQ && BF16 && blockIdx.x < items * per) load_frags(frags, p.S, warp, lane);
-  for (long long group = blockIdx.x; group < items * per; group += gridDim.x) {
-    const long long item = group / per;
-    const int hk = (int)(item / tiles), tile = (int)(item % tiles);
-    const int group0 = (int)(group % per) * kMergeRows, row0 = group0 + 4 * warp;
+  Frags frags;
+  if (VQ && BF16 && blockIdx.x < groups) load_frags(frags, p.S, p.s_exp, warp, lane);
+  for (int group = blockIdx.x; group < groups; group += gridDim.x) {
+    const int item = group / per;
+    const int hk = item / tiles, tile = item % tiles;
+    const int group0 = group % per * kMergeRows, row0 = group0 + 4 * warp;
     const int b = p.tile_seq[tile];
     const Rows r = tile_rows(p, b, tile - p.tile_start[b]);
     if (group0 >= r.count) continue;
@@ -511,16 +574,15 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge(const __grid_consta
     }
     for (int c = c0; c <= c1; ++c) {
       const float2* ml = reinterpret_cast<const float2*>(segment_ml(p, item, c, DV)) + row0;
-      const float* so = segment_o(p, item, c, DV) + (size_t)row0 * DV + lane;
+      const float* so = segment_o(p, item, c, DV) + (size_t)row0 * DV;
       float o[4][4], z[4][4], f[4];
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        f[v] = row0 + v < r.count ? ml[v].x : -INFINITY;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          o[v][k] = row0 + v < r.count ? so[v * DV + 32 * k] : 0.f;
-          z[v][k] = VQ && row0 + v < r.count ? so[v * DV + kHeadDim + 32 * k] : 0.f;
-        }
+        f[v] = -INFINITY;
+        if (row0 + v >= r.count) continue;
+        f[v] = ml[v].x;
+        load4(o[v], so + v * DV, false, lane);
+        if (VQ) load4(z[v], so + v * DV + kHeadDim, false, lane);
       }
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
@@ -534,38 +596,45 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge(const __grid_consta
         }
       }
     }
+    float back[4];  // powers of two of the product's rows
     if (VQ) {  // acc += kappa S^T accz
       const float zs = kKappa * (BF16 ? kSketchScale / kCodeScale : 1.f);
 #pragma unroll
-      for (int v = 0; v < 4; ++v)
+      for (int v = 0; v < 4; ++v) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) s_z[4 * warp + v][32 * k + lane] = accz[v][k] * zs;
+        for (int k = 0; k < 4; ++k) accz[v][k] *= zs;
+        if (BF16) back[v] = store_row(s_a[4 * warp + v], accz[v], lane);
+        else store4(s_z[4 * warp + v], accz[v], lane);
+      }
     }
     if (VQ && BF16) {
       __syncthreads();
-      tf32_product(frags, s_z, s_c, warp, lane);
+      fp16_product(frags, s_a, s_z, warp, lane);
       __syncthreads();
 #pragma unroll
-      for (int v = 0; v < 4; ++v)
+      for (int v = 0; v < 4; ++v) {
+        load4(accz[v], s_z[4 * warp + v], false, lane);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) acc[v][k] += s_c[4 * warp + v][32 * k + lane];
+        for (int k = 0; k < 4; ++k) acc[v][k] = fmaf(accz[v][k], back[v], acc[v][k]);
+      }
     } else if (VQ) {
       __syncwarp();
 #pragma unroll 16
       for (int j = 0; j < kHeadDim; ++j) {
-        float sj[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) sj[k] = __ldg(p.S + j * kHeadDim + 32 * k + lane);
+        const float4 sj = __ldg(reinterpret_cast<const float4*>(p.S + j * kHeadDim) + lane);
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const float x = s_z[4 * warp + v][j];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) acc[v][k] = fmaf(sj[k], x, acc[v][k]);
+          acc[v][0] = fmaf(sj.x, x, acc[v][0]);
+          acc[v][1] = fmaf(sj.y, x, acc[v][1]);
+          acc[v][2] = fmaf(sj.z, x, acc[v][2]);
+          acc[v][3] = fmaf(sj.w, x, acc[v][3]);
         }
       }
       __syncwarp();
     }
-    const float* sg = p.signs + hk * p.signs_stride;
+    float sg[4];
+    load4(sg, p.signs + hk * p.signs_stride, false, lane);
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       fwht(acc[v], lane);
@@ -574,29 +643,28 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge(const __grid_consta
       const float f = l[v] > 0.f ? (BF16 ? kCodeScale : 1.f) / (kHeadDim * l[v]) : l[v];  // 0: nothing attended; or NaN
       const size_t at = ((size_t)(r.start + r.first + row / p.group) * p.Hq + hk * p.group + row % p.group) * kHeadDim;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float x = acc[v][k] * f * sg[32 * k + lane];
-        if (BF16) static_cast<__nv_bfloat16*>(p.out)[at + 32 * k + lane] = __float2bfloat16_rn(x);
-        else static_cast<float*>(p.out)[at + 32 * k + lane] = x;
-      }
+      for (int k = 0; k < 4; ++k) acc[v][k] *= f * sg[k];
+      if (BF16)
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at + 4 * lane) =
+            pack4(__floats2bfloat162_rn(acc[v][0], acc[v][1]), __floats2bfloat162_rn(acc[v][2], acc[v][3]));
+      else
+        store4(static_cast<float*>(p.out) + at, acc[v], lane);
     }
   }
 }
 
-// Blocks that take groups of rows in turn: as many as fit at once, so that a block's fragments of the sketch
-// matrix serve many groups.
-constexpr long long kGroupBlocks = 148 * 3;
-
+// Blocks take groups of rows in turn, as many blocks as fit at once (2 or 3 an SM by their registers), so that a
+// block's fragments of the sketch matrix serve many groups.
 template <bool KQ, bool BF16>
 cudaError_t launch_prep(const ChunkParams& p, cudaStream_t s) {
   const long long groups = ((long long)p.n_tokens * p.Hq + kPrepRows - 1) / kPrepRows;
-  chunk_prep<KQ, BF16><<<1 + (unsigned)std::min(groups, kGroupBlocks), kPrepThreads, 0, s>>>(p);
+  chunk_prep<KQ, BF16><<<1 + (unsigned)std::min(groups, 2ll * p.ctas), kPrepThreads, 0, s>>>(p);
   return launched();
 }
 template <bool VQ, bool BF16>
 cudaError_t launch_merge(const ChunkParams& p, cudaStream_t s) {
   const long long groups = (long long)p.max_tiles * p.Hkv * (p.rows / kMergeRows);
-  chunk_merge<VQ, BF16><<<(unsigned)std::min(groups, kGroupBlocks), kMergeThreads, 0, s>>>(p);
+  chunk_merge<VQ, BF16><<<(unsigned)std::min(groups, (VQ ? 2ll : 3ll) * p.ctas), kMergeThreads, 0, s>>>(p);
   return launched();
 }
 

@@ -111,12 +111,11 @@ __device__ __forceinline__ float* segment_o(const ChunkParams& p, long long item
   return segment_ml(p, item, cta, dv) + 2 * p.rows;
 }
 
-// Where the tensor-core kernel keeps coordinate 32 k + lane of a query (or of its sketch), so that the keys'
-// order in a tile need not change (see there).
-__device__ __forceinline__ int query_pos(int order, int k, int lane) {
-  if (order == kOrderOctet) return 32 * ((lane >> 2) & 3) + 8 * k + 4 * (lane >> 4) + (lane & 3);
-  const int byte = 4 * (k & 1) + (lane >> 3);  // of 8 in half a row
-  return 64 * (k >> 1) + 8 * (lane & 7) + byte;
+// Where the tensor-core kernel keeps coordinate 4 lane + k of a query (or of its sketch), so that the keys' order
+// in a tile need not change (see there): the place of k = 0; k is k further in octet order, 8 k in token order.
+__device__ __forceinline__ int query_pos(int order, int lane) {
+  if (order == kOrderOctet) return 32 * (lane & 3) + 8 * (lane >> 3) + 4 * ((lane >> 2) & 1);
+  return 64 * (lane >> 4) + 32 * (lane & 1) + ((lane >> 1) & 7);
 }
 constexpr float kCodeScale = 8.f, kSketchScale = 16.f;  // its operands hold 1/8 of a code, 1/16 of a sketch entry
 

@@ -201,6 +201,7 @@ struct ChunkParams {
   int signs_stride;
   const float* S;
   const float* St;
+  int s_exp;                // S / 2^s_exp is within fp16's range
   float logit_scale;        // softmax_scale * log2(e)
   int* err;
   long long wait_limit;
@@ -318,6 +319,7 @@ struct kvq_cache {
   float* d_signs = nullptr;
   float* d_S = nullptr;
   float* d_St = nullptr;
+  int s_exp = 0;            // power of two that brings S's largest entry to [2^9, 2^10)
   char* d_k = nullptr;
   char* d_v = nullptr;
   size_t k_region = 0, v_region = 0;
