@@ -1333,16 +1333,24 @@ kvq_status kvq_chunk_attention(const kvq_cache* c, const void* q, kvq_dtype dtyp
   p.err = c->d_status;
   p.wait_limit = kWaitLimitCycles;
   char* w = static_cast<char*>(workspace);
-  p.rows = L.rows;
-  p.max_tiles = L.max_tiles;
   p.ctas = L.ctas;
-  p.unit_start = reinterpret_cast<long long*>(w + L.unit_start);
-  p.tile_seq = reinterpret_cast<int*>(w + L.tile_seq);
-  p.tile_start = reinterpret_cast<int*>(w + L.tile_start);
-  p.head = reinterpret_cast<long long*>(w + L.head);
+  p.sets = L.sets;
+  for (int i = 0; i < L.sets; ++i) {
+    const ChunkLayout::Set& from = L.set[i];
+    ChunkSet& to = p.set[i];
+    to.above = from.above;
+    to.upto = from.upto;
+    to.rows = from.rows;
+    to.unit = from.unit;
+    to.max_tiles = from.max_tiles;
+    to.unit_start = reinterpret_cast<long long*>(w + from.unit_start);
+    to.tile_seq = reinterpret_cast<int*>(w + from.tile_seq);
+    to.tile_start = reinterpret_cast<int*>(w + from.tile_start);
+    to.head = reinterpret_cast<long long*>(w + from.head);
+    to.part = reinterpret_cast<float*>(w + from.part);
+  }
   p.qprep = w + L.qprep;
   p.qscale = reinterpret_cast<float*>(w + L.qscale);
-  p.part = reinterpret_cast<float*>(w + L.part);
   return launch_chunk_attention(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 

@@ -133,12 +133,12 @@ __device__ __forceinline__ float store_row(__half* a, const float (&u)[4], int l
   return pow2(e);
 }
 
-// One block's plan of the call: row tiles per request, their units, prefix sums of both.
-__device__ void plan(const ChunkParams& p) {
+// One block's plan of a set: row tiles per request, their units, prefix sums of both.
+__device__ void plan(const ChunkParams& p, const ChunkSet& s) {
   __shared__ long long s_warp[kPrepThreads / 32];
   __shared__ long long s_run;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = p.rows / p.group;
+  const int per = s.rows / p.group;
   auto scan = [&](long long v) {  // exclusive prefix of v over the block, carried in s_run
     long long x = v;
 #pragma unroll
@@ -161,14 +161,15 @@ __device__ void plan(const ChunkParams& p) {
     const int b = b0 + tid;
     int n = 0;
     if (b < p.B) n = max(clamp_start(p, b + 1) - clamp_start(p, b), 0);
+    if (n * p.group <= s.above || n * p.group > s.upto) n = 0;
     const long long at = scan((n + per - 1) / per);
     // max_tiles holds every tile of a seq_start that does not decrease; another one is cut there
-    if (b < p.B) p.tile_start[b] = (int)min(at, (long long)p.max_tiles);
+    if (b < p.B) s.tile_start[b] = (int)min(at, (long long)s.max_tiles);
   }
-  const int tiles = (int)min(s_run, (long long)p.max_tiles);
+  const int tiles = (int)min(s_run, (long long)s.max_tiles);
   __syncthreads();
   if (tid == 0) {
-    p.tile_start[p.B] = tiles;
+    s.tile_start[p.B] = tiles;
     s_run = 0;
   }
   __syncthreads();
@@ -179,33 +180,34 @@ __device__ void plan(const ChunkParams& p) {
       int lo = 0, hi = p.B;  // the last request with tile_start <= t
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (p.tile_start[mid] <= t) lo = mid;
+        if (s.tile_start[mid] <= t) lo = mid;
         else hi = mid;
       }
-      p.tile_seq[t] = lo;
-      const Rows r = tile_rows(p, lo, t - p.tile_start[lo]);
-      units = max(1, (r.limit + kPage - 1) / kPage);
+      s.tile_seq[t] = lo;
+      const Rows r = tile_rows(p, s, lo, t - s.tile_start[lo]);
+      units = max(1, (r.limit + s.unit - 1) / s.unit);
     }
     const long long at = scan(units);
-    if (t < tiles) p.unit_start[t] = at;
+    if (t < tiles) s.unit_start[t] = at;
   }
   if (tid == 0) {
-    p.unit_start[tiles] = s_run;
-    p.head[0] = tiles;
-    p.head[1] = s_run;
+    s.unit_start[tiles] = s_run;
+    s.head[0] = tiles;
+    s.head[1] = s_run;
   }
 }
 
-// Block 0 plans; the others rotate (and sketch) kPrepRows query rows each, the logit scale and 1/sqrt(d) of
+// The first blocks plan, one a set; the others rotate (and sketch) kPrepRows query rows each, the logit scale and 1/sqrt(d) of
 // the keys folded in. fp32 queries: rows of fp32 [d (+ m)]. bf16 queries: rows of fp16 for the tensor-core
 // kernel, in its order and with its scales, divided by a power of two (kept in qscale) that brings the row's
 // largest entry to [2^9, 2^10): half a step is 2^-11 of an entry down to 2^-23 of the largest.
 template <bool KQ, bool BF16>
 __global__ void __launch_bounds__(kPrepThreads, 2) chunk_prep(const __grid_constant__ ChunkParams p) {
-  if (blockIdx.x == 0) {
-    plan(p);
+  if (blockIdx.x < p.sets) {
+    plan(p, p.set[blockIdx.x]);
     return;
   }
+  const int block = blockIdx.x - p.sets, blocks = gridDim.x - p.sets;
   __shared__ __align__(16) float s_q[KQ ? kPrepRows : 1][kPad];   // queries, and then (bf16) their sketches
   __shared__ __align__(16) __half s_a[KQ && BF16 ? kPrepRows : 1][kPadH];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -223,8 +225,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2) chunk_prep(const __grid_const
       if (row < rows) load4(next[v], static_cast<const char*>(p.q) + (size_t)row * kHeadDim * (BF16 ? 2 : 4), BF16, lane);
     }
   };
-  fetch(blockIdx.x - 1);
-  for (int group = blockIdx.x - 1; group * kPrepRows < rows; group += gridDim.x - 1) {
+  fetch(block);
+  for (int group = block; group * kPrepRows < rows; group += blocks) {
     const int row0 = group * kPrepRows + 4 * warp;
     int head = row0 % p.Hq;
     float rot[4][4], sk[4][4];
@@ -235,7 +237,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) chunk_prep(const __grid_const
         rot[v][k] = next[v][k];
         sk[v][k] = 0.f;
       }
-    fetch(group + gridDim.x - 1);
+    fetch(group + blocks);
     float back[4];  // powers of two of the product's rows
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
@@ -394,9 +396,10 @@ __global__ void __launch_bounds__(256) chunk_f32(const __grid_constant__ ChunkPa
   extern __shared__ __align__(16) unsigned char smem[];
   Smem& sm = *reinterpret_cast<Smem*>(smem);
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  const ChunkSet& set = p.set[kWide];
   Walk w;
-  w.init(p, blockIdx.x);
-  while (w.next(p)) {
+  w.init(p, set, blockIdx.x);
+  while (w.next(p, set)) {
     const Rows r = w.rows;
     const size_t qrow0 = (size_t)(r.start + r.first) * p.Hq + w.hk * p.group;
     __syncthreads();
@@ -502,8 +505,8 @@ __global__ void __launch_bounds__(256) chunk_f32(const __grid_constant__ ChunkPa
         }
       }
     }
-    float* ml = segment_ml(p, w.item, blockIdx.x, DV);
-    float* so = segment_o(p, w.item, blockIdx.x, DV);
+    float* ml = segment_ml(set, w.item, blockIdx.x, DV);
+    float* so = segment_o(set, w.item, blockIdx.x, DV);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int row = 4 * ty + i;
@@ -525,22 +528,27 @@ __global__ void __launch_bounds__(kMergeThreads, VQ ? 2 : 3) chunk_merge(const _
   constexpr int DV = VQ ? 2 * kHeadDim : kHeadDim;
   __shared__ __align__(16) float s_z[VQ ? kMergeRows : 1][kPad];   // sketch sums; bf16: their products
   __shared__ __align__(16) __half s_a[VQ && BF16 ? kMergeRows : 1][kPadH];
-  const int tiles = (int)p.head[0];
-  const int per = p.rows / kMergeRows;
-  const int groups = tiles * p.Hkv * per;  // a 32nd of the query rows, and what their tiles leave free
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long units = p.head[1], T = units * p.Hkv, G = cta_count(p, T);
+  int groups = 0, first[2];  // groups of both sets, one after the other
+  for (int i = 0; i < p.sets; ++i) {
+    first[i] = groups;
+    groups += (int)p.set[i].head[0] * p.Hkv * (p.set[i].rows / kMergeRows);
+  }
   Frags frags;
   if (VQ && BF16 && blockIdx.x < groups) load_frags(frags, p.S, p.s_exp, warp, lane);
-  for (int group = blockIdx.x; group < groups; group += gridDim.x) {
+  for (int g = blockIdx.x; g < groups; g += gridDim.x) {
+    const int in = p.sets > 1 && g >= first[1];
+    const ChunkSet& set = p.set[in];
+    const int group = g - (in ? first[1] : 0), per = set.rows / kMergeRows, tiles = (int)set.head[0];
+    const long long units = set.head[1], T = units * p.Hkv, G = cta_count(p, T);
     const int item = group / per;
     const int hk = item / tiles, tile = item % tiles;
     const int group0 = group % per * kMergeRows, row0 = group0 + 4 * warp;
-    const int b = p.tile_seq[tile];
-    const Rows r = tile_rows(p, b, tile - p.tile_start[b]);
+    const int b = set.tile_seq[tile];
+    const Rows r = tile_rows(p, set, b, tile - set.tile_start[b]);
     if (group0 >= r.count) continue;
-    const int c0 = cta_of(hk * units + p.unit_start[tile], T, G);
-    const int c1 = cta_of(hk * units + p.unit_start[tile + 1] - 1, T, G);
+    const int c0 = cta_of(hk * units + set.unit_start[tile], T, G);
+    const int c1 = cta_of(hk * units + set.unit_start[tile + 1] - 1, T, G);
     // the segments' maxima and sums first, a lane per segment; then their rows, four in flight
     float acc[4][4], accz[4][4], l[4], m[4];
 #pragma unroll
@@ -551,7 +559,7 @@ __global__ void __launch_bounds__(kMergeThreads, VQ ? 2 : 3) chunk_merge(const _
       for (int k = 0; k < 4; ++k) acc[v][k] = accz[v][k] = 0.f;
     }
     for (int c = c0 + lane; c <= c1; c += 32) {
-      const float2* ml = reinterpret_cast<const float2*>(segment_ml(p, item, c, DV)) + row0;
+      const float2* ml = reinterpret_cast<const float2*>(segment_ml(set, item, c, DV)) + row0;
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         if (row0 + v >= r.count) continue;
@@ -572,9 +580,10 @@ __global__ void __launch_bounds__(kMergeThreads, VQ ? 2 : 3) chunk_merge(const _
       for (int x = 16; x > 0; x >>= 1) l[v] += __shfl_xor_sync(0xffffffffu, l[v], x);
       m[v] = top;
     }
+#pragma unroll 2
     for (int c = c0; c <= c1; ++c) {
-      const float2* ml = reinterpret_cast<const float2*>(segment_ml(p, item, c, DV)) + row0;
-      const float* so = segment_o(p, item, c, DV) + (size_t)row0 * DV;
+      const float2* ml = reinterpret_cast<const float2*>(segment_ml(set, item, c, DV)) + row0;
+      const float* so = segment_o(set, item, c, DV) + (size_t)row0 * DV;
       float o[4][4], z[4][4], f[4];
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
@@ -658,12 +667,13 @@ __global__ void __launch_bounds__(kMergeThreads, VQ ? 2 : 3) chunk_merge(const _
 template <bool KQ, bool BF16>
 cudaError_t launch_prep(const ChunkParams& p, cudaStream_t s) {
   const long long groups = ((long long)p.n_tokens * p.Hq + kPrepRows - 1) / kPrepRows;
-  chunk_prep<KQ, BF16><<<1 + (unsigned)std::min(groups, 2ll * p.ctas), kPrepThreads, 0, s>>>(p);
+  chunk_prep<KQ, BF16><<<p.sets + (unsigned)std::min(groups, 2ll * p.ctas), kPrepThreads, 0, s>>>(p);
   return launched();
 }
 template <bool VQ, bool BF16>
 cudaError_t launch_merge(const ChunkParams& p, cudaStream_t s) {
-  const long long groups = (long long)p.max_tiles * p.Hkv * (p.rows / kMergeRows);
+  long long groups = 0;
+  for (int i = 0; i < p.sets; ++i) groups += (long long)p.set[i].max_tiles * p.Hkv * (p.set[i].rows / kMergeRows);
   chunk_merge<VQ, BF16><<<(unsigned)std::min(groups, (VQ ? 2ll : 3ll) * p.ctas), kMergeThreads, 0, s>>>(p);
   return launched();
 }
@@ -683,24 +693,36 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 ChunkLayout chunk_layout(int n_tokens, int batch, int Hq, int Hkv, bool k_qjl, bool v_qjl, bool bf16, int sms) {
   ChunkLayout L;
-  L.rows = bf16 ? chunk_umma_rows(v_qjl) : kF32Rows;
-  const int per = L.rows / (Hq / Hkv);
-  L.max_tiles = n_tokens / per + std::min(batch, n_tokens) + 1;
   L.ctas = sms;
-  const size_t rows = (size_t)n_tokens * Hq, segments = (size_t)L.max_tiles * Hkv + L.ctas;
+  L.sets = bf16 ? 2 : 1;
+  const int group = Hq / Hkv;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
     off = up256(off + bytes);
     return at;
   };
-  L.head = take(2 * sizeof(long long));
-  L.unit_start = take(sizeof(long long) * ((size_t)L.max_tiles + 1));
-  L.tile_seq = take(sizeof(int) * (size_t)L.max_tiles);
-  L.tile_start = take(sizeof(int) * ((size_t)batch + 1));
+  for (int i = 0; i < L.sets; ++i) {
+    ChunkLayout::Set& s = L.set[i];
+    // up to kNarrowRows rows of a kv-head: the narrow kernel (bf16)
+    s.above = bf16 && i == kWide ? kNarrowRows : 0;
+    s.upto = i == kNarrow ? kNarrowRows : 0x7fffffff;
+    s.rows = i == kNarrow ? kNarrowRows : bf16 ? chunk_umma_rows(v_qjl) : kF32Rows;
+    s.unit = i == kNarrow ? 2 * kPage : kPage;
+    // requests of a set have above / group + 1 tokens at least, a tile each and one per `rows` rows
+    s.max_tiles = std::min(batch, n_tokens / (s.above / group + 1));
+    if (i == kWide) s.max_tiles += n_tokens / (s.rows / group);
+    if (n_tokens * (long long)group <= s.above) s.max_tiles = 0;
+    s.head = take(2 * sizeof(long long));
+    s.unit_start = take(sizeof(long long) * ((size_t)s.max_tiles + 1));
+    s.tile_seq = take(sizeof(int) * (size_t)s.max_tiles);
+    s.tile_start = take(sizeof(int) * ((size_t)batch + 1));
+    const size_t segments = s.max_tiles ? (size_t)s.max_tiles * Hkv + L.ctas : 0;
+    s.part = take(sizeof(float) * segments * s.rows * (2 + kHeadDim * (v_qjl ? 2 : 1)));
+  }
+  const size_t rows = (size_t)n_tokens * Hq;
   L.qprep = take(rows * kHeadDim * (k_qjl ? 2 : 1) * (bf16 ? sizeof(__half) : sizeof(float)));
   L.qscale = take(bf16 ? sizeof(float) * rows : 0);
-  L.part = take(sizeof(float) * segments * L.rows * (2 + kHeadDim * (v_qjl ? 2 : 1)));
   L.total = off;
   return L;
 }
@@ -710,9 +732,13 @@ cudaError_t launch_chunk_attention(const ChunkParams& p, cudaStream_t s) {
   if (p.bf16) e = p.k.qjl ? launch_prep<true, true>(p, s) : launch_prep<false, true>(p, s);
   else e = p.k.qjl ? launch_prep<true, false>(p, s) : launch_prep<false, false>(p, s);
   if (e != cudaSuccess) return e;
-  if (p.bf16) e = launch_chunk_umma(p, s);
-  else if (p.k.qjl) e = p.v.qjl ? launch_f32<true, true>(p, s) : launch_f32<true, false>(p, s);
-  else e = p.v.qjl ? launch_f32<false, true>(p, s) : launch_f32<false, false>(p, s);
+  if (p.bf16) {
+    e = p.set[kWide].max_tiles ? launch_chunk_umma(p, s) : cudaSuccess;
+    if (e == cudaSuccess) e = launch_chunk_narrow(p, s);
+  } else if (p.k.qjl) e = p.v.qjl ? launch_f32<true, true>(p, s) : launch_f32<true, false>(p, s);
+  else {
+    e = p.v.qjl ? launch_f32<false, true>(p, s) : launch_f32<false, false>(p, s);
+  }
   if (e != cudaSuccess) return e;
   if (p.bf16) return p.v.qjl ? launch_merge<true, true>(p, s) : launch_merge<false, true>(p, s);
   return p.v.qjl ? launch_merge<true, false>(p, s) : launch_merge<false, false>(p, s);

@@ -1,12 +1,12 @@
 // Pieces shared by the chunk attention kernels: the work plan over ragged requests and the states its
 // segments leave behind.
 //
-// Rows. A kv-head of request b has n_b * group query rows, row r = token r / group, head r % group. Row
-// tiles of `rows` rows never cross a request; tile t of a kv-head belongs to request tile_seq[t], the
-// tiles of request b being tile_start[b] .. tile_start[b + 1] - 1.
+// Rows. A kv-head of request b has n_b * group query rows, row r = token r / group, head r % group. A set (ChunkSet)
+// takes the requests whose rows are within its bounds. Row tiles of `rows` rows never cross a request; tile t of a
+// kv-head belongs to request tile_seq[t], the tiles of request b being tile_start[b] .. tile_start[b + 1] - 1.
 //
-// Units. Tile t attends to the positions below its limit, the last row's position + 1, in units of one
-// 64-token page; unit_start[t] is the prefix sum of max(1, ceil(limit / 64)). The units of all kv-heads
+// Units. Tile t attends to the positions below its limit, the last row's position + 1, in units of one or two
+// 64-token pages; unit_start[t] is the prefix sum of max(1, ceil(limit / unit)). The units of all kv-heads
 // lie end to end (kv-head h's from h * head[1]), and CTA c of G = min(CTAs, T) takes the units floor(c T / G)
 // .. floor((c + 1) T / G) - 1 of the T: an even split whatever the lengths, without a host that knows them.
 // A CTA's run of units in one tile is a segment; segment number = item + CTA (item = h * tiles + t) is
@@ -21,7 +21,7 @@
 namespace kvq {
 namespace chunk {
 
-constexpr int kPage = kTile * kTilePair;  // tokens of a unit
+constexpr int kPage = kTile * kTilePair;
 
 struct Rows {        // one row tile
   int b;             // request
@@ -35,12 +35,12 @@ struct Rows {        // one row tile
 
 __device__ __forceinline__ int clamp_start(const ChunkParams& p, int b) { return min(max(p.seq_start[b], 0), p.n_tokens); }
 
-__device__ __forceinline__ Rows tile_rows(const ChunkParams& p, int b, int tile) {
+__device__ __forceinline__ Rows tile_rows(const ChunkParams& p, const ChunkSet& s, int b, int tile) {
   Rows r;
   r.b = b;
   r.start = clamp_start(p, b);
   const int n = max(clamp_start(p, b + 1) - r.start, 0);
-  const int per = p.rows / p.group;  // tokens of a row tile
+  const int per = s.rows / p.group;  // tokens of a row tile
   r.first = tile * per;
   const int tokens = min(per, n - r.first);
   r.count = tokens * p.group;
@@ -62,13 +62,12 @@ struct Walk {
   int tiles, tile, hk;
   // current segment
   long long item;
-  int k0, k1;      // its units within the tile: pages k0 .. k1 - 1
-  int whole;       // the segment is the whole tile
+  int k0, k1;      // its units within the tile: k0 .. k1 - 1
   Rows rows;
 
-  __device__ __forceinline__ void init(const ChunkParams& p, int cta) {
-    tiles = (int)p.head[0];
-    units = p.head[1];
+  __device__ __forceinline__ void init(const ChunkParams& p, const ChunkSet& s, int cta) {
+    tiles = (int)s.head[0];
+    units = s.head[1];
     const long long T = units * p.Hkv;
     const long long G = cta_count(p, T);
     u = cta < G ? cta_first(cta, T, G) : 0;
@@ -78,51 +77,53 @@ struct Walk {
     int lo = 0, hi = tiles;  // the last tile with unit_start <= r
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (p.unit_start[mid] <= r) lo = mid;
+      if (s.unit_start[mid] <= r) lo = mid;
       else hi = mid;
     }
     tile = lo;
   }
-  __device__ __forceinline__ bool next(const ChunkParams& p) {
+  __device__ __forceinline__ bool next(const ChunkParams& p, const ChunkSet& s) {
     if (u >= end) return false;
     if (tile == tiles) {
       tile = 0;
       ++hk;
     }
     const long long base = hk * units;
-    const long long t0 = base + p.unit_start[tile], t1 = base + p.unit_start[tile + 1];
+    const long long t0 = base + s.unit_start[tile], t1 = base + s.unit_start[tile + 1];
     const long long stop = min(t1, end);
     k0 = (int)(u - t0);
     k1 = (int)(stop - t0);
-    whole = u == t0 && stop == t1;
     item = (long long)hk * tiles + tile;
-    const int b = p.tile_seq[tile];
-    rows = tile_rows(p, b, tile - p.tile_start[b]);
+    const int b = s.tile_seq[tile];
+    rows = tile_rows(p, s, b, tile - s.tile_start[b]);
     u = stop;
     if (stop == t1) ++tile;
     return true;
   }
 };
 
-__device__ __forceinline__ float* segment_ml(const ChunkParams& p, long long item, int cta, int dv) {
-  return p.part + (size_t)(item + cta) * p.rows * (2 + dv);
+__device__ __forceinline__ float* segment_ml(const ChunkSet& s, long long item, int cta, int dv) {
+  return s.part + (size_t)(item + cta) * s.rows * (2 + dv);
 }
-__device__ __forceinline__ float* segment_o(const ChunkParams& p, long long item, int cta, int dv) {
-  return segment_ml(p, item, cta, dv) + 2 * p.rows;
+__device__ __forceinline__ float* segment_o(const ChunkSet& s, long long item, int cta, int dv) {
+  return segment_ml(s, item, cta, dv) + 2 * s.rows;
 }
 
-// Where the tensor-core kernel keeps coordinate 4 lane + k of a query (or of its sketch), so that the keys' order
-// in a tile need not change (see there): the place of k = 0; k is k further in octet order, 8 k in token order.
+// Where the tensor-core kernels keep coordinate 4 lane + k of a query (or of its sketch), so that the keys' order
+// in a tile need not change (kvq_chunk_dequant.cuh): the place of k = 0; k is k further in octet order, 8 k in token order.
 __device__ __forceinline__ int query_pos(int order, int lane) {
   if (order == kOrderOctet) return 32 * (lane & 3) + 8 * (lane >> 3) + 4 * ((lane >> 2) & 1);
   return 64 * (lane >> 4) + 32 * (lane & 1) + ((lane >> 1) & 7);
 }
-constexpr float kCodeScale = 8.f, kSketchScale = 16.f;  // its operands hold 1/8 of a code, 1/16 of a sketch entry
+constexpr float kCodeScale = 8.f, kSketchScale = 16.f;  // their operands hold 1/8 of a code, 1/16 of a sketch entry
 
 }  // namespace chunk
 
-// The bf16 path's segment kernel (kvq_chunk_umma.cu), and the query rows of its tile.
+// The bf16 path's segment kernels: kvq_chunk_umma.cu for the wide set (and the query rows of its tile),
+// kvq_chunk_narrow.cu for the narrow one.
 int chunk_umma_rows(bool v_qjl);
 cudaError_t launch_chunk_umma(const ChunkParams& p, cudaStream_t s);
+constexpr int kNarrowRows = 32;
+cudaError_t launch_chunk_narrow(const ChunkParams& p, cudaStream_t s);
 
 }  // namespace kvq

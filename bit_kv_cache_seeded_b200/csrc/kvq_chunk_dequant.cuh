@@ -1,0 +1,263 @@
+// Pieces shared by the tensor-core chunk attention kernels: a packed 64-token page turned into fp16 operand rows
+// in shared memory.
+//
+// Operands lie in shared memory as 128-byte-swizzled K-major rows: row r of an atom of 64 K-elements is 128
+// bytes, its 16-byte chunk c at chunk c ^ (r % 8). A dequantising thread makes 8 elements of a row at a time
+// and stores them as one chunk; 8 neighbouring threads fill 8 different chunks (no bank conflicts). Keys in
+// octet order give a thread coordinates 32 m + 16 h + 4 t + i of 8 tokens; the queries are stored in that
+// order (query_pos), since the product does not mind which way its K-elements are numbered.
+//
+// Entries are n c / 8 (a code times the token's norm) and +-n gamma / 16 (a sign bit): the powers of two keep
+// every fp16 norm's entries in range, and the queries and the merge carry their inverses. A value whose norm is
+// not finite enters as zeros (0 p would be NaN in every row); the rows that attend to it get a NaN sum from the
+// page's mask instead.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "kvq_chunk.cuh"
+
+namespace kvq {
+namespace chunk {
+
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
+         ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t half_bits(float x) { return (uint32_t)__half_as_ushort(__float2half_rn(x)); }
+__device__ __forceinline__ float half_of(uint32_t bits) { return __half2float(__ushort_as_half((unsigned short)bits)); }
+
+// The code words (one per plane) of 32 elements, element (byte i, bit s): prepared once, then the fp16 pairs of
+// bytes 0, 1 and 2, 3 for s = 0 .. 7 in turn, which shifts the words along. Two bits: the code picks one of 4
+// halves. Three: the lower two bits, inverted below zero, pick one of 4 magnitudes. A sign word is rotated so
+// that bit s of bytes 0 and 1 comes to bits 15 and 31 after s steps, that of bytes 2 and 3 eight later.
+__device__ __forceinline__ uint32_t rotr(uint32_t w, int n) { return __funnelshift_r(w, w, n); }
+__device__ __forceinline__ uint32_t sign_word(uint32_t w) { return rotr(__byte_perm(~w, 0, 0x3120), 17); }
+constexpr uint32_t kSigns = 0x80008000u;
+
+template <int BITS>
+struct Codes {
+  uint32_t even, odd, neg;
+  __device__ __forceinline__ void set(uint32_t w0, uint32_t w1, uint32_t w2) {
+    if (BITS == 1) neg = sign_word(w0);
+    if (BITS >= 2) {
+      const uint32_t flip = BITS == 3 ? ~w2 : 0u;
+      const uint32_t a = w0 ^ flip, b = w1 ^ flip;
+      even = (a & 0x55555555u) | ((b & 0x55555555u) << 1);
+      odd = ((a >> 1) & 0x55555555u) | (b & 0xAAAAAAAAu);
+      if (BITS == 3) neg = sign_word(w2);
+    }
+  }
+  // the next s, of parity `parity`; lo, hi: the 4 halves (one bit: lo holds the magnitude twice)
+  __device__ __forceinline__ void next(int parity, uint32_t lo, uint32_t hi, uint32_t& p01, uint32_t& p23) {
+    if (BITS == 1) {
+      p01 = p23 = lo;
+    } else {
+      uint32_t& w = parity ? odd : even;
+      const uint32_t sel = (w & 0x03030303u) * 0x22u + 0x10101010u;
+      w >>= 2;
+      p01 = __byte_perm(lo, hi, sel);
+      p23 = __byte_perm(lo, hi, sel >> 16);
+    }
+    if (BITS != 2) {
+      p01 ^= neg & kSigns;
+      p23 ^= rotr(neg, 8) & kSigns;
+      neg = rotr(neg, 1);
+    }
+  }
+};
+
+__device__ __forceinline__ void code_halves(const SideLayout& L, uint32_t& lo, uint32_t& hi) {
+  if (L.bits == 1) {
+    lo = hi = half_bits(L.cent[1] * 0.125f) * 0x10001u;
+  } else {
+    const int at = L.bits == 3 ? 4 : 0;
+    lo = half_bits(L.cent[at] * 0.125f) | half_bits(L.cent[at + 1] * 0.125f) << 16;
+    hi = half_bits(L.cent[at + 2] * 0.125f) | half_bits(L.cent[at + 3] * 0.125f) << 16;
+  }
+}
+
+// A thread's share of one side's page: 8 bytes of every plane, and 8 tokens' norms (keys in token order: one).
+struct PageRegs {
+  uint2 plane[kMaxBits], sketch;
+  uint4 norm, gamma;
+};
+
+template <bool QJL>
+__device__ __forceinline__ void load_page(PageRegs& r, const SideLayout& L, const unsigned char* tile, int off8, int slot) {
+#pragma unroll
+  for (int p = 0; p < kMaxBits; ++p)
+    r.plane[p] = p >= L.bits ? make_uint2(0, 0) : __ldg(reinterpret_cast<const uint2*>(tile + L.off_planes + p * (kTile * 16) + off8));
+  if (QJL) r.sketch = __ldg(reinterpret_cast<const uint2*>(tile + L.off_sketch + off8));
+  r.norm = __ldg(reinterpret_cast<const uint4*>(tile + L.off_norm + 2 * slot));
+  if (QJL) r.gamma = __ldg(reinterpret_cast<const uint4*>(tile + L.off_gamma + 2 * slot));
+}
+
+__device__ __forceinline__ uint32_t half_at(const uint4& v, int i) {  // i-th of 8
+  const uint32_t w = (i >> 1) == 0 ? v.x : (i >> 1) == 1 ? v.y : (i >> 1) == 2 ? v.z : v.w;
+  return i & 1 ? w >> 16 : w & 0xFFFFu;
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// For s = 0 .. 7 the 8 elements (4 of each word) scaled by a norm, stored as one chunk at d + s * step + 16 (x ^ s),
+// and their signs times the sketch's magnitude sketch_off further. ROWS (keys): s is a token, nn[s / 2] holds
+// its norm in half s % 2, ng the magnitude. Otherwise (values) pair i of tokens has nn[i], ng[i].
+// The loop stays rolled: unrolled, the four roles' code misses the instruction cache (38% of all
+// stalls; a page took 4500 cycles to dequantise).
+template <int BITS, bool QJL, bool ROWS>
+__device__ __forceinline__ void expand(const PageRegs& r, uint32_t lo, uint32_t hi, const uint32_t (&nn)[4], const uint32_t (&ng)[4],
+                                       uint32_t d, int step, uint32_t x, int sketch_off) {
+  Codes<BITS> a, b;
+  a.set(r.plane[0].x, r.plane[1].x, r.plane[2].x);
+  b.set(r.plane[0].y, r.plane[1].y, r.plane[2].y);
+  uint32_t za = QJL ? sign_word(r.sketch.x) : 0u, zb = QJL ? sign_word(r.sketch.y) : 0u;
+  uint32_t n[4] = {nn[0], nn[1], nn[2], nn[3]}, g[4] = {ng[0], ng[1], ng[2], ng[3]};
+#pragma unroll 1
+  for (int q = 0; q < 4; ++q) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t at = d + ((x ^ (2 * q + e)) << 4);
+      uint32_t v[4], m[4], h[4];
+      a.next(e, lo, hi, v[0], v[1]);
+      b.next(e, lo, hi, v[2], v[3]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        m[i] = ROWS ? __byte_perm(n[0], 0, e ? 0x3232 : 0x1010) : n[i];
+        h[i] = ROWS ? __byte_perm(g[0], 0, e ? 0x3232 : 0x1010) : g[i];
+      }
+      sts16(at, mul2(v[0], m[0]), mul2(v[1], m[1]), mul2(v[2], m[2]), mul2(v[3], m[3]));
+      if (QJL) {
+        sts16(at + sketch_off, h[0] ^ (za & kSigns), h[1] ^ (rotr(za, 8) & kSigns), h[2] ^ (zb & kSigns), h[3] ^ (rotr(zb, 8) & kSigns));
+        za = rotr(za, 1);
+        zb = rotr(zb, 1);
+      }
+      d += step;
+    }
+    if (ROWS) {
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        n[i] = n[i + 1];
+        g[i] = g[i + 1];
+      }
+    }
+  }
+}
+
+template <bool QJL, bool ROWS>
+__device__ __forceinline__ void expand_bits(int bits, const PageRegs& r, uint32_t lo, uint32_t hi, const uint32_t (&nn)[4],
+                                            const uint32_t (&ng)[4], uint32_t d, int step, uint32_t x, int sketch_off) {
+  if (bits == 2) expand<2, QJL, ROWS>(r, lo, hi, nn, ng, d, step, x, sketch_off);
+  else if (bits == 3) expand<3, QJL, ROWS>(r, lo, hi, nn, ng, d, step, x, sketch_off);
+  else expand<1, QJL, ROWS>(r, lo, hi, nn, ng, d, step, x, sketch_off);
+}
+
+// One of 128 threads that dequantise the pages of a side's keys: octet order: tokens 8 o .. + 7, coordinates of words
+// 2 g, 2 g + 1; token order: token th / 2, half a row.
+template <bool KQ>
+struct KeyThread {
+  uint32_t lo, hi, row_off, x;
+  int tile, off8, slot, step, tok;
+  bool octet;
+  // atom: bytes of an operand's atom of 64 K-elements
+  __device__ __forceinline__ void init(const ChunkParams& p, int th, int atom) {
+    octet = p.k.order == kOrderOctet;
+    const int o = th >> 4, g = th & 15;
+    tok = th >> 1;
+    tile = octet ? o >> 2 : tok >> 5;
+    off8 = octet ? (o & 3) * 128 + g * 8 : (tok & 31) * 16 + (th & 1) * 8;
+    slot = octet ? 8 * (o & 3) : tok & 24;
+    row_off = octet ? (g >> 3) * atom + o * 1024 : (th & 1) * atom + tok * 128;
+    step = octet ? 128 : 0;
+    x = octet ? g & 7 : tok & 7;
+    code_halves(p.k, lo, hi);
+  }
+  __device__ __forceinline__ void fetch(const ChunkParams& p, PageRegs& r, long ti) const {
+    load_page<KQ>(r, p.k, reinterpret_cast<const unsigned char*>(p.kreg) + (size_t)(ti + tile) * p.k.tile_bytes, off8, slot);
+  }
+  // the page's rows from `base` on (the sketch two atoms behind the codes)
+  __device__ __forceinline__ void store(const ChunkParams& p, const PageRegs& cur, uint32_t base, int atom) const {
+    uint32_t nn[4] = {cur.norm.x, cur.norm.y, cur.norm.z, cur.norm.w}, ng[4] = {};
+    if (KQ) {
+      const uint32_t gg[4] = {cur.gamma.x, cur.gamma.y, cur.gamma.z, cur.gamma.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ng[i] = mul2(mul2(nn[i], 0x2C002C00u), gg[i]);  // n / 16 * gamma
+    }
+    if (!octet) {  // one token
+      const uint32_t nt = half_at(cur.norm, tok & 7) * 0x10001u;
+      const uint32_t gt = KQ ? half_at(make_uint4(ng[0], ng[1], ng[2], ng[3]), tok & 7) * 0x10001u : 0u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        nn[i] = nt;
+        ng[i] = gt;
+      }
+    }
+    expand_bits<KQ, true>(p.k.bits, cur, lo, hi, nn, ng, base + row_off, step, x, 2 * atom);
+  }
+};
+
+// One of 128 threads that dequantise values: rows are dims, 8 k .. + 7 of them, of tokens 8 c .. + 7.
+template <bool VQ>
+struct ValueThread {
+  uint32_t lo, hi;
+  int c, k;
+  __device__ __forceinline__ void init(const ChunkParams& p, int th) {
+    c = th & 7;
+    k = th >> 3;
+    code_halves(p.v, lo, hi);
+  }
+  __device__ __forceinline__ void fetch(const ChunkParams& p, PageRegs& r, long ti) const {
+    load_page<VQ>(r, p.v, reinterpret_cast<const unsigned char*>(p.vreg) + (size_t)(ti + (c >> 2)) * p.v.tile_bytes,
+                  k * kTile + 8 * (c & 3), 8 * (c & 3));
+  }
+  // the page's dims from `base` on (the sketch's 128 behind the codes'); tokens from `limit` on enter as zeros.
+  // Returns this thread's 8 tokens whose norms are not finite, a bit each (zeros too).
+  __device__ __forceinline__ uint32_t store(const ChunkParams& p, const PageRegs& cur, uint32_t base, int limit) const {
+    const int tokens = limit - 8 * c;
+    uint32_t nn[4], ng[4], bad = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t nh[2], gh[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        nh[e] = 2 * i + e < tokens ? half_at(cur.norm, 2 * i + e) : 0u;
+        gh[e] = VQ && 2 * i + e < tokens ? half_at(cur.gamma, 2 * i + e) : 0u;
+        if ((nh[e] & 0x7C00u) == 0x7C00u || (gh[e] & 0x7C00u) == 0x7C00u) {
+          bad |= 1u << (2 * i + e);
+          nh[e] = gh[e] = 0u;
+        }
+      }
+      nn[i] = nh[0] | nh[1] << 16;
+      ng[i] = half_bits(half_of(nh[0]) * half_of(gh[0]) * 0.0625f) | half_bits(half_of(nh[1]) * half_of(gh[1]) * 0.0625f) << 16;
+    }
+    expand_bits<VQ, false>(p.v.bits, cur, lo, hi, nn, ng, base + k * 1024, 128, c, kHeadDim * 128);
+    return bad;
+  }
+};
+
+// A page's block-table entry (loaded a page before it is looked at: looking waits for the load), and its
+// first tile, page 0's for an entry that names none (kvq_tiles.cuh).
+__device__ __forceinline__ int page_entry(const ChunkParams& p, const Walk& w, int page) {
+  return p.table && page < p.pages_per_seq ? __ldcg(p.table + (long)w.rows.b * p.pages_per_seq + page) : 0;
+}
+__device__ __forceinline__ long page_tile(const ChunkParams& p, const Walk& w, int page, int entry) {
+  if (!p.table) return ((long)w.rows.b * p.Hkv + w.hk) * p.tiles_per_seq + 2 * page;
+  if (entry < 0 || entry >= p.n_pages) {
+    atomicOr(p.err, kStatusBadPage);
+    entry = 0;
+  }
+  return ((long)entry * p.Hkv + w.hk) * 2;
+}
+
+}  // namespace chunk
+}  // namespace kvq

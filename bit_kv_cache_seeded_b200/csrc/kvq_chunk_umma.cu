@@ -4,9 +4,7 @@
 // A CTA walks its segments page by page (64 tokens). Per page and tile of 128 query rows
 //   S [128 x 64]  = Q [128 x DK] . K^T          (A, B from shared memory; DK = 128, + 128 of the key sketch)
 //   O [128 x DV] += P [128 x 64] . V            (A from tensor memory; DV = 128, + 128 of the value sketch)
-// with K and V dequantised from the packed page into fp16: entries n c / 8 (a code times the token's norm)
-// and +-n gamma / 16 (a sign bit); the powers of two keep every fp16 norm's entries in range, and the
-// queries and the merge carry their inverses. NT row tiles share a page's dequantisation: two where tensor
+// with K and V dequantised from the packed page into fp16 (kvq_chunk_dequant.cuh). NT row tiles share a page's dequantisation: two where tensor
 // memory holds their sums (O takes 2 x 128 columns, S 2 x 2 x 64), one with a value sketch (O 256).
 //
 // Warps: 4 per row tile for the softmax (thread = row), 4 or 8 that dequantise keys (and fetch the queries of
@@ -15,20 +13,10 @@
 // tile, so that dequantisation, S, softmax and P V of neighbouring pages overlap. P overwrites the first
 // 32 columns of its S.
 //
-// Operands lie in shared memory as 128-byte-swizzled K-major rows: row r of an atom of 64 K-elements is 128
-// bytes, its 16-byte chunk c at chunk c ^ (r % 8). A dequantising thread makes 8 elements of a row at a time
-// and stores them as one chunk; 8 neighbouring threads fill 8 different chunks (no bank conflicts). Keys in
-// octet order give a thread coordinates 32 m + 16 h + 4 t + i of 8 tokens; the queries are stored in that
-// order (query_pos), since the product does not mind which way its K-elements are numbered.
-//
 // Softmax weights are p = 2^(x - m + 7), m the row's maximum but for steps under 2^8, by which it may lag
 // before O is rescaled: p stays under 2^15 in fp16, and a weight is dropped only below 2^-31 of the largest.
-// A value whose norm is not finite enters as zeros (0 p would be NaN in every row); the rows that attend
-// to it get a NaN sum from the page's mask instead.
-#include <cuda_fp16.h>
-
 #include "kvq_async.cuh"
-#include "kvq_chunk.cuh"
+#include "kvq_chunk_dequant.cuh"
 #include "kvq_tcgen05.cuh"
 
 namespace kvq {
@@ -63,15 +51,6 @@ struct Bars {
   int fail;
 };
 
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr) {
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
-         ((uint64_t)2 << 61);
-}
-__device__ __forceinline__ float ex2f(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-  return y;
-}
 // Pairs of fp32 (one issue for two).
 struct F2 {
   unsigned long long v;
@@ -117,154 +96,7 @@ __device__ __forceinline__ F2 ex2_fma(F2 x) {
   t.get(a, b);
   return mul(y, F2(__int_as_float(__float_as_int(a) * (1 << 23) + 0x3f800000), __int_as_float(__float_as_int(b) * (1 << 23) + 0x3f800000)));
 }
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
-  const __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t half_bits(float x) { return (uint32_t)__half_as_ushort(__float2half_rn(x)); }
-__device__ __forceinline__ float half_of(uint32_t bits) { return __half2float(__ushort_as_half((unsigned short)bits)); }
-
-// The code words (one per plane) of 32 elements, element (byte i, bit s): prepared once, then the fp16 pairs of
-// bytes 0, 1 and 2, 3 for s = 0 .. 7 in turn, which shifts the words along. Two bits: the code picks one of 4
-// halves. Three: the lower two bits, inverted below zero, pick one of 4 magnitudes. A sign word is rotated so
-// that bit s of bytes 0 and 1 comes to bits 15 and 31 after s steps, that of bytes 2 and 3 eight later.
-__device__ __forceinline__ uint32_t rotr(uint32_t w, int n) { return __funnelshift_r(w, w, n); }
-__device__ __forceinline__ uint32_t sign_word(uint32_t w) { return rotr(__byte_perm(~w, 0, 0x3120), 17); }
-constexpr uint32_t kSigns = 0x80008000u;
-
-template <int BITS>
-struct Codes {
-  uint32_t even, odd, neg;
-  __device__ __forceinline__ void set(uint32_t w0, uint32_t w1, uint32_t w2) {
-    if (BITS == 1) neg = sign_word(w0);
-    if (BITS >= 2) {
-      const uint32_t flip = BITS == 3 ? ~w2 : 0u;
-      const uint32_t a = w0 ^ flip, b = w1 ^ flip;
-      even = (a & 0x55555555u) | ((b & 0x55555555u) << 1);
-      odd = ((a >> 1) & 0x55555555u) | (b & 0xAAAAAAAAu);
-      if (BITS == 3) neg = sign_word(w2);
-    }
-  }
-  // the next s, of parity `parity`; lo, hi: the 4 halves (one bit: lo holds the magnitude twice)
-  __device__ __forceinline__ void next(int parity, uint32_t lo, uint32_t hi, uint32_t& p01, uint32_t& p23) {
-    if (BITS == 1) {
-      p01 = p23 = lo;
-    } else {
-      uint32_t& w = parity ? odd : even;
-      const uint32_t sel = (w & 0x03030303u) * 0x22u + 0x10101010u;
-      w >>= 2;
-      p01 = __byte_perm(lo, hi, sel);
-      p23 = __byte_perm(lo, hi, sel >> 16);
-    }
-    if (BITS != 2) {
-      p01 ^= neg & kSigns;
-      p23 ^= rotr(neg, 8) & kSigns;
-      neg = rotr(neg, 1);
-    }
-  }
-};
-
-__device__ __forceinline__ void code_halves(const SideLayout& L, uint32_t& lo, uint32_t& hi) {
-  if (L.bits == 1) {
-    lo = hi = half_bits(L.cent[1] * 0.125f) * 0x10001u;
-  } else {
-    const int at = L.bits == 3 ? 4 : 0;
-    lo = half_bits(L.cent[at] * 0.125f) | half_bits(L.cent[at + 1] * 0.125f) << 16;
-    hi = half_bits(L.cent[at + 2] * 0.125f) | half_bits(L.cent[at + 3] * 0.125f) << 16;
-  }
-}
-
-// A thread's share of one side's page: 8 bytes of every plane, and 8 tokens' norms (keys in token order: one).
-struct PageRegs {
-  uint2 plane[kMaxBits], sketch;
-  uint4 norm, gamma;
-};
-
-template <bool QJL>
-__device__ __forceinline__ void load_page(PageRegs& r, const SideLayout& L, const unsigned char* tile, int off8, int slot) {
-#pragma unroll
-  for (int p = 0; p < kMaxBits; ++p)
-    r.plane[p] = p >= L.bits ? make_uint2(0, 0) : __ldg(reinterpret_cast<const uint2*>(tile + L.off_planes + p * (kTile * 16) + off8));
-  if (QJL) r.sketch = __ldg(reinterpret_cast<const uint2*>(tile + L.off_sketch + off8));
-  r.norm = __ldg(reinterpret_cast<const uint4*>(tile + L.off_norm + 2 * slot));
-  if (QJL) r.gamma = __ldg(reinterpret_cast<const uint4*>(tile + L.off_gamma + 2 * slot));
-}
-
-__device__ __forceinline__ uint32_t half_at(const uint4& v, int i) {  // i-th of 8
-  const uint32_t w = (i >> 1) == 0 ? v.x : (i >> 1) == 1 ? v.y : (i >> 1) == 2 ? v.z : v.w;
-  return i & 1 ? w >> 16 : w & 0xFFFFu;
-}
-__device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-
-// For s = 0 .. 7 the 8 elements (4 of each word) scaled by a norm, stored as one chunk at d + s * step + 16 (x ^ s),
-// and their signs times the sketch's magnitude sketch_off further. ROWS (keys): s is a token, nn[s / 2] holds
-// its norm in half s % 2, ng the magnitude. Otherwise (values) pair i of tokens has nn[i], ng[i].
-// The loop stays rolled: unrolled, the four roles' code misses the instruction cache (38% of all
-// stalls; a page took 4500 cycles to dequantise).
-template <int BITS, bool QJL, bool ROWS>
-__device__ __forceinline__ void expand(const PageRegs& r, uint32_t lo, uint32_t hi, const uint32_t (&nn)[4], const uint32_t (&ng)[4],
-                                       uint32_t d, int step, uint32_t x, int sketch_off) {
-  Codes<BITS> a, b;
-  a.set(r.plane[0].x, r.plane[1].x, r.plane[2].x);
-  b.set(r.plane[0].y, r.plane[1].y, r.plane[2].y);
-  uint32_t za = QJL ? sign_word(r.sketch.x) : 0u, zb = QJL ? sign_word(r.sketch.y) : 0u;
-  uint32_t n[4] = {nn[0], nn[1], nn[2], nn[3]}, g[4] = {ng[0], ng[1], ng[2], ng[3]};
-#pragma unroll 1
-  for (int q = 0; q < 4; ++q) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const uint32_t at = d + ((x ^ (2 * q + e)) << 4);
-      uint32_t v[4], m[4], h[4];
-      a.next(e, lo, hi, v[0], v[1]);
-      b.next(e, lo, hi, v[2], v[3]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        m[i] = ROWS ? __byte_perm(n[0], 0, e ? 0x3232 : 0x1010) : n[i];
-        h[i] = ROWS ? __byte_perm(g[0], 0, e ? 0x3232 : 0x1010) : g[i];
-      }
-      sts16(at, mul2(v[0], m[0]), mul2(v[1], m[1]), mul2(v[2], m[2]), mul2(v[3], m[3]));
-      if (QJL) {
-        sts16(at + sketch_off, h[0] ^ (za & kSigns), h[1] ^ (rotr(za, 8) & kSigns), h[2] ^ (zb & kSigns), h[3] ^ (rotr(zb, 8) & kSigns));
-        za = rotr(za, 1);
-        zb = rotr(zb, 1);
-      }
-      d += step;
-    }
-    if (ROWS) {
-#pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        n[i] = n[i + 1];
-        g[i] = g[i + 1];
-      }
-    }
-  }
-}
-
-template <bool QJL, bool ROWS>
-__device__ __forceinline__ void expand_bits(int bits, const PageRegs& r, uint32_t lo, uint32_t hi, const uint32_t (&nn)[4],
-                                            const uint32_t (&ng)[4], uint32_t d, int step, uint32_t x, int sketch_off) {
-  if (bits == 2) expand<2, QJL, ROWS>(r, lo, hi, nn, ng, d, step, x, sketch_off);
-  else if (bits == 3) expand<3, QJL, ROWS>(r, lo, hi, nn, ng, d, step, x, sketch_off);
-  else expand<1, QJL, ROWS>(r, lo, hi, nn, ng, d, step, x, sketch_off);
-}
-
 __device__ __forceinline__ int segment_pages(const Walk& w) { return max(0, min(w.k1, (w.rows.limit + kPage - 1) / kPage) - w.k0); }
-
-// A page's block-table entry (loaded a page before it is looked at: looking waits for the load), and its
-// first tile, page 0's for an entry that names none (kvq_tiles.cuh).
-__device__ __forceinline__ int page_entry(const ChunkParams& p, const Walk& w, int page) {
-  return p.table && page < p.pages_per_seq ? __ldcg(p.table + (long)w.rows.b * p.pages_per_seq + page) : 0;
-}
-__device__ __forceinline__ long page_tile(const ChunkParams& p, const Walk& w, int page, int entry) {
-  if (!p.table) return ((long)w.rows.b * p.Hkv + w.hk) * p.tiles_per_seq + 2 * page;
-  if (entry < 0 || entry >= p.n_pages) {
-    atomicOr(p.err, kStatusBadPage);
-    entry = 0;
-  }
-  return ((long)entry * p.Hkv + w.hk) * 2;
-}
 
 template <bool KQ, bool VQ>
 __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __grid_constant__ ChunkParams p) {
@@ -272,6 +104,8 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
   constexpr int NT = C::NT, DK = C::DK, DV = C::DV;
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ __align__(8) Bars<NT> bars;
+  const ChunkSet& set = p.set[kWide];
+  if (set.head[1] == 0) return;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -309,14 +143,14 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
     }
   };
   Walk w;
-  w.init(p, blockIdx.x);
+  w.init(p, set, blockIdx.x);
 
   if (warp < C::kWarpK) {  // ---- softmax: thread = row
     const int t = warp >> 2, row = tid;  // row of the NT * 128
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tO = tmem + lanes + t * DV, tS = tmem + lanes + kColS + t * 128;
     int n = 0, nv = 0;  // pages this tile, and the CTA, has seen
-    while (w.next(p)) {
+    while (w.next(p, set)) {
       const Rows r = w.rows;
       const int np = segment_pages(w);
       const bool used = t * kTileRows < r.count && np > 0;
@@ -419,8 +253,8 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
         tc::fence_after();
       }
       if (work) {
-        float* ml = segment_ml(p, w.item, blockIdx.x, DV) + 2 * row;
-        float* so = segment_o(p, w.item, blockIdx.x, DV) + (size_t)row * DV;
+        float* ml = segment_ml(set, w.item, blockIdx.x, DV) + 2 * row;
+        float* so = segment_o(set, w.item, blockIdx.x, DV) + (size_t)row * DV;
         if (row < r.count) *reinterpret_cast<float2*>(ml) = make_float2(m == -INFINITY ? m : ref, m == -INFINITY && l == l ? 0.f : l);
 #pragma unroll 1
         for (int c = 0; c < DV; c += 16) {
@@ -440,27 +274,16 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
     }
   } else if (warp < C::kWarpV) {  // ---- keys, and the queries of each segment
     const int all = tid - 32 * C::kWarpK, th = all & 127, grp = all >> 7;
-    const bool octet = p.k.order == kOrderOctet;
-    // octet order: tokens 8 o .. + 7, coordinates of words 2 g, 2 g + 1; token order: token th / 2, half a row
-    const int o = th >> 4, g = th & 15;
-    const int tok = th >> 1;
-    const int tile = octet ? o >> 2 : tok >> 5;
-    const int off8 = octet ? (o & 3) * 128 + g * 8 : (tok & 31) * 16 + (th & 1) * 8;
-    const int slot = octet ? 8 * (o & 3) : tok & 24;
-    const uint32_t row_off = octet ? (g >> 3) * (kPage * 128) + o * 1024 : (th & 1) * (kPage * 128) + tok * 128;
-    uint32_t lo, hi;
-    code_halves(p.k, lo, hi);
-    auto fetch = [&](PageRegs& r, long ti) {
-      load_page<KQ>(r, p.k, reinterpret_cast<const unsigned char*>(p.kreg) + (size_t)(ti + tile) * p.k.tile_bytes, off8, slot);
-    };
+    KeyThread<KQ> keys;
+    keys.init(p, th, kPage * 128);
     int n = 0, seg = 0;
     PageRegs regs;
-    while (w.next(p)) {
+    while (w.next(p, set)) {
       const Rows r = w.rows;
       const int np = segment_pages(w);
       if (np == 0) continue;
       const int first = (grp + C::KG - n % C::KG) % C::KG;  // this group's first page of the segment
-      if (first < np) fetch(regs, page_tile(p, w, w.k0 + first, page_entry(p, w, w.k0 + first)));
+      if (first < np) keys.fetch(p, regs, page_tile(p, w, w.k0 + first, page_entry(p, w, w.k0 + first)));
       int entry = page_entry(p, w, w.k0 + first + C::KG);  // of the page after the one in regs
       if (seg > 0) wait(bars.qempty, (seg - 1) & 1);
       ++seg;
@@ -485,26 +308,10 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
         const uint32_t base = sm + C::kOffK + st * C::kKStage;
         const PageRegs cur = regs;
         if (j + C::KG < np) {
-          fetch(regs, page_tile(p, w, w.k0 + j + C::KG, entry));
+          keys.fetch(p, regs, page_tile(p, w, w.k0 + j + C::KG, entry));
           entry = page_entry(p, w, w.k0 + j + 2 * C::KG);
         }
-        uint32_t nn[4] = {cur.norm.x, cur.norm.y, cur.norm.z, cur.norm.w}, ng[4] = {};
-        if (KQ) {
-          const uint32_t gg[4] = {cur.gamma.x, cur.gamma.y, cur.gamma.z, cur.gamma.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) ng[i] = mul2(mul2(nn[i], 0x2C002C00u), gg[i]);  // n / 16 * gamma
-        }
-        if (!octet) {  // one token
-          const uint32_t nt = half_at(cur.norm, tok & 7) * 0x10001u;
-          const uint32_t gt = KQ ? half_at(make_uint4(ng[0], ng[1], ng[2], ng[3]), tok & 7) * 0x10001u : 0u;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            nn[i] = nt;
-            ng[i] = gt;
-          }
-        }
-        expand_bits<KQ, true>(p.k.bits, cur, lo, hi, nn, ng, base + row_off, octet ? 128 : 0, octet ? g & 7 : tok & 7,
-                              2 * kPage * 128);
+        keys.store(p, cur, base, kPage * 128);
         fence_proxy_async();
         mbar_arrive(smem_addr(&bars.kfull[st]));
       }
@@ -512,48 +319,27 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
     }
   } else if (warp < C::kWarpS) {  // ---- values: dims 8 k .. + 7 of tokens 8 c .. + 7
     const int th = (tid - 32 * C::kWarpV) & 127, grp = (tid - 32 * C::kWarpV) >> 7;
-    const int c = th & 7, k = th >> 3;
-    uint32_t lo, hi;
-    code_halves(p.v, lo, hi);
-    auto fetch = [&](PageRegs& r, long ti) {
-      load_page<VQ>(r, p.v, reinterpret_cast<const unsigned char*>(p.vreg) + (size_t)(ti + (c >> 2)) * p.v.tile_bytes,
-                    k * kTile + 8 * (c & 3), 8 * (c & 3));
-    };
+    ValueThread<VQ> values;
+    values.init(p, th);
     int n = 0;
     PageRegs regs;
-    while (w.next(p)) {
+    while (w.next(p, set)) {
       const int np = segment_pages(w);
       if (np == 0) continue;
       const int first = (grp + C::VG - n % C::VG) % C::VG;  // this group's first page of the segment
-      if (first < np) fetch(regs, page_tile(p, w, w.k0 + first, page_entry(p, w, w.k0 + first)));
+      if (first < np) values.fetch(p, regs, page_tile(p, w, w.k0 + first, page_entry(p, w, w.k0 + first)));
       int entry = page_entry(p, w, w.k0 + first + C::VG);  // of the page after the one in regs
       for (int j = first; j < np; j += C::VG) {
         const int nj = n + j, st = nj % kStages;
         if (nj >= kStages) wait(bars.vempty[st], (nj / kStages - 1) & 1);
         const PageRegs cur = regs;
-        const int tokens = w.rows.limit - (w.k0 + j) * kPage - 8 * c;  // of this thread's 8
+        const int limit = w.rows.limit - (w.k0 + j) * kPage;
         if (j + C::VG < np) {
-          fetch(regs, page_tile(p, w, w.k0 + j + C::VG, entry));
+          values.fetch(p, regs, page_tile(p, w, w.k0 + j + C::VG, entry));
           entry = page_entry(p, w, w.k0 + j + 2 * C::VG);
         }
-        uint32_t nn[4], ng[4], bad = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t nh[2], gh[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            nh[e] = 2 * i + e < tokens ? half_at(cur.norm, 2 * i + e) : 0u;
-            gh[e] = VQ && 2 * i + e < tokens ? half_at(cur.gamma, 2 * i + e) : 0u;
-            if ((nh[e] & 0x7C00u) == 0x7C00u || (gh[e] & 0x7C00u) == 0x7C00u) {
-              bad |= 1u << (2 * i + e);
-              nh[e] = gh[e] = 0u;
-            }
-          }
-          nn[i] = nh[0] | nh[1] << 16;
-          ng[i] = half_bits(half_of(nh[0]) * half_of(gh[0]) * 0.0625f) | half_bits(half_of(nh[1]) * half_of(gh[1]) * 0.0625f) << 16;
-        }
-        if (k == 0) bars.vbad[st][c] = (unsigned char)bad;
-        expand_bits<VQ, false>(p.v.bits, cur, lo, hi, nn, ng, sm + C::kOffV + st * C::kVStage + k * 1024, 128, c, kHeadDim * 128);
+        const uint32_t bad = values.store(p, cur, sm + C::kOffV + st * C::kVStage, limit);
+        if (th < 8) bars.vbad[st][th] = (unsigned char)bad;
         fence_proxy_async();
         mbar_arrive(smem_addr(&bars.vfull[st]));
       }
@@ -562,7 +348,7 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
   } else if (warp == C::kWarpS) {  // ---- S = Q K^T (the whole warp, so that control stays uniform)
     constexpr uint32_t id = tc::idesc_f16(0, 0, 0, kTileRows, kPage);
     int n = 0, seg = 0, nt[NT] = {};
-    while (w.next(p)) {
+    while (w.next(p, set)) {
       const int np = __shfl_sync(0xffffffffu, segment_pages(w), 0), count = __shfl_sync(0xffffffffu, w.rows.count, 0);
       if (np == 0) continue;
       wait(bars.qfull, seg & 1);
@@ -594,7 +380,7 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
   } else {  // ---- O += P V
     constexpr uint32_t id = tc::idesc_f16(0, 0, 0, kTileRows, DV);
     int n = 0, nt[NT] = {};
-    while (w.next(p)) {
+    while (w.next(p, set)) {
       const int np = __shfl_sync(0xffffffffu, segment_pages(w), 0), count = __shfl_sync(0xffffffffu, w.rows.count, 0);
       for (int j = 0; j < np; ++j, ++n) {
         const int st = n % kStages;

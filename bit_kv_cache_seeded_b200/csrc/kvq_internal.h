@@ -182,7 +182,21 @@ struct SlotQuantizeParams {
   int* err;
 };
 
-// Chunk attention (kvq_chunk.cu): the workspace is laid out by chunk_layout().
+// Chunk attention (kvq_chunk.cu): the workspace is laid out by chunk_layout(). The requests of one set are those
+// whose query rows of a kv-head lie within its bounds; each set has its own plan, segment kernel and states.
+struct ChunkSet {
+  int above, upto;          // rows of a request: above < rows <= upto
+  int rows;                 // query rows of a row tile
+  int unit;                 // tokens of a unit
+  int max_tiles;            // row tiles of one kv-head the workspace holds
+  long long* unit_start;    // [max_tiles + 1]
+  int* tile_seq;            // [max_tiles]
+  int* tile_start;          // [B + 1]
+  long long* head;          // row tiles of a kv-head, units of a kv-head
+  float* part;              // softmax states of the segments
+};
+constexpr int kWide = 0, kNarrow = 1;  // sets (fp32 calls have the first alone)
+
 struct ChunkParams {
   const void* q;            // [n_tokens, Hq, d]
   void* out;                // the same, in q's type
@@ -206,22 +220,21 @@ struct ChunkParams {
   int* err;
   long long wait_limit;
   // workspace
-  int rows;                 // query rows of a row tile
-  int max_tiles;            // row tiles of one kv-head the workspace holds
-  int ctas;                 // CTAs that share the units
-  long long* unit_start;    // [max_tiles + 1]
-  int* tile_seq;            // [max_tiles]
-  int* tile_start;          // [B + 1]
-  long long* head;          // row tiles of a kv-head, units of a kv-head
+  int ctas;                 // CTAs that share a set's units
+  int sets;
+  ChunkSet set[2];
   void* qprep;              // rotated (and sketched) queries
   float* qscale;            // [n_tokens * Hq] (bf16)
-  float* part;              // softmax states of the segments
 };
 
-// Byte offsets of a chunk call's workspace.
+// A chunk call's workspace: its sets with byte offsets in place of the pointers.
 struct ChunkLayout {
-  int rows, max_tiles, ctas;
-  size_t unit_start, tile_seq, tile_start, head, qprep, qscale, part, total;
+  struct Set {
+    int above, upto, rows, unit, max_tiles;
+    size_t unit_start, tile_seq, tile_start, head, part;
+  } set[2];
+  int ctas, sets;
+  size_t qprep, qscale, total;
 };
 
 // Reads cudaGetLastError() right after a kernel launch and, when it is cudaSuccess, adds one to

@@ -52,21 +52,23 @@ __device__ __forceinline__ void umma_f16(uint32_t d_tmem, uint64_t a_desc, uint6
       ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
 
-// Four K steps of 16 at once, for a whole converged warp (one elected lane issues): operands of 16-bit elements
-// in 128-byte swizzled atoms of 64 K-elements, a step 32 bytes on; the later three accumulate. With the issue
-// spread over lane 0's branches and one descriptor move per product, an MMA left every 110-160 cycles.
+// Four K steps of 16 at once, for a whole converged warp (one elected lane issues), operands of 16-bit elements;
+// A and B move on by AS and BS bytes a step (32 in 128-byte swizzled atoms of 64 K-elements). The later three
+// accumulate. With the issue spread over lane 0's branches and one descriptor move per product, an MMA left every
+// 110-160 cycles.
+template <int AS = 32, int BS = 32>
 __device__ __forceinline__ void umma_f16_x4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                             uint32_t accumulate) {
   asm volatile(
       "{\n .reg .pred p, t, e;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n"
       " elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, 0, 0;\n"
-      " add.s64 a1, %1, 2;\n add.s64 a2, %1, 4;\n add.s64 a3, %1, 6;\n"
-      " add.s64 b1, %2, 2;\n add.s64 b2, %2, 4;\n add.s64 b3, %2, 6;\n"
+      " add.s64 a1, %1, %5;\n add.s64 a2, a1, %5;\n add.s64 a3, a2, %5;\n"
+      " add.s64 b1, %2, %6;\n add.s64 b2, b1, %6;\n add.s64 b3, b2, %6;\n"
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n"
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n"
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n}\n"
-      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(AS / 16), "n"(BS / 16) : "memory");
 }
 // The same with A in tensor memory, two elements per column.
 __device__ __forceinline__ void umma_f16_ta_x4(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
