@@ -38,10 +38,10 @@ __device__ __forceinline__ float half_of(uint32_t bits) { return __half2float(__
 
 // The code words (one per plane) of 32 elements, element (byte i, bit s): prepared once, then the fp16 pairs of
 // bytes 0, 1 and 2, 3 for s = 0 .. 7 in turn, which shifts the words along. Two bits: the code picks one of 4
-// halves. Three: the lower two bits, inverted below zero, pick one of 4 magnitudes. A sign word is rotated so
-// that bit s of bytes 0 and 1 comes to bits 15 and 31 after s steps, that of bytes 2 and 3 eight later.
-__device__ __forceinline__ uint32_t rotr(uint32_t w, int n) { return __funnelshift_r(w, w, n); }
-__device__ __forceinline__ uint32_t sign_word(uint32_t w) { return rotr(__byte_perm(~w, 0, 0x3120), 17); }
+// halves. Three: the lower two bits, inverted below zero, pick one of 4 magnitudes. A sign word has bytes 1 and 2
+// exchanged, so that bits s of a pair lie 16 apart; a product with 2^(15 - s) (bytes 0, 1) or 2^(7 - s) (2, 3) takes
+// them to bits 15 and 31. Products rather than shifts: they leave the ALU pipe, which bounds this, to the rest.
+__device__ __forceinline__ uint32_t sign_word(uint32_t w) { return __byte_perm(~w, 0, 0x3120); }
 constexpr uint32_t kSigns = 0x80008000u;
 
 template <int BITS>
@@ -57,8 +57,10 @@ struct Codes {
       if (BITS == 3) neg = sign_word(w2);
     }
   }
-  // the next s, of parity `parity`; lo, hi: the 4 halves (one bit: lo holds the magnitude twice)
-  __device__ __forceinline__ void next(int parity, uint32_t lo, uint32_t hi, uint32_t& p01, uint32_t& p23) {
+  // the next s, of parity `parity`; lo, hi: the 4 halves (one bit: lo holds the magnitude twice); m01 = 2^(15 - s), m23
+  // = 2^(7 - s)
+  __device__ __forceinline__ void next(int parity, uint32_t lo, uint32_t hi, uint32_t m01, uint32_t m23, uint32_t& p01,
+                                       uint32_t& p23) {
     if (BITS == 1) {
       p01 = p23 = lo;
     } else {
@@ -69,9 +71,8 @@ struct Codes {
       p23 = __byte_perm(lo, hi, sel >> 16);
     }
     if (BITS != 2) {
-      p01 ^= neg & kSigns;
-      p23 ^= rotr(neg, 8) & kSigns;
-      neg = rotr(neg, 1);
+      p01 ^= neg * m01 & kSigns;
+      p23 ^= neg * m23 & kSigns;
     }
   }
 };
@@ -121,29 +122,29 @@ __device__ __forceinline__ void expand(const PageRegs& r, uint32_t lo, uint32_t 
   Codes<BITS> a, b;
   a.set(r.plane[0].x, r.plane[1].x, r.plane[2].x);
   b.set(r.plane[0].y, r.plane[1].y, r.plane[2].y);
-  uint32_t za = QJL ? sign_word(r.sketch.x) : 0u, zb = QJL ? sign_word(r.sketch.y) : 0u;
+  const uint32_t za = QJL ? sign_word(r.sketch.x) : 0u, zb = QJL ? sign_word(r.sketch.y) : 0u;
   uint32_t n[4] = {nn[0], nn[1], nn[2], nn[3]}, g[4] = {ng[0], ng[1], ng[2], ng[3]};
+  uint32_t top = 0x8000u, at = d + (x << 4);  // rows are 128 bytes: x ^ s only turns bits of the chunk within one
 #pragma unroll 1
   for (int q = 0; q < 4; ++q) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const uint32_t at = d + ((x ^ (2 * q + e)) << 4);
+      const uint32_t m01 = top >> e, m23 = top >> (8 + e), to = (at ^ (e << 4)) + e * step;
       uint32_t v[4], m[4], h[4];
-      a.next(e, lo, hi, v[0], v[1]);
-      b.next(e, lo, hi, v[2], v[3]);
+      a.next(e, lo, hi, m01, m23, v[0], v[1]);
+      b.next(e, lo, hi, m01, m23, v[2], v[3]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         m[i] = ROWS ? __byte_perm(n[0], 0, e ? 0x3232 : 0x1010) : n[i];
         h[i] = ROWS ? __byte_perm(g[0], 0, e ? 0x3232 : 0x1010) : g[i];
       }
-      sts16(at, mul2(v[0], m[0]), mul2(v[1], m[1]), mul2(v[2], m[2]), mul2(v[3], m[3]));
-      if (QJL) {
-        sts16(at + sketch_off, h[0] ^ (za & kSigns), h[1] ^ (rotr(za, 8) & kSigns), h[2] ^ (zb & kSigns), h[3] ^ (rotr(zb, 8) & kSigns));
-        za = rotr(za, 1);
-        zb = rotr(zb, 1);
-      }
-      d += step;
+      sts16(to, mul2(v[0], m[0]), mul2(v[1], m[1]), mul2(v[2], m[2]), mul2(v[3], m[3]));
+      if (QJL)
+        sts16(to + sketch_off, h[0] ^ (za * m01 & kSigns), h[1] ^ (za * m23 & kSigns), h[2] ^ (zb * m01 & kSigns),
+              h[3] ^ (zb * m23 & kSigns));
     }
+    top >>= 2;
+    at = (at ^ ((q ^ (q + 1)) << 5)) + 2 * step;
     if (ROWS) {
 #pragma unroll
       for (int i = 0; i < 3; ++i) {
@@ -191,7 +192,7 @@ struct KeyThread {
     if (KQ) {
       const uint32_t gg[4] = {cur.gamma.x, cur.gamma.y, cur.gamma.z, cur.gamma.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) ng[i] = mul2(mul2(nn[i], 0x2C002C00u), gg[i]);  // n / 16 * gamma
+      for (int i = 0; i < 4; ++i) ng[i] = mul2(nn[i], mul2(gg[i], 0x2C002C00u));  // n * (gamma / 16)
     }
     if (!octet) {  // one token
       const uint32_t nt = half_at(cur.norm, tok & 7) * 0x10001u;
@@ -224,22 +225,28 @@ struct ValueThread {
   // Returns this thread's 8 tokens whose norms are not finite, a bit each (zeros too).
   __device__ __forceinline__ uint32_t store(const ChunkParams& p, const PageRegs& cur, uint32_t base, int limit) const {
     const int tokens = limit - 8 * c;
-    uint32_t nn[4], ng[4], bad = 0;
+    uint32_t nn[4] = {cur.norm.x, cur.norm.y, cur.norm.z, cur.norm.w}, ng[4] = {}, bad = 0;
+    if (VQ) {
+      ng[0] = cur.gamma.x; ng[1] = cur.gamma.y; ng[2] = cur.gamma.z; ng[3] = cur.gamma.w;
+    }
+    uint32_t odd = 0;  // an exponent of all ones carries into the sign's place
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t nh[2], gh[2];
+    for (int i = 0; i < 4; ++i) odd |= ((nn[i] & 0x7C007C00u) + 0x04000400u) | ((ng[i] & 0x7C007C00u) + 0x04000400u);
+    if ((odd & kSigns) != 0 || tokens < 8) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        nh[e] = 2 * i + e < tokens ? half_at(cur.norm, 2 * i + e) : 0u;
-        gh[e] = VQ && 2 * i + e < tokens ? half_at(cur.gamma, 2 * i + e) : 0u;
-        if ((nh[e] & 0x7C00u) == 0x7C00u || (gh[e] & 0x7C00u) == 0x7C00u) {
-          bad |= 1u << (2 * i + e);
-          nh[e] = gh[e] = 0u;
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t half = i & 1 ? 0xFFFF0000u : 0xFFFFu;
+        const bool in = i < tokens;
+        const bool finite = (((nn[i >> 1] & 0x7C007C00u) + 0x04000400u) | ((ng[i >> 1] & 0x7C007C00u) + 0x04000400u)) & kSigns & half ? false : true;
+        if (in && !finite) bad |= 1u << i;
+        if (!in || !finite) {
+          nn[i >> 1] &= ~half;
+          ng[i >> 1] &= ~half;
         }
       }
-      nn[i] = nh[0] | nh[1] << 16;
-      ng[i] = half_bits(half_of(nh[0]) * half_of(gh[0]) * 0.0625f) | half_bits(half_of(nh[1]) * half_of(gh[1]) * 0.0625f) << 16;
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ng[i] = mul2(nn[i], mul2(ng[i], 0x2C002C00u));  // n * (gamma / 16)
     expand_bits<VQ, false>(p.v.bits, cur, lo, hi, nn, ng, base + k * 1024, 128, c, kHeadDim * 128);
     return bad;
   }
