@@ -15,6 +15,7 @@
 
 #include <cuda_fp16.h>
 
+#include "kvq_async.cuh"
 #include "kvq_chunk.cuh"
 
 namespace kvq {
@@ -32,6 +33,13 @@ __device__ __forceinline__ float ex2f(float x) {
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   const __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
+}
+// The bytes of (lo, hi) that the selector's low four nibbles (each under 8) name: one instruction, where __byte_perm
+// masks a selector that it does not know.
+__device__ __forceinline__ uint32_t pick(uint32_t lo, uint32_t hi, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;\n" : "=r"(r) : "r"(lo), "r"(hi), "r"(sel));
+  return r;
 }
 __device__ __forceinline__ uint32_t half_bits(float x) { return (uint32_t)__half_as_ushort(__float2half_rn(x)); }
 __device__ __forceinline__ float half_of(uint32_t bits) { return __half2float(__ushort_as_half((unsigned short)bits)); }
@@ -67,8 +75,8 @@ struct Codes {
       uint32_t& w = parity ? odd : even;
       const uint32_t sel = (w & 0x03030303u) * 0x22u + 0x10101010u;
       w >>= 2;
-      p01 = __byte_perm(lo, hi, sel);
-      p23 = __byte_perm(lo, hi, sel >> 16);
+      p01 = pick(lo, hi, sel);
+      p23 = pick(lo, hi, sel >> 16);
     }
     if (BITS != 2) {
       p01 ^= neg * m01 & kSigns;
@@ -77,7 +85,9 @@ struct Codes {
   }
 };
 
-__device__ __forceinline__ void code_halves(const SideLayout& L, uint32_t& lo, uint32_t& hi) {
+// A side's codes as halves (Codes::next), eighths of them.
+__device__ __forceinline__ uint2 code_halves(const SideLayout& L) {
+  uint32_t lo, hi;
   if (L.bits == 1) {
     lo = hi = half_bits(L.cent[1] * 0.125f) * 0x10001u;
   } else {
@@ -85,6 +95,7 @@ __device__ __forceinline__ void code_halves(const SideLayout& L, uint32_t& lo, u
     lo = half_bits(L.cent[at] * 0.125f) | half_bits(L.cent[at + 1] * 0.125f) << 16;
     hi = half_bits(L.cent[at + 2] * 0.125f) | half_bits(L.cent[at + 3] * 0.125f) << 16;
   }
+  return make_uint2(lo, hi);
 }
 
 // A thread's share of one side's page: 8 bytes of every plane, and 8 tokens' norms (keys in token order: one).
@@ -93,14 +104,28 @@ struct PageRegs {
   uint4 norm, gamma;
 };
 
+// Loads that stay where they are written: the compiler would move them down to their first use, a page later, and
+// leave their latency in the open.
+__device__ __forceinline__ uint2 load8(const unsigned char* at) {
+  uint2 v;
+  asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "l"(at));
+  return v;
+}
+__device__ __forceinline__ uint4 load16(const unsigned char* at) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(at));
+  return v;
+}
+
 template <bool QJL>
 __device__ __forceinline__ void load_page(PageRegs& r, const SideLayout& L, const unsigned char* tile, int off8, int slot) {
-#pragma unroll
-  for (int p = 0; p < kMaxBits; ++p)
-    r.plane[p] = p >= L.bits ? make_uint2(0, 0) : __ldg(reinterpret_cast<const uint2*>(tile + L.off_planes + p * (kTile * 16) + off8));
-  if (QJL) r.sketch = __ldg(reinterpret_cast<const uint2*>(tile + L.off_sketch + off8));
-  r.norm = __ldg(reinterpret_cast<const uint4*>(tile + L.off_norm + 2 * slot));
-  if (QJL) r.gamma = __ldg(reinterpret_cast<const uint4*>(tile + L.off_gamma + 2 * slot));
+  const unsigned char* planes = tile + L.off_planes + off8;
+  r.plane[0] = load8(planes);
+  if (L.bits > 1) r.plane[1] = load8(planes + kTile * 16);
+  if (L.bits > 2) r.plane[2] = load8(planes + 2 * kTile * 16);
+  if (QJL) r.sketch = load8(tile + L.off_sketch + off8);
+  r.norm = load16(tile + L.off_norm + 2 * slot);
+  if (QJL) r.gamma = load16(tile + L.off_gamma + 2 * slot);
 }
 
 __device__ __forceinline__ uint32_t half_at(const uint4& v, int i) {  // i-th of 8
@@ -111,63 +136,85 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uin
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// For s = 0 .. 7 the 8 elements (4 of each word) scaled by a norm, stored as one chunk at d + s * step + 16 (x ^ s),
-// and their signs times the sketch's magnitude sketch_off further. ROWS (keys): s is a token, nn[s / 2] holds
-// its norm in half s % 2, ng the magnitude. Otherwise (values) pair i of tokens has nn[i], ng[i].
-// The loop stays rolled: unrolled, the four roles' code misses the instruction cache (38% of all
-// stalls; a page took 4500 cycles to dequantise).
-template <int BITS, bool QJL, bool ROWS>
-__device__ __forceinline__ void expand(const PageRegs& r, uint32_t lo, uint32_t hi, const uint32_t (&nn)[4], const uint32_t (&ng)[4],
-                                       uint32_t d, int step, uint32_t x, int sketch_off) {
+// For s = 0 .. 7 the 8 elements (4 of each word) scaled by a norm, stored as one chunk at d + s * step + 16 (x ^ s).
+// ROWS (keys): s is a token, nn[s / 2] holds its norm in half s % 2. Otherwise (values) pair i of tokens has nn[i].
+// The loops stay rolled: unrolled, the roles' code missed the instruction cache (38% of all stalls; a page took
+// 4500 cycles to dequantise).
+template <bool ROWS>
+__device__ __forceinline__ void row_factors(const uint32_t (&n)[4], int e, uint32_t (&m)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m[i] = ROWS ? __byte_perm(n[0], 0, e ? 0x3232 : 0x1010) : n[i];
+}
+template <bool ROWS>
+__device__ __forceinline__ void next_rows(uint32_t (&n)[4]) {
+  if (ROWS) {
+    n[0] = n[1]; n[1] = n[2]; n[2] = n[3];
+  }
+}
+
+template <int BITS, bool ROWS>
+__device__ __forceinline__ void expand_codes(const PageRegs& r, uint2 lut, const uint32_t (&nn)[4], uint32_t d, int step, uint32_t x) {
   Codes<BITS> a, b;
   a.set(r.plane[0].x, r.plane[1].x, r.plane[2].x);
   b.set(r.plane[0].y, r.plane[1].y, r.plane[2].y);
-  const uint32_t za = QJL ? sign_word(r.sketch.x) : 0u, zb = QJL ? sign_word(r.sketch.y) : 0u;
-  uint32_t n[4] = {nn[0], nn[1], nn[2], nn[3]}, g[4] = {ng[0], ng[1], ng[2], ng[3]};
+  uint32_t n[4] = {nn[0], nn[1], nn[2], nn[3]};
   uint32_t top = 0x8000u, at = d + (x << 4);  // rows are 128 bytes: x ^ s only turns bits of the chunk within one
 #pragma unroll 1
   for (int q = 0; q < 4; ++q) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const uint32_t m01 = top >> e, m23 = top >> (8 + e), to = (at ^ (e << 4)) + e * step;
-      uint32_t v[4], m[4], h[4];
-      a.next(e, lo, hi, m01, m23, v[0], v[1]);
-      b.next(e, lo, hi, m01, m23, v[2], v[3]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        m[i] = ROWS ? __byte_perm(n[0], 0, e ? 0x3232 : 0x1010) : n[i];
-        h[i] = ROWS ? __byte_perm(g[0], 0, e ? 0x3232 : 0x1010) : g[i];
-      }
-      sts16(to, mul2(v[0], m[0]), mul2(v[1], m[1]), mul2(v[2], m[2]), mul2(v[3], m[3]));
-      if (QJL)
-        sts16(to + sketch_off, h[0] ^ (za * m01 & kSigns), h[1] ^ (za * m23 & kSigns), h[2] ^ (zb * m01 & kSigns),
-              h[3] ^ (zb * m23 & kSigns));
+      uint32_t v[4], m[4];
+      a.next(e, lut.x, lut.y, top >> e, top >> (8 + e), v[0], v[1]);
+      b.next(e, lut.x, lut.y, top >> e, top >> (8 + e), v[2], v[3]);
+      row_factors<ROWS>(n, e, m);
+      sts16((at ^ (e << 4)) + e * step, mul2(v[0], m[0]), mul2(v[1], m[1]), mul2(v[2], m[2]), mul2(v[3], m[3]));
     }
     top >>= 2;
     at = (at ^ ((q ^ (q + 1)) << 5)) + 2 * step;
-    if (ROWS) {
+    next_rows<ROWS>(n);
+  }
+}
+template <bool ROWS>
+__device__ __forceinline__ void expand_codes(int bits, const PageRegs& r, uint2 lut, const uint32_t (&nn)[4], uint32_t d, int step,
+                                             uint32_t x) {
+  if (bits == 2) expand_codes<2, ROWS>(r, lut, nn, d, step, x);
+  else if (bits == 3) expand_codes<3, ROWS>(r, lut, nn, d, step, x);
+  else expand_codes<1, ROWS>(r, lut, nn, d, step, x);
+}
+// The same of the sketch's signs: +-ng.
+template <bool ROWS>
+__device__ __forceinline__ void expand_signs(const PageRegs& r, const uint32_t (&ng)[4], uint32_t d, int step, uint32_t x) {
+  const uint32_t za = sign_word(r.sketch.x), zb = sign_word(r.sketch.y);
+  uint32_t g[4] = {ng[0], ng[1], ng[2], ng[3]};
+  uint32_t top = 0x8000u, at = d + (x << 4);
+#pragma unroll 1
+  for (int q = 0; q < 4; ++q) {
 #pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        n[i] = n[i + 1];
-        g[i] = g[i + 1];
-      }
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t m01 = top >> e, m23 = top >> (8 + e);
+      uint32_t h[4];
+      row_factors<ROWS>(g, e, h);
+      sts16((at ^ (e << 4)) + e * step, h[0] ^ (za * m01 & kSigns), h[1] ^ (za * m23 & kSigns), h[2] ^ (zb * m01 & kSigns),
+            h[3] ^ (zb * m23 & kSigns));
     }
+    top >>= 2;
+    at = (at ^ ((q ^ (q + 1)) << 5)) + 2 * step;
+    next_rows<ROWS>(g);
   }
 }
 
-template <bool QJL, bool ROWS>
-__device__ __forceinline__ void expand_bits(int bits, const PageRegs& r, uint32_t lo, uint32_t hi, const uint32_t (&nn)[4],
-                                            const uint32_t (&ng)[4], uint32_t d, int step, uint32_t x, int sketch_off) {
-  if (bits == 2) expand<2, QJL, ROWS>(r, lo, hi, nn, ng, d, step, x, sketch_off);
-  else if (bits == 3) expand<3, QJL, ROWS>(r, lo, hi, nn, ng, d, step, x, sketch_off);
-  else expand<1, QJL, ROWS>(r, lo, hi, nn, ng, d, step, x, sketch_off);
+// Of a warp whose threads have written operand rows: visible to the products, one arrival.
+__device__ __forceinline__ void arrive_rows(uint64_t& bar) {
+  fence_proxy_async();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_addr(&bar));
 }
 
 // One of 128 threads that dequantise the pages of a side's keys: octet order: tokens 8 o .. + 7, coordinates of words
 // 2 g, 2 g + 1; token order: token th / 2, half a row.
 template <bool KQ>
 struct KeyThread {
-  uint32_t lo, hi, row_off, x;
+  uint32_t row_off, x;
   int tile, off8, slot, step, tok;
   bool octet;
   // atom: bytes of an operand's atom of 64 K-elements
@@ -181,41 +228,33 @@ struct KeyThread {
     row_off = octet ? (g >> 3) * atom + o * 1024 : (th & 1) * atom + tok * 128;
     step = octet ? 128 : 0;
     x = octet ? g & 7 : tok & 7;
-    code_halves(p.k, lo, hi);
   }
   __device__ __forceinline__ void fetch(const ChunkParams& p, PageRegs& r, long ti) const {
     load_page<KQ>(r, p.k, reinterpret_cast<const unsigned char*>(p.kreg) + (size_t)(ti + tile) * p.k.tile_bytes, off8, slot);
   }
-  // the page's rows from `base` on (the sketch two atoms behind the codes)
-  __device__ __forceinline__ void store(const ChunkParams& p, const PageRegs& cur, uint32_t base, int atom) const {
-    uint32_t nn[4] = {cur.norm.x, cur.norm.y, cur.norm.z, cur.norm.w}, ng[4] = {};
-    if (KQ) {
-      const uint32_t gg[4] = {cur.gamma.x, cur.gamma.y, cur.gamma.z, cur.gamma.w};
+  // the page's rows from `base` on: its codes, then (where the caller wants them) its signs
+  __device__ __forceinline__ void codes(const ChunkParams& p, const PageRegs& cur, uint2 lut, uint32_t base) const {
+    uint32_t nn[4] = {cur.norm.x, cur.norm.y, cur.norm.z, cur.norm.w};
+    if (!octet) nn[0] = nn[1] = nn[2] = nn[3] = half_at(cur.norm, tok & 7) * 0x10001u;  // one token
+    expand_codes<true>(p.k.bits, cur, lut, nn, base + row_off, step, x);
+  }
+  __device__ __forceinline__ void signs(const PageRegs& cur, uint32_t base) const {
+    const uint32_t nn[4] = {cur.norm.x, cur.norm.y, cur.norm.z, cur.norm.w};
+    uint32_t ng[4] = {cur.gamma.x, cur.gamma.y, cur.gamma.z, cur.gamma.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) ng[i] = mul2(nn[i], mul2(gg[i], 0x2C002C00u));  // n * (gamma / 16)
-    }
-    if (!octet) {  // one token
-      const uint32_t nt = half_at(cur.norm, tok & 7) * 0x10001u;
-      const uint32_t gt = KQ ? half_at(make_uint4(ng[0], ng[1], ng[2], ng[3]), tok & 7) * 0x10001u : 0u;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        nn[i] = nt;
-        ng[i] = gt;
-      }
-    }
-    expand_bits<KQ, true>(p.k.bits, cur, lo, hi, nn, ng, base + row_off, step, x, 2 * atom);
+    for (int i = 0; i < 4; ++i) ng[i] = mul2(nn[i], mul2(ng[i], 0x2C002C00u));  // n * (gamma / 16)
+    if (!octet) ng[0] = ng[1] = ng[2] = ng[3] = half_at(make_uint4(ng[0], ng[1], ng[2], ng[3]), tok & 7) * 0x10001u;
+    expand_signs<true>(cur, ng, base + row_off, step, x);
   }
 };
 
 // One of 128 threads that dequantise values: rows are dims, 8 k .. + 7 of them, of tokens 8 c .. + 7.
 template <bool VQ>
 struct ValueThread {
-  uint32_t lo, hi;
   int c, k;
-  __device__ __forceinline__ void init(const ChunkParams& p, int th) {
+  __device__ __forceinline__ void init(int th) {
     c = th & 7;
     k = th >> 3;
-    code_halves(p.v, lo, hi);
   }
   __device__ __forceinline__ void fetch(const ChunkParams& p, PageRegs& r, long ti) const {
     load_page<VQ>(r, p.v, reinterpret_cast<const unsigned char*>(p.vreg) + (size_t)(ti + (c >> 2)) * p.v.tile_bytes,
@@ -223,7 +262,7 @@ struct ValueThread {
   }
   // the page's dims from `base` on (the sketch's 128 behind the codes'); tokens from `limit` on enter as zeros.
   // Returns this thread's 8 tokens whose norms are not finite, a bit each (zeros too).
-  __device__ __forceinline__ uint32_t store(const ChunkParams& p, const PageRegs& cur, uint32_t base, int limit) const {
+  __device__ __forceinline__ uint32_t store(const ChunkParams& p, const PageRegs& cur, uint2 lut, uint32_t base, int limit) const {
     const int tokens = limit - 8 * c;
     uint32_t nn[4] = {cur.norm.x, cur.norm.y, cur.norm.z, cur.norm.w}, ng[4] = {}, bad = 0;
     if (VQ) {
@@ -245,9 +284,12 @@ struct ValueThread {
         }
       }
     }
+    expand_codes<false>(p.v.bits, cur, lut, nn, base + k * 1024, 128, c);
+    if (VQ) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) ng[i] = mul2(nn[i], mul2(ng[i], 0x2C002C00u));  // n * (gamma / 16)
-    expand_bits<VQ, false>(p.v.bits, cur, lo, hi, nn, ng, base + k * 1024, 128, c, kHeadDim * 128);
+      for (int i = 0; i < 4; ++i) ng[i] = mul2(nn[i], mul2(ng[i], 0x2C002C00u));  // n * (gamma / 16)
+      expand_signs<false>(cur, ng, base + kHeadDim * 128 + k * 1024, 128, c);
+    }
     return bad;
   }
 };
@@ -255,7 +297,10 @@ struct ValueThread {
 // A page's block-table entry (loaded a page before it is looked at: looking waits for the load), and its
 // first tile, page 0's for an entry that names none (kvq_tiles.cuh).
 __device__ __forceinline__ int page_entry(const ChunkParams& p, const Walk& w, int page) {
-  return p.table && page < p.pages_per_seq ? __ldcg(p.table + (long)w.rows.b * p.pages_per_seq + page) : 0;
+  int entry = 0;
+  if (p.table && page < p.pages_per_seq)
+    asm volatile("ld.global.cg.s32 %0, [%1];\n" : "=r"(entry) : "l"(p.table + (long)w.rows.b * p.pages_per_seq + page));
+  return entry;
 }
 __device__ __forceinline__ long page_tile(const ChunkParams& p, const Walk& w, int page, int entry) {
   if (!p.table) return ((long)w.rows.b * p.Hkv + w.hk) * p.tiles_per_seq + 2 * page;

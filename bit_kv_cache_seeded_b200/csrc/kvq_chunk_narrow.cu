@@ -9,8 +9,9 @@
 // no row's maximum grows by more than 2^8: sums stay with their thread until the segment's end.
 //
 // Warps: 4 softmax, 4 + 4 that dequantise keys (the step's first and second page; they also fetch the queries), 4 +
-// 4 values, 2 that issue the products. Measured against the wide kernel on 16 requests of 4-32 rows over 7000
-// tokens, 2 bits and sketches on both sides: see launch.
+// 4 values, 2 that issue the products. Where 227 KB hold two stages of values, but one of keys, the keys' codes
+// and signs are handed over apart: the products with the codes run while the signs are made, and free the codes'
+// half for the next step.
 #include "kvq_async.cuh"
 #include "kvq_chunk_dequant.cuh"
 #include "kvq_tcgen05.cuh"
@@ -30,17 +31,19 @@ constexpr uint32_t kColO = 2 * N, kTmemCols = 128;
 template <bool KQ, bool VQ>
 struct Cfg {
   static constexpr int DK = KQ ? 256 : 128, DV = VQ ? 256 : 128;
-  static constexpr int KS = KQ && VQ ? 1 : 2, VS = 2;  // stages: what 227 KB hold
-  static constexpr int kQBytes = N * DK * 2, kKStage = kStep * DK * 2, kVPage = DV * 128, kVStage = 2 * kVPage;
+  // stages: what 227 KB hold. Keys come in parts of 128 K-elements, codes and signs, a stage each
+  static constexpr int KP = DK / 128, KS = KQ && VQ ? 2 : 2 * KP, VS = 2;
+  static constexpr int kQBytes = N * DK * 2, kKStage = kStep * 256, kVPage = DV * 128, kVStage = 2 * kVPage;
   static constexpr int kOffP = kQBytes, kOffK = kOffP + 2 * kPBytes, kOffV = kOffK + KS * kKStage, kOffEnd = kOffV + VS * kVStage;
 };
-// Registers a thread: launched with 80 (22 warps), the softmax keeps two sets of 32 and takes what the dequantising
-// warps give back: 4 * 176 + 16 * 56 + 2 * 80 = 22 * 80, on every quarter of the SM.
-constexpr int kRegsSoftmax = 176, kRegsDequant = 56;
-constexpr int kWarpK = 4, kWarpV = 12, kWarpS = 20, kThreads = 32 * 22;
+// Registers a thread: launched with 80 (24 warps, of which two only give theirs back). The softmax keeps two sets of 32;
+// nothing may spill, since shared memory leaves the L1 too small to hold local memory (232 us where 100 bytes did).
+// 4 * 136 + 16 * 72 + 4 * 56 = 24 * 80, on every quarter of the SM.
+constexpr int kRegsSoftmax = 136, kRegsDequant = 72, kRegsIssue = 56;
+constexpr int kWarpK = 4, kWarpV = 12, kWarpS = 20, kWarpO = 21, kThreads = 32 * 24;
 
 struct Bars {
-  uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pready[2], pvdone[2], qfull, qempty, done[2];
+  uint64_t kfull[4], kempty[4], vfull[2], vempty[2], sfull[2], pready[2], pvdone[2], qfull, qempty, done[2];
   unsigned char vbad[2][16];  // tokens of the step whose value norm is not finite, a bit each
   float4 col[N / 2];          // of a pair of rows: query scales, minus the references
   float m[N];                 // maxima the references belong to
@@ -74,17 +77,19 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow(const __grid_constan
   if (set.head[1] == 0) return;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_addr(&bars.kfull[i]), 256);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_addr(&bars.kfull[i]), 8);
       mbar_init(smem_addr(&bars.kempty[i]), 1);
-      mbar_init(smem_addr(&bars.vfull[i]), 256);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&bars.vfull[i]), 8);
       mbar_init(smem_addr(&bars.vempty[i]), 1);
       mbar_init(smem_addr(&bars.sfull[i]), 1);
-      mbar_init(smem_addr(&bars.pready[i]), 128);
+      mbar_init(smem_addr(&bars.pready[i]), 4);
       mbar_init(smem_addr(&bars.pvdone[i]), 1);
       mbar_init(smem_addr(&bars.done[i]), 1);
     }
-    mbar_init(smem_addr(&bars.qfull), 256);
+    mbar_init(smem_addr(&bars.qfull), 8);
     mbar_init(smem_addr(&bars.qempty), 1);
     mbar_init_fence();
     bars.fail = 0;
@@ -135,15 +140,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow(const __grid_constan
         wait(bars.sfull[b], (n >> 1) & 1);
         tc::fence_after();
         float e[N];
-        {
-          uint32_t s[N];
-          tc::tmem_ld32(tS + N * b, s);
+#pragma unroll
+        for (int h = 0; h < N; h += 16) {
+          uint32_t s[16];
+          tc::tmem_ld16(tS + N * b + h, s);
           tc::wait_ld();
 #pragma unroll
-          for (int c = 0; c < N / 2; ++c) {
-            const float4 q = bars.col[c];
-            e[2 * c] = fmaf(__uint_as_float(s[2 * c]), q.x, q.z);
-            e[2 * c + 1] = fmaf(__uint_as_float(s[2 * c + 1]), q.y, q.w);
+          for (int c = 0; c < 8; ++c) {
+            const float4 q = bars.col[h / 2 + c];
+            e[h + 2 * c] = fmaf(__uint_as_float(s[2 * c]), q.x, q.z);
+            e[h + 2 * c + 1] = fmaf(__uint_as_float(s[2 * c + 1]), q.y, q.w);
           }
         }
         if (t0 + kStep - 1 > r.pos0) {  // some row does not attend to the whole step
@@ -178,13 +184,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow(const __grid_constan
             wait(bars.pvdone[(n - 1) & 1], ((n - 1) >> 1) & 1);
             tc::fence_after();
 #pragma unroll 1
-            for (int i = 0; i < DV / 128; ++i) {
-              uint32_t o[N];
-              tc::tmem_ld32(tO + i * N, o);
+            for (int i = 0; i < DV / 128 * (N / 8); ++i) {
+              uint32_t o[8];
+              tc::tmem_ld8(tO + 8 * i, o);
               tc::wait_ld();
 #pragma unroll
-              for (int c = 0; c < N; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * __shfl_sync(0xffffffffu, alpha, c));
-              tc::tmem_st32(tO + i * N, o);
+              for (int c = 0; c < 8; ++c)
+                o[c] = __float_as_uint(__uint_as_float(o[c]) * __shfl_sync(0xffffffffu, alpha, 8 * (i % (N / 8)) + c));
+              tc::tmem_st8(tO + 8 * i, o);
             }
             tc::wait_st();
           }
@@ -217,9 +224,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow(const __grid_constan
           for (int c = 0; c < N; ++c)
             if (t <= bars.last[c]) l[c] = NAN;
         }
-        fence_proxy_async();
         tc::fence_before();
-        mbar_arrive(smem_addr(&bars.pready[b]));
+        arrive_rows(bars.pready[b]);
       }
       // the segment's state
       float mine = 0.f;
@@ -242,31 +248,33 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow(const __grid_constan
         tc::fence_after();
       }
 #pragma unroll 1
-      for (int i = 0; i < DV / 128; ++i) {
-        uint32_t o[N];
+      for (int i = 0; i < DV / 128 * (N / 8); ++i) {
+        uint32_t o[8];
         if (ns > 0) {
-          tc::tmem_ld32(tO + i * N, o);
+          tc::tmem_ld8(tO + 8 * i, o);
           tc::wait_ld();
         }
+        const int row0 = 8 * (i % (N / 8)), dim = i / (N / 8) * 128;
 #pragma unroll
-        for (int c = 0; c < N; ++c)
-          if (c < r.count) so[(size_t)c * DV + i * 128] = ns > 0 ? __uint_as_float(o[c]) : 0.f;
+        for (int c = 0; c < 8; ++c)
+          if (row0 + c < r.count) so[(size_t)(row0 + c) * DV + dim] = ns > 0 ? __uint_as_float(o[c]) : 0.f;
       }
       tc::fence_before();
       bar128();  // the next segment's rows replace these
     }
   } else if (warp < kWarpV) {  // ---- keys, and the queries of each segment
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsDequant));
-    const int all = tid - 32 * kWarpK, grp = all >> 7;
+    const int all = tid - 32 * kWarpK, second = all >> 7;
     KeyThread<KQ> keys;
     keys.init(p, all & 127, kAtom);
-    int n = 0, seg = 0;
+    const uint2 lut = code_halves(p.k);
+    int n = 0, seg = 0;  // n: parts handed over
     PageRegs regs = {};
     while (w.next(p, set)) {
       const Rows r = w.rows;
       const int ns = segment_steps(w);
       if (ns == 0) continue;
-      int page = 2 * w.k0 + grp;
+      int page = 2 * w.k0 + second;
       if (page * kPage < r.limit) keys.fetch(p, regs, page_tile(p, w, page, page_entry(p, w, page)));
       int entry = page_entry(p, w, page + 2);  // of the page after the one in regs
       if (seg > 0) wait(bars.qempty, (seg - 1) & 1);
@@ -282,98 +290,109 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow(const __grid_constan
                                                (qrow0 + (size_t)(row / p.group) * p.Hq + row % p.group) * DK) + ch);
         *reinterpret_cast<uint4*>(smem + (ch >> 3) * (N * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = v;
       }
-      fence_proxy_async();
-      mbar_arrive(smem_addr(&bars.qfull));
-      for (int j = 0; j < ns; ++j, ++n, page += 2) {
-        const int st = n % C::KS;
-        if (n >= C::KS) wait(bars.kempty[st], (n / C::KS - 1) & 1);
+      arrive_rows(bars.qfull);
+      for (int j = 0; j < ns; ++j, page += 2) {
         const PageRegs cur = regs;
         if (j + 1 < ns && (page + 2) * kPage < r.limit) {
           keys.fetch(p, regs, page_tile(p, w, page + 2, entry));
           entry = page_entry(p, w, page + 4);
         }
-        // a second page behind the limit stays as it was: its logits are masked
-        if (page * kPage < r.limit) keys.store(p, cur, sm + C::kOffK + st * C::kKStage + grp * kPage * 128, kAtom);
-        fence_proxy_async();
-        mbar_arrive(smem_addr(&bars.kfull[st]));
+#pragma unroll
+        for (int part = 0; part < C::KP; ++part, ++n) {
+          const int st = n % C::KS;
+          const uint32_t base = sm + C::kOffK + st * C::kKStage + second * kPage * 128;
+          if (n >= C::KS) wait(bars.kempty[st], (n / C::KS - 1) & 1);
+          if (page * kPage < r.limit) {  // a second page behind the limit stays as it was: its logits are masked
+            if (part == 0) keys.codes(p, cur, lut, base);
+            else keys.signs(cur, base);
+          }
+          arrive_rows(bars.kfull[st]);
+        }
       }
     }
   } else if (warp < kWarpS) {  // ---- values
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsDequant));
-    const int all = tid - 32 * kWarpV, grp = all >> 7, th = all & 127;
+    const int all = tid - 32 * kWarpV, second = all >> 7, th = all & 127;
     ValueThread<VQ> values;
-    values.init(p, th);
+    values.init(th);
+    const uint2 lut = code_halves(p.v);
     int n = 0;
     PageRegs regs = {};
     while (w.next(p, set)) {
       const int ns = segment_steps(w), limit = w.rows.limit;
       if (ns == 0) continue;
-      int page = 2 * w.k0 + grp;
+      int page = 2 * w.k0 + second;
       if (page * kPage < limit) values.fetch(p, regs, page_tile(p, w, page, page_entry(p, w, page)));
       int entry = page_entry(p, w, page + 2);  // of the page after the one in regs
       for (int j = 0; j < ns; ++j, ++n, page += 2) {
         const int st = n % C::VS;
-        if (n >= C::VS) wait(bars.vempty[st], (n / C::VS - 1) & 1);
         const PageRegs cur = regs;
         if (j + 1 < ns && (page + 2) * kPage < limit) {
           values.fetch(p, regs, page_tile(p, w, page + 2, entry));
           entry = page_entry(p, w, page + 4);
         }
+        if (n >= C::VS) wait(bars.vempty[st], (n / C::VS - 1) & 1);
         // a second page behind the limit enters as zeros
-        const uint32_t bad = values.store(p, cur, sm + C::kOffV + st * C::kVStage + grp * C::kVPage, limit - page * kPage);
-        if (th < 8) bars.vbad[st][8 * grp + th] = (unsigned char)bad;
-        fence_proxy_async();
-        mbar_arrive(smem_addr(&bars.vfull[st]));
+        const uint32_t bad = values.store(p, cur, lut, sm + C::kOffV + st * C::kVStage + second * C::kVPage, limit - page * kPage);
+        if (th < 8) bars.vbad[st][8 * second + th] = (unsigned char)bad;
+        arrive_rows(bars.vfull[st]);
       }
     }
-  } else if (warp == kWarpS) {  // ---- S^T = K Q^T (the whole warp, so that control stays uniform)
-    constexpr uint32_t id = tc::idesc_f16(0, 0, 0, kStep, N);
-    int n = 0, seg = 0;
-    while (w.next(p, set)) {
-      const int ns = __shfl_sync(0xffffffffu, segment_steps(w), 0);
-      if (ns == 0) continue;
-      wait(bars.qfull, seg & 1);
-      ++seg;
-      for (int j = 0; j < ns; ++j, ++n) {
-        const int st = n % C::KS, b = n & 1;
-        wait(bars.kfull[st], (n / C::KS) & 1);
-        if (n >= 2) wait(bars.pready[b], ((n >> 1) - 1) & 1);  // S of two steps before is read
-        tc::fence_after();
-        const uint64_t kd = desc_sw128(sm + C::kOffK + st * C::kKStage), qd = desc_sw128(sm);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsIssue));
+    if (warp == kWarpS) {  // ---- S^T = K Q^T (the whole warp, so that control stays uniform)
+      constexpr uint32_t id = tc::idesc_f16(0, 0, 0, kStep, N);
+      int n = 0, seg = 0;
+      while (w.next(p, set)) {
+        const int ns = __shfl_sync(0xffffffffu, segment_steps(w), 0);
+        if (ns == 0) continue;
+        wait(bars.qfull, seg & 1);
+        ++seg;
+        for (int j = 0; j < ns; ++j, ++n) {
+          const int b = n & 1;
+          if (n >= 2) wait(bars.pready[b], ((n >> 1) - 1) & 1);  // S of two steps before is read
 #pragma unroll
-        for (int i = 0; i < DK / 64; ++i)
-          tc::umma_f16_x4(tmem + b * N, kd + ((i * kAtom) >> 4), qd + ((i * N * 128) >> 4), id, i > 0);
-        tc::commit_elected(smem_addr(&bars.sfull[b]));
-        tc::commit_elected(smem_addr(&bars.kempty[st]));
+          for (int part = 0; part < C::KP; ++part) {
+            const int np = n * C::KP + part, st = np % C::KS;
+            wait(bars.kfull[st], (np / C::KS) & 1);
+            tc::fence_after();
+            const uint64_t kd = desc_sw128(sm + C::kOffK + st * C::kKStage), qd = desc_sw128(sm + part * 2 * N * 128);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              tc::umma_f16_x4(tmem + b * N, kd + ((i * kAtom) >> 4), qd + ((i * N * 128) >> 4), id, part > 0 || i > 0);
+            tc::commit_elected(smem_addr(&bars.kempty[st]));
+          }
+          tc::commit_elected(smem_addr(&bars.sfull[b]));
+        }
+        tc::commit_elected(smem_addr(&bars.qempty));
       }
-      tc::commit_elected(smem_addr(&bars.qempty));
-    }
-    tc::commit_elected(smem_addr(&bars.done[0]));
-    mbar_wait(smem_addr(&bars.done[0]), 0, p.wait_limit);
-  } else {  // ---- O^T += V^T P^T
-    constexpr uint32_t id = tc::idesc_f16(0, 0, 1, 128, N);
-    int n = 0;
-    while (w.next(p, set)) {
-      const int ns = __shfl_sync(0xffffffffu, segment_steps(w), 0);
-      for (int j = 0; j < ns; ++j, ++n) {
-        const int st = n % C::VS, b = n & 1;
-        wait(bars.vfull[st], (n / C::VS) & 1);
-        wait(bars.pready[b], (n >> 1) & 1);
-        tc::fence_after();
-        const uint64_t vd = desc_sw128(sm + C::kOffV + st * C::kVStage);
-        const uint64_t pd = tc::smem_desc(sm + C::kOffP + b * kPBytes, N / 8 * 128, 128);
-#pragma unroll
-        for (int g = 0; g < 2; ++g)
-#pragma unroll
-          for (int i = 0; i < DV / 128; ++i)
-            tc::umma_f16_x4<32, 2 * (N / 8) * 128>(tmem + kColO + i * N, vd + ((g * C::kVPage + i * 128 * 128) >> 4),
-                                                   pd + ((g * kPBytes / 2) >> 4), id, j > 0 || g > 0);
-        tc::commit_elected(smem_addr(&bars.pvdone[b]));
-        tc::commit_elected(smem_addr(&bars.vempty[st]));
+      tc::commit_elected(smem_addr(&bars.done[0]));
+      mbar_wait(smem_addr(&bars.done[0]), 0, p.wait_limit);
+    } else if (warp == kWarpO) {  // ---- O^T += V^T P^T
+      constexpr uint32_t id = tc::idesc_f16(0, 0, 1, 128, N);
+      int n = 0;
+      while (w.next(p, set)) {
+        const int ns = __shfl_sync(0xffffffffu, segment_steps(w), 0);
+        for (int j = 0; j < ns; ++j, ++n) {
+          const int st = n % C::VS, b = n & 1;
+          wait(bars.vfull[st], (n / C::VS) & 1);
+          wait(bars.pready[b], (n >> 1) & 1);
+          tc::fence_after();
+          const uint64_t vd = desc_sw128(sm + C::kOffV + st * C::kVStage);
+          const uint64_t pd = tc::smem_desc(sm + C::kOffP + b * kPBytes, N / 8 * 128, 128);
+  #pragma unroll
+          for (int g = 0; g < 2; ++g)
+  #pragma unroll
+            for (int i = 0; i < DV / 128; ++i)
+              tc::umma_f16_x4<32, 2 * (N / 8) * 128>(tmem + kColO + i * N, vd + ((g * C::kVPage + i * 128 * 128) >> 4),
+                                                     pd + ((g * kPBytes / 2) >> 4), id, j > 0 || g > 0);
+          tc::commit_elected(smem_addr(&bars.pvdone[b]));
+          tc::commit_elected(smem_addr(&bars.vempty[st]));
+        }
       }
+      tc::commit_elected(smem_addr(&bars.done[1]));
+      mbar_wait(smem_addr(&bars.done[1]), 0, p.wait_limit);
     }
-    tc::commit_elected(smem_addr(&bars.done[1]));
-    mbar_wait(smem_addr(&bars.done[1]), 0, p.wait_limit);
   }
   __syncwarp();
   tc::fence_before();

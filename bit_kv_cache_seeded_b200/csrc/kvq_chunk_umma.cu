@@ -109,18 +109,18 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_addr(&bars.kfull[i]), 128);
+      mbar_init(smem_addr(&bars.kfull[i]), 4);
       mbar_init(smem_addr(&bars.kempty[i]), 1);
-      mbar_init(smem_addr(&bars.vfull[i]), 128);
+      mbar_init(smem_addr(&bars.vfull[i]), 4);
       mbar_init(smem_addr(&bars.vempty[i]), 1);
     }
     for (int t = 0; t < NT; ++t)
       for (int b = 0; b < 2; ++b) {
         mbar_init(smem_addr(&bars.sfull[t][b]), 1);
-        mbar_init(smem_addr(&bars.pready[t][b]), 128);
+        mbar_init(smem_addr(&bars.pready[t][b]), 4);
         mbar_init(smem_addr(&bars.pvdone[t][b]), 1);
       }
-    mbar_init(smem_addr(&bars.qfull), 128 * C::KG);
+    mbar_init(smem_addr(&bars.qfull), 4 * C::KG);
     mbar_init(smem_addr(&bars.qempty), 1);
     mbar_init(smem_addr(&bars.done[0]), 1);
     mbar_init(smem_addr(&bars.done[1]), 1);
@@ -244,7 +244,8 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
           tc::wait_st();
         }
         tc::fence_before();
-        mbar_arrive(smem_addr(&bars.pready[t][b]));
+        __syncwarp();
+        if ((tid & 31) == 0) mbar_arrive(smem_addr(&bars.pready[t][b]));
       }
       nv += np;
       // the segment's state
@@ -276,8 +277,9 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
     const int all = tid - 32 * C::kWarpK, th = all & 127, grp = all >> 7;
     KeyThread<KQ> keys;
     keys.init(p, th, kPage * 128);
+    const uint2 lut = code_halves(p.k);
     int n = 0, seg = 0;
-    PageRegs regs;
+    PageRegs regs = {};
     while (w.next(p, set)) {
       const Rows r = w.rows;
       const int np = segment_pages(w);
@@ -300,29 +302,29 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
         *reinterpret_cast<uint4*>(smem + (row / kTileRows) * C::kQTile + (ch >> 3) * (kTileRows * 128) + rr * 128 +
                                   (((ch & 7) ^ (rr & 7)) << 4)) = v;
       }
-      fence_proxy_async();
-      mbar_arrive(smem_addr(&bars.qfull));
+      arrive_rows(bars.qfull);
       for (int j = first; j < np; j += C::KG) {
         const int nj = n + j, st = nj % kStages;
-        if (nj >= kStages) wait(bars.kempty[st], (nj / kStages - 1) & 1);
-        const uint32_t base = sm + C::kOffK + st * C::kKStage;
         const PageRegs cur = regs;
         if (j + C::KG < np) {
           keys.fetch(p, regs, page_tile(p, w, w.k0 + j + C::KG, entry));
           entry = page_entry(p, w, w.k0 + j + 2 * C::KG);
         }
-        keys.store(p, cur, base, kPage * 128);
-        fence_proxy_async();
-        mbar_arrive(smem_addr(&bars.kfull[st]));
+        if (nj >= kStages) wait(bars.kempty[st], (nj / kStages - 1) & 1);
+        const uint32_t base = sm + C::kOffK + st * C::kKStage;
+        keys.codes(p, cur, lut, base);
+        if (KQ) keys.signs(cur, base + 2 * kPage * 128);
+        arrive_rows(bars.kfull[st]);
       }
       n += np;
     }
   } else if (warp < C::kWarpS) {  // ---- values: dims 8 k .. + 7 of tokens 8 c .. + 7
     const int th = (tid - 32 * C::kWarpV) & 127, grp = (tid - 32 * C::kWarpV) >> 7;
     ValueThread<VQ> values;
-    values.init(p, th);
+    values.init(th);
+    const uint2 lut = code_halves(p.v);
     int n = 0;
-    PageRegs regs;
+    PageRegs regs = {};
     while (w.next(p, set)) {
       const int np = segment_pages(w);
       if (np == 0) continue;
@@ -331,17 +333,16 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
       int entry = page_entry(p, w, w.k0 + first + C::VG);  // of the page after the one in regs
       for (int j = first; j < np; j += C::VG) {
         const int nj = n + j, st = nj % kStages;
-        if (nj >= kStages) wait(bars.vempty[st], (nj / kStages - 1) & 1);
         const PageRegs cur = regs;
         const int limit = w.rows.limit - (w.k0 + j) * kPage;
         if (j + C::VG < np) {
           values.fetch(p, regs, page_tile(p, w, w.k0 + j + C::VG, entry));
           entry = page_entry(p, w, w.k0 + j + 2 * C::VG);
         }
-        const uint32_t bad = values.store(p, cur, sm + C::kOffV + st * C::kVStage, limit);
+        if (nj >= kStages) wait(bars.vempty[st], (nj / kStages - 1) & 1);
+        const uint32_t bad = values.store(p, cur, lut, sm + C::kOffV + st * C::kVStage, limit);
         if (th < 8) bars.vbad[st][th] = (unsigned char)bad;
-        fence_proxy_async();
-        mbar_arrive(smem_addr(&bars.vfull[st]));
+        arrive_rows(bars.vfull[st]);
       }
       n += np;
     }
