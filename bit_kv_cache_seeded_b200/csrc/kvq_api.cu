@@ -1333,7 +1333,7 @@ kvq_status kvq_chunk_attention(const kvq_cache* c, const void* q, kvq_dtype dtyp
   p.err = c->d_status;
   p.wait_limit = kWaitLimitCycles;
   char* w = static_cast<char*>(workspace);
-  p.ctas = L.ctas;
+  p.sms = c->sms;
   p.sets = L.sets;
   for (int i = 0; i < L.sets; ++i) {
     const ChunkLayout::Set& from = L.set[i];
@@ -1342,6 +1342,7 @@ kvq_status kvq_chunk_attention(const kvq_cache* c, const void* q, kvq_dtype dtyp
     to.upto = from.upto;
     to.rows = from.rows;
     to.unit = from.unit;
+    to.ctas = from.ctas;
     to.max_tiles = from.max_tiles;
     to.unit_start = reinterpret_cast<long long*>(w + from.unit_start);
     to.tile_seq = reinterpret_cast<int*>(w + from.tile_seq);

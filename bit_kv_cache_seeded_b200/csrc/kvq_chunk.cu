@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kMergeThreads, VQ ? 2 : 3) chunk_merge(const _
     const int in = p.sets > 1 && g >= first[1];
     const ChunkSet& set = p.set[in];
     const int group = g - (in ? first[1] : 0), per = set.rows / kMergeRows, tiles = (int)set.head[0];
-    const long long units = set.head[1], T = units * p.Hkv, G = cta_count(p, T);
+    const long long units = set.head[1], T = units * p.Hkv, G = cta_count(set, T);
     const int item = group / per;
     const int hk = item / tiles, tile = item % tiles;
     const int group0 = group % per * kMergeRows, row0 = group0 + 4 * warp;
@@ -667,14 +667,14 @@ __global__ void __launch_bounds__(kMergeThreads, VQ ? 2 : 3) chunk_merge(const _
 template <bool KQ, bool BF16>
 cudaError_t launch_prep(const ChunkParams& p, cudaStream_t s) {
   const long long groups = ((long long)p.n_tokens * p.Hq + kPrepRows - 1) / kPrepRows;
-  chunk_prep<KQ, BF16><<<p.sets + (unsigned)std::min(groups, 2ll * p.ctas), kPrepThreads, 0, s>>>(p);
+  chunk_prep<KQ, BF16><<<p.sets + (unsigned)std::min(groups, 2ll * p.sms), kPrepThreads, 0, s>>>(p);
   return launched();
 }
 template <bool VQ, bool BF16>
 cudaError_t launch_merge(const ChunkParams& p, cudaStream_t s) {
   long long groups = 0;
   for (int i = 0; i < p.sets; ++i) groups += (long long)p.set[i].max_tiles * p.Hkv * (p.set[i].rows / kMergeRows);
-  chunk_merge<VQ, BF16><<<(unsigned)std::min(groups, (VQ ? 2ll : 3ll) * p.ctas), kMergeThreads, 0, s>>>(p);
+  chunk_merge<VQ, BF16><<<(unsigned)std::min(groups, (VQ ? 2ll : 3ll) * p.sms), kMergeThreads, 0, s>>>(p);
   return launched();
 }
 
@@ -683,7 +683,7 @@ cudaError_t launch_f32(const ChunkParams& p, cudaStream_t s) {
   constexpr int smem = (int)sizeof(F32Smem<KQ, VQ>);
   const cudaError_t e = cudaFuncSetAttribute(chunk_f32<KQ, VQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  chunk_f32<KQ, VQ><<<p.ctas, 256, smem, s>>>(p);
+  chunk_f32<KQ, VQ><<<p.set[kWide].ctas, 256, smem, s>>>(p);
   return launched();
 }
 
@@ -693,7 +693,6 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 ChunkLayout chunk_layout(int n_tokens, int batch, int Hq, int Hkv, bool k_qjl, bool v_qjl, bool bf16, int sms) {
   ChunkLayout L;
-  L.ctas = sms;
   L.sets = bf16 ? 2 : 1;
   const int group = Hq / Hkv;
   size_t off = 0;
@@ -708,7 +707,8 @@ ChunkLayout chunk_layout(int n_tokens, int batch, int Hq, int Hkv, bool k_qjl, b
     s.above = bf16 && i == kWide ? kNarrowRows : 0;
     s.upto = i == kNarrow ? kNarrowRows : 0x7fffffff;
     s.rows = i == kNarrow ? kNarrowRows : bf16 ? chunk_umma_rows(v_qjl) : kF32Rows;
-    s.unit = i == kNarrow ? 2 * kPage : kPage;
+    s.unit = bf16 ? 2 * kPage : kPage;
+    s.ctas = bf16 && i == kWide ? std::max(sms / 2, 1) : sms;
     // requests of a set have above / group + 1 tokens at least, a tile each and one per `rows` rows
     s.max_tiles = std::min(batch, n_tokens / (s.above / group + 1));
     if (i == kWide) s.max_tiles += n_tokens / (s.rows / group);
@@ -717,7 +717,7 @@ ChunkLayout chunk_layout(int n_tokens, int batch, int Hq, int Hkv, bool k_qjl, b
     s.unit_start = take(sizeof(long long) * ((size_t)s.max_tiles + 1));
     s.tile_seq = take(sizeof(int) * (size_t)s.max_tiles);
     s.tile_start = take(sizeof(int) * ((size_t)batch + 1));
-    const size_t segments = s.max_tiles ? (size_t)s.max_tiles * Hkv + L.ctas : 0;
+    const size_t segments = s.max_tiles ? (size_t)s.max_tiles * Hkv + s.ctas : 0;
     s.part = take(sizeof(float) * segments * s.rows * (2 + kHeadDim * (v_qjl ? 2 : 1)));
   }
   const size_t rows = (size_t)n_tokens * Hq;

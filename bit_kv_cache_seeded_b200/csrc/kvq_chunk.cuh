@@ -2,7 +2,7 @@
 // segments leave behind.
 //
 // Rows. A kv-head of request b has n_b * group query rows, row r = token r / group, head r % group. A set (ChunkSet)
-// takes the requests whose rows are within its bounds. Row tiles of `rows` rows never cross a request; tile t of a
+// takes the requests whose rows are within its bounds. (A pair of CTAs counts as one CTA here.) Row tiles of `rows` rows never cross a request; tile t of a
 // kv-head belongs to request tile_seq[t], the tiles of request b being tile_start[b] .. tile_start[b + 1] - 1.
 //
 // Units. Tile t attends to the positions below its limit, the last row's position + 1, in units of one or two
@@ -52,7 +52,7 @@ __device__ __forceinline__ Rows tile_rows(const ChunkParams& p, const ChunkSet& 
 
 // CTAs that share T units (each has one at least), and the CTA that owns unit u: the largest c with
 // floor(c T / G) <= u.
-__device__ __forceinline__ long long cta_count(const ChunkParams& p, long long T) { return min((long long)p.ctas, T); }
+__device__ __forceinline__ long long cta_count(const ChunkSet& s, long long T) { return min((long long)s.ctas, T); }
 __device__ __forceinline__ long long cta_first(long long c, long long T, long long G) { return c * T / G; }
 __device__ __forceinline__ int cta_of(long long u, long long T, long long G) { return (int)(((u + 1) * G - 1) / T); }
 
@@ -69,7 +69,7 @@ struct Walk {
     tiles = (int)s.head[0];
     units = s.head[1];
     const long long T = units * p.Hkv;
-    const long long G = cta_count(p, T);
+    const long long G = cta_count(s, T);
     u = cta < G ? cta_first(cta, T, G) : 0;
     end = cta < G ? cta_first(cta + 1, T, G) : 0;
     hk = units > 0 ? (int)(u / units) : 0;

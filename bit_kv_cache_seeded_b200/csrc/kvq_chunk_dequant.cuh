@@ -248,21 +248,22 @@ struct KeyThread {
   }
 };
 
-// One of 128 threads that dequantise values: rows are dims, 8 k .. + 7 of them, of tokens 8 c .. + 7.
+// One of the threads that dequantise values: rows are dims, dims 8 k .. + 7 in rows 8 row8 .. + 7, of tokens 8 c .. + 7.
 template <bool VQ>
 struct ValueThread {
-  int c, k;
-  __device__ __forceinline__ void init(int th) {
-    c = th & 7;
-    k = th >> 3;
+  int c, k, row8;
+  __device__ __forceinline__ void init(int chunk, int octet, int rows8) {
+    c = chunk;
+    k = octet;
+    row8 = rows8;
   }
   __device__ __forceinline__ void fetch(const ChunkParams& p, PageRegs& r, long ti) const {
     load_page<VQ>(r, p.v, reinterpret_cast<const unsigned char*>(p.vreg) + (size_t)(ti + (c >> 2)) * p.v.tile_bytes,
                   k * kTile + 8 * (c & 3), 8 * (c & 3));
   }
-  // the page's dims from `base` on (the sketch's 128 behind the codes'); tokens from `limit` on enter as zeros.
+  // the page's dims from `base` on (the signs' `signs` bytes behind the codes'); tokens from `limit` on enter as zeros.
   // Returns this thread's 8 tokens whose norms are not finite, a bit each (zeros too).
-  __device__ __forceinline__ uint32_t store(const ChunkParams& p, const PageRegs& cur, uint2 lut, uint32_t base, int limit) const {
+  __device__ __forceinline__ uint32_t store(const ChunkParams& p, const PageRegs& cur, uint2 lut, uint32_t base, int signs, int limit) const {
     const int tokens = limit - 8 * c;
     uint32_t nn[4] = {cur.norm.x, cur.norm.y, cur.norm.z, cur.norm.w}, ng[4] = {}, bad = 0;
     if (VQ) {
@@ -284,11 +285,11 @@ struct ValueThread {
         }
       }
     }
-    expand_codes<false>(p.v.bits, cur, lut, nn, base + k * 1024, 128, c);
+    expand_codes<false>(p.v.bits, cur, lut, nn, base + row8 * 1024, 128, c);
     if (VQ) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) ng[i] = mul2(nn[i], mul2(ng[i], 0x2C002C00u));  // n * (gamma / 16)
-      expand_signs<false>(cur, ng, base + kHeadDim * 128 + k * 1024, 128, c);
+      expand_signs<false>(cur, ng, base + signs + row8 * 1024, 128, c);
     }
     return bad;
   }

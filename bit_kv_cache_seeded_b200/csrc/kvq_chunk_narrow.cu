@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow(const __grid_constan
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsDequant));
     const int all = tid - 32 * kWarpV, second = all >> 7, th = all & 127;
     ValueThread<VQ> values;
-    values.init(th);
+    values.init(th & 7, th >> 3, th >> 3);
     const uint2 lut = code_halves(p.v);
     int n = 0;
     PageRegs regs = {};
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow(const __grid_constan
         }
         if (n >= C::VS) wait(bars.vempty[st], (n / C::VS - 1) & 1);
         // a second page behind the limit enters as zeros
-        const uint32_t bad = values.store(p, cur, lut, sm + C::kOffV + st * C::kVStage + second * C::kVPage, limit - page * kPage);
+        const uint32_t bad = values.store(p, cur, lut, sm + C::kOffV + st * C::kVStage + second * C::kVPage, kHeadDim * 128, limit - page * kPage);
         if (th < 8) bars.vbad[st][8 * second + th] = (unsigned char)bad;
         arrive_rows(bars.vfull[st]);
       }
@@ -408,7 +408,7 @@ cudaError_t launch(const ChunkParams& p, cudaStream_t s) {
   constexpr int smem = Cfg<KQ, VQ>::kOffEnd;
   const cudaError_t e = cudaFuncSetAttribute(chunk_narrow<KQ, VQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  chunk_narrow<KQ, VQ><<<p.ctas, kThreads, smem, s>>>(p);
+  chunk_narrow<KQ, VQ><<<p.set[kNarrow].ctas, kThreads, smem, s>>>(p);
   return launched();
 }
 

@@ -1,17 +1,22 @@
 // Chunk attention's segment kernel on 5th-generation tensor cores (tcgen05, kind::f16, fp32 sums), for bf16
-// queries. Work plan and the states it leaves: kvq_chunk.cuh.
+// queries of requests with many rows (kvq_chunk_narrow.cu takes the others). Work plan and the states it leaves:
+// kvq_chunk.cuh.
 //
-// A CTA walks its segments page by page (64 tokens). Per page and tile of 128 query rows
-//   S [128 x 64]  = Q [128 x DK] . K^T          (A, B from shared memory; DK = 128, + 128 of the key sketch)
-//   O [128 x DV] += P [128 x 64] . V            (A from tensor memory; DV = 128, + 128 of the value sketch)
-// with K and V dequantised from the packed page into fp16 (kvq_chunk_dequant.cuh). NT row tiles share a page's dequantisation: two where tensor
-// memory holds their sums (O takes 2 x 128 columns, S 2 x 2 x 64), one with a value sketch (O 256).
+// A pair of CTAs (cta_group::2) walks its segments in steps of 128 tokens. Per step and tile of 256 query rows
+//   S [256 x 128] = Q [256 x DK] . K^T            (A, B from shared memory; DK = 128, + 128 of the key sketch)
+//   O [256 x DV] += P [256 x 128] . V              (A from tensor memory; DV = 128, + 128 of the value sketch)
+// with K and V dequantised from the packed pages into fp16 (kvq_chunk_dequant.cuh). Each CTA holds 128 rows of a
+// tile and makes half of either operand: keys, the tokens of one of the step's pages; values, half of the dims of
+// both. A CTA of its own makes all of them for as many rows and runs S in halves of 64 tokens, which read A from
+// shared memory twice (40-48 cycles a K step where the product takes 32): 2.72 ms on a 2048-token chunk of 64 heads
+// over 32768 tokens against MEASURED for pairs. NT row tiles share the operands: two where tensor memory holds their
+// sums (O takes 2 x 128 columns, S 2 x 128), one with a value sketch (O 256, S twice).
 //
 // Warps: 4 per row tile for the softmax (thread = row), 4 or 8 that dequantise keys (and fetch the queries of
-// a segment), 4 or 8 for values, 2 that issue the products (S, and P V one page behind; one thread issues an MMA
-// about every 50 cycles, so the two kinds run on two warps). K and V pages are staged twice, S twice per
-// tile, so that dequantisation, S, softmax and P V of neighbouring pages overlap. P overwrites the first
-// 32 columns of its S.
+// a segment), 4 or 8 for values, and in the first CTA 2 that issue the products, S and P V. K and V are staged
+// twice; two tiles, or two S of one, alternate, so that the softmax of one runs under the products of the other.
+// P overwrites the first half of its S. Barriers that the products wait for are the first CTA's, and the second
+// arrives there; those that they complete are told to both.
 //
 // Softmax weights are p = 2^(x - m + 7), m the row's maximum but for steps under 2^8, by which it may lag
 // before O is rescaled: p stays under 2^15 in fp16, and a weight is dropped only below 2^-31 of the largest.
@@ -25,28 +30,30 @@ namespace {
 using namespace chunk;
 
 constexpr int kStages = 2;
-constexpr int kTileRows = 128;
+constexpr int kTileRows = 128;        // of a CTA
+constexpr int kStep = 2 * kPage;
 constexpr float kLag = 8.f, kShift = 7.f;
 constexpr uint32_t kColS = 256, kTmemCols = 512;
 
 template <bool KQ, bool VQ>
 struct Cfg {
-  static constexpr int NT = VQ ? 1 : 2;
+  static constexpr int NT = VQ ? 1 : 2, NB = 2 / NT;  // row tiles, and S of each
   static constexpr int DK = KQ ? 256 : 128, DV = VQ ? 256 : 128;
-  // groups of 4 warps that dequantise a side, page n on group n % G: two where a sketch doubles the work
+  // groups of 4 warps that dequantise a side, step n on group n % G: two where a sketch doubles the work
   static constexpr int KG = KQ ? 2 : 1, VG = VQ ? 2 : 1;
   static constexpr int kWarpK = 4 * NT, kWarpV = kWarpK + 4 * KG, kWarpS = kWarpV + 4 * VG, kWarpO = kWarpS + 1;
   static constexpr int kThreads = 32 * (kWarpO + 1);
-  static constexpr int kQTile = kTileRows * DK * 2, kKStage = kPage * DK * 2, kVStage = kPage * DV * 2;
+  static constexpr int kKAtom = kPage * 128, kVAtom = DV / 2 * 128;  // operand atoms of 64 K-elements, this CTA's rows
+  static constexpr int kQTile = kTileRows * DK * 2, kKStage = DK / 64 * kKAtom, kVStage = 2 * kVAtom;
   static constexpr int kOffK = NT * kQTile, kOffV = kOffK + kStages * kKStage, kOffEnd = kOffV + kStages * kVStage;
 };
 
-template <int NT>
+template <int NT, int NB>
 struct Bars {
-  uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages];
-  uint64_t sfull[NT][2], pready[NT][2], pvdone[NT][2];
-  uint64_t qfull, qempty, done[2];
-  unsigned char vbad[kStages][8];  // tokens of the page whose value norm is not finite, a bit each
+  uint64_t kfull[kStages], vfull[kStages], pready[NT][NB], qfull;                  // the first CTA's count both
+  uint64_t kempty[kStages], vempty[kStages], sfull[NT][NB], pvdone[NT][NB], qempty, done[2];
+  uint64_t vhere[kStages];          // this CTA's values (and mask) are there
+  unsigned char vbad[kStages][16];  // tokens of the step whose value norm is not finite, a bit each
   uint32_t tmem;
   int fail;
 };
@@ -96,44 +103,55 @@ __device__ __forceinline__ F2 ex2_fma(F2 x) {
   t.get(a, b);
   return mul(y, F2(__int_as_float(__float_as_int(a) * (1 << 23) + 0x3f800000), __int_as_float(__float_as_int(b) * (1 << 23) + 0x3f800000)));
 }
-__device__ __forceinline__ int segment_pages(const Walk& w) { return max(0, min(w.k1, (w.rows.limit + kPage - 1) / kPage) - w.k0); }
+
+__device__ __forceinline__ int segment_steps(const Walk& w) { return max(0, min(w.k1, (w.rows.limit + kStep - 1) / kStep) - w.k0); }
+
+// Of a warp whose threads have written operand rows (or P): visible to the pair's products, one arrival at the first CTA.
+__device__ __forceinline__ void arrive_first(uint64_t& bar) {
+  fence_proxy_async();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive_at(smem_addr(&bar), 0);
+}
 
 template <bool KQ, bool VQ>
 __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __grid_constant__ ChunkParams p) {
   using C = Cfg<KQ, VQ>;
-  constexpr int NT = C::NT, DK = C::DK, DV = C::DV;
+  constexpr int NT = C::NT, NB = C::NB, DK = C::DK, DV = C::DV;
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ __align__(8) Bars<NT> bars;
+  __shared__ __align__(16) Bars<NT, NB> bars;
   const ChunkSet& set = p.set[kWide];
   if (set.head[1] == 0) return;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const int rank = (int)cluster_rank(), pair = blockIdx.x >> 1;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_addr(&bars.kfull[i]), 4);
+      mbar_init(smem_addr(&bars.kfull[i]), 8);
       mbar_init(smem_addr(&bars.kempty[i]), 1);
-      mbar_init(smem_addr(&bars.vfull[i]), 4);
+      mbar_init(smem_addr(&bars.vfull[i]), 8);
       mbar_init(smem_addr(&bars.vempty[i]), 1);
+      mbar_init(smem_addr(&bars.vhere[i]), 4);
     }
     for (int t = 0; t < NT; ++t)
-      for (int b = 0; b < 2; ++b) {
+      for (int b = 0; b < NB; ++b) {
         mbar_init(smem_addr(&bars.sfull[t][b]), 1);
-        mbar_init(smem_addr(&bars.pready[t][b]), 4);
+        mbar_init(smem_addr(&bars.pready[t][b]), 8);
         mbar_init(smem_addr(&bars.pvdone[t][b]), 1);
       }
-    mbar_init(smem_addr(&bars.qfull), 4 * C::KG);
+    mbar_init(smem_addr(&bars.qfull), 8 * C::KG);
     mbar_init(smem_addr(&bars.qempty), 1);
     mbar_init(smem_addr(&bars.done[0]), 1);
     mbar_init(smem_addr(&bars.done[1]), 1);
     mbar_init_fence();
     bars.fail = 0;
   }
-  if (warp == 0) tc::alloc(smem_addr(&bars.tmem), kTmemCols);
+  if (warp == 0) tc::pair_alloc(smem_addr(&bars.tmem), kTmemCols);
   tc::fence_before();
   __syncthreads();
+  cluster_sync();  // both CTAs' barriers and tensor memory are there
   tc::fence_after();
   const uint32_t tmem = bars.tmem;
   const uint32_t sm = smem_addr(smem);
-  // a wait that gives up ends every later one at once; the loops are bounded by the plan
+  // a wait that gives up ends every later one of its CTA at once; the loops are bounded by the plan
   auto wait = [&](uint64_t& bar, uint32_t parity) {
     const uint32_t a = smem_addr(&bar);
     if (mbar_try(a, parity) || *(volatile int*)&bars.fail) return;
@@ -142,35 +160,44 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
       atomicOr(p.err, 1);
     }
   };
+  auto wait_both = [&](uint64_t& bar, uint32_t parity) {  // for arrivals of both CTAs
+    if (*(volatile int*)&bars.fail) return;
+    if (!mbar_wait_cluster(smem_addr(&bar), parity, p.wait_limit)) {
+      bars.fail = 1;
+      atomicOr(p.err, 1);
+    }
+  };
   Walk w;
-  w.init(p, set, blockIdx.x);
+  w.init(p, set, pair);
 
   if (warp < C::kWarpK) {  // ---- softmax: thread = row
-    const int t = warp >> 2, row = tid;  // row of the NT * 128
+    const int t = warp >> 2, row = t * 2 * kTileRows + rank * kTileRows + (tid & 127);  // of the NT * 256
+    const int row0 = row & ~31;                                                    // of this warp
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t tO = tmem + lanes + t * DV, tS = tmem + lanes + kColS + t * 128;
-    int n = 0, nv = 0;  // pages this tile, and the CTA, has seen
+    const uint32_t tO = tmem + lanes + t * DV, tS = tmem + lanes + kColS + t * NB * kStep;
+    int n = 0, nv = 0;  // steps this tile, and the pair, has seen
     while (w.next(p, set)) {
       const Rows r = w.rows;
-      const int np = segment_pages(w);
-      const bool used = t * kTileRows < r.count && np > 0;
-      const bool work = warp * 32 < r.count;
+      const int ns = segment_steps(w);
+      const bool used = t * 2 * kTileRows < r.count && ns > 0;
+      const bool work = row0 < r.count;
       // rows of no token count as unmasked: what they compute is not kept, and the others' mask may still be empty
       const int last = row < r.count ? min(r.pos0 + row / p.group, r.ctx - 1) : 0x7fffffff;
       float qs = 1.f;
       if (row < r.count)
         qs = p.qscale[(size_t)(r.start + r.first + row / p.group) * p.Hq + w.hk * p.group + row % p.group];
       float m = -INFINITY, ref = 0.f, l = 0.f;
-      for (int j = 0; used && j < np; ++j, ++n) {
-        const int b = n & 1, st = (nv + j) % kStages;
-        wait(bars.sfull[t][b], (n >> 1) & 1);
+      for (int j = 0; used && j < ns; ++j, ++n) {
+        const int b = n % NB, st = (nv + j) % kStages;
+        wait(bars.sfull[t][b], (n / NB) & 1);
         tc::fence_after();
         if (work) {
-          // two halves of 32 columns, read from tensor memory again for the second pass: a rolled loop (see expand)
-          const int reach = last - (w.k0 + j) * kPage;  // the page's tokens 0 .. reach are attended
-          const bool full = __all_sync(0xffffffffu, reach >= kPage - 1);
+          // quarters of 32 columns, read from tensor memory again for the second pass: rolled loops (the code of all
+          // roles has to stay in the instruction cache)
+          const int reach = last - (w.k0 + j) * kStep;  // the step's tokens 0 .. reach are attended
+          const bool full = __all_sync(0xffffffffu, reach >= kStep - 1);
           auto logits = [&](uint32_t (&s)[32], int c) {
-            tc::tmem_ld32(tS + 64 * b + c, s);
+            tc::tmem_ld32(tS + kStep * b + c, s);
             tc::wait_ld();
             if (!full) {
 #pragma unroll
@@ -179,7 +206,7 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
           };
           float mx2[2] = {-INFINITY, -INFINITY};
 #pragma unroll 1
-          for (int c = 0; c < kPage; c += 32) {
+          for (int c = 0; c < kStep; c += 32) {
             uint32_t s[32];
             logits(s, c);
 #pragma unroll
@@ -196,7 +223,7 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
             }
             l *= alpha;
             if (j > 0) {
-              wait(bars.pvdone[t][(n - 1) & 1], ((n - 1) >> 1) & 1);
+              wait(bars.pvdone[t][(n - 1) % NB], ((n - 1) / NB) & 1);
               tc::fence_after();
 #pragma unroll 1
               for (int c = 0; c < DV; c += 16) {
@@ -213,7 +240,7 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
           F2 sum[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
           const F2 qs2(qs, qs), ref2(-ref, -ref);
 #pragma unroll 1
-          for (int c = 0; c < kPage; c += 32) {
+          for (int c = 0; c < kStep; c += 32) {
             uint32_t s[32], ph[16];
             logits(s, c);
 #pragma unroll
@@ -233,29 +260,32 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
               const __half2 h = __floats2half2_rn(a, d);
               ph[i] = *reinterpret_cast<const uint32_t*>(&h);
             }
-            tc::tmem_st16(tS + 64 * b + c / 2, ph);
+            tc::tmem_st16(tS + kStep * b + c / 2, ph);
           }
           float la, lb;
           add(sum[0], sum[1]).get(la, lb);
           l += la + lb;
-          wait(bars.vfull[st], ((nv + j) / kStages) & 1);
-          const unsigned long long bad = *reinterpret_cast<const volatile unsigned long long*>(bars.vbad[st]);
-          if (bad != 0 && reach >= 0 && (bad & (~0ull >> (63 - min(reach, 63)))) != 0) l = NAN;
+          wait(bars.vhere[st], ((nv + j) / kStages) & 1);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const unsigned long long bad = reinterpret_cast<const volatile unsigned long long*>(bars.vbad[st])[h];
+            const int to = reach - 64 * h;
+            if (bad != 0 && to >= 0 && (bad & (~0ull >> (63 - min(to, 63)))) != 0) l = NAN;
+          }
           tc::wait_st();
         }
         tc::fence_before();
-        __syncwarp();
-        if ((tid & 31) == 0) mbar_arrive(smem_addr(&bars.pready[t][b]));
+        arrive_first(bars.pready[t][b]);
       }
-      nv += np;
+      nv += ns;
       // the segment's state
       if (used) {
-        wait(bars.pvdone[t][(n - 1) & 1], ((n - 1) >> 1) & 1);
+        wait(bars.pvdone[t][(n - 1) % NB], ((n - 1) / NB) & 1);
         tc::fence_after();
       }
       if (work) {
-        float* ml = segment_ml(set, w.item, blockIdx.x, DV) + 2 * row;
-        float* so = segment_o(set, w.item, blockIdx.x, DV) + (size_t)row * DV;
+        float* ml = segment_ml(set, w.item, pair, DV) + 2 * row;
+        float* so = segment_o(set, w.item, pair, DV) + (size_t)row * DV;
         if (row < r.count) *reinterpret_cast<float2*>(ml) = make_float2(m == -INFINITY ? m : ref, m == -INFINITY && l == l ? 0.f : l);
 #pragma unroll 1
         for (int c = 0; c < DV; c += 16) {
@@ -264,151 +294,163 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
             tc::tmem_ld16(tO + c, o);
             tc::wait_ld();
           }
+          // with a sketch each CTA's half of the columns is 64 codes, 64 signs
+          const int dim = VQ ? (c & 63) + (c & 128) / 2 + (c & 64) * 2 : c;
           if (row < r.count)
 #pragma unroll
             for (int i = 0; i < 16; i += 4)
-              *reinterpret_cast<uint4*>(so + c + i) =
+              *reinterpret_cast<uint4*>(so + dim + i) =
                   used ? make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]) : make_uint4(0, 0, 0, 0);
         }
       }
       tc::fence_before();
     }
-  } else if (warp < C::kWarpV) {  // ---- keys, and the queries of each segment
+  } else if (warp < C::kWarpV) {  // ---- keys of page `rank` of every step, and the queries of each segment
     const int all = tid - 32 * C::kWarpK, th = all & 127, grp = all >> 7;
     KeyThread<KQ> keys;
-    keys.init(p, th, kPage * 128);
+    keys.init(p, th, C::kKAtom);
     const uint2 lut = code_halves(p.k);
     int n = 0, seg = 0;
     PageRegs regs = {};
     while (w.next(p, set)) {
       const Rows r = w.rows;
-      const int np = segment_pages(w);
-      if (np == 0) continue;
-      const int first = (grp + C::KG - n % C::KG) % C::KG;  // this group's first page of the segment
-      if (first < np) keys.fetch(p, regs, page_tile(p, w, w.k0 + first, page_entry(p, w, w.k0 + first)));
-      int entry = page_entry(p, w, w.k0 + first + C::KG);  // of the page after the one in regs
+      const int ns = segment_steps(w);
+      if (ns == 0) continue;
+      const int first = (grp + C::KG - n % C::KG) % C::KG;  // this group's first step of the segment
+      int page = 2 * (w.k0 + first) + rank;
+      if (page * kPage < r.limit) keys.fetch(p, regs, page_tile(p, w, page, page_entry(p, w, page)));
+      int entry = page_entry(p, w, page + 2 * C::KG);  // of the page after the one in regs
       if (seg > 0) wait(bars.qempty, (seg - 1) & 1);
       ++seg;
       constexpr int kChunks = DK / 8;
       const size_t qrow0 = (size_t)(r.start + r.first) * p.Hq + w.hk * p.group;
 #pragma unroll 8
       for (int i = all; i < NT * kTileRows * kChunks; i += 128 * C::KG) {
-        const int row = i / kChunks, ch = i % kChunks;
+        const int here = i / kChunks, ch = i % kChunks;
+        const int t = here / kTileRows, rr = here & (kTileRows - 1), row = t * 2 * kTileRows + rank * kTileRows + rr;
         uint4 v = make_uint4(0, 0, 0, 0);
         if (row < r.count)
           v = *(reinterpret_cast<const uint4*>(static_cast<const __half*>(p.qprep) +
                                                (qrow0 + (size_t)(row / p.group) * p.Hq + row % p.group) * DK) + ch);
-        const int rr = row & (kTileRows - 1);
-        *reinterpret_cast<uint4*>(smem + (row / kTileRows) * C::kQTile + (ch >> 3) * (kTileRows * 128) + rr * 128 +
+        *reinterpret_cast<uint4*>(smem + t * C::kQTile + (ch >> 3) * (kTileRows * 128) + rr * 128 +
                                   (((ch & 7) ^ (rr & 7)) << 4)) = v;
       }
-      arrive_rows(bars.qfull);
-      for (int j = first; j < np; j += C::KG) {
+      arrive_first(bars.qfull);
+      for (int j = first; j < ns; j += C::KG, page += 2 * C::KG) {
         const int nj = n + j, st = nj % kStages;
         const PageRegs cur = regs;
-        if (j + C::KG < np) {
-          keys.fetch(p, regs, page_tile(p, w, w.k0 + j + C::KG, entry));
-          entry = page_entry(p, w, w.k0 + j + 2 * C::KG);
+        if (j + C::KG < ns && (page + 2 * C::KG) * kPage < r.limit) {
+          keys.fetch(p, regs, page_tile(p, w, page + 2 * C::KG, entry));
+          entry = page_entry(p, w, page + 4 * C::KG);
         }
         if (nj >= kStages) wait(bars.kempty[st], (nj / kStages - 1) & 1);
-        const uint32_t base = sm + C::kOffK + st * C::kKStage;
-        keys.codes(p, cur, lut, base);
-        if (KQ) keys.signs(cur, base + 2 * kPage * 128);
-        arrive_rows(bars.kfull[st]);
+        if (page * kPage < r.limit) {  // a second page behind the limit stays as it was: its logits are masked
+          const uint32_t base = sm + C::kOffK + st * C::kKStage;
+          keys.codes(p, cur, lut, base);
+          if (KQ) keys.signs(cur, base + 2 * C::kKAtom);
+        }
+        arrive_first(bars.kfull[st]);
       }
-      n += np;
+      n += ns;
     }
-  } else if (warp < C::kWarpS) {  // ---- values: dims 8 k .. + 7 of tokens 8 c .. + 7
-    const int th = (tid - 32 * C::kWarpV) & 127, grp = (tid - 32 * C::kWarpV) >> 7;
+  } else if (warp < C::kWarpS) {  // ---- dims 64 rank .. + 63 of both pages' values
+    const int th = (tid - 32 * C::kWarpV) & 127, grp = (tid - 32 * C::kWarpV) >> 7, second = th >> 6;
     ValueThread<VQ> values;
-    values.init(th);
+    values.init(th & 7, 8 * rank + ((th >> 3) & 7), (th >> 3) & 7);
     const uint2 lut = code_halves(p.v);
     int n = 0;
     PageRegs regs = {};
     while (w.next(p, set)) {
-      const int np = segment_pages(w);
-      if (np == 0) continue;
-      const int first = (grp + C::VG - n % C::VG) % C::VG;  // this group's first page of the segment
-      if (first < np) values.fetch(p, regs, page_tile(p, w, w.k0 + first, page_entry(p, w, w.k0 + first)));
-      int entry = page_entry(p, w, w.k0 + first + C::VG);  // of the page after the one in regs
-      for (int j = first; j < np; j += C::VG) {
+      const int ns = segment_steps(w), limit = w.rows.limit;
+      if (ns == 0) continue;
+      const int first = (grp + C::VG - n % C::VG) % C::VG;  // this group's first step of the segment
+      int page = 2 * (w.k0 + first) + second;
+      if (page * kPage < limit) values.fetch(p, regs, page_tile(p, w, page, page_entry(p, w, page)));
+      int entry = page_entry(p, w, page + 2 * C::VG);  // of the page after the one in regs
+      for (int j = first; j < ns; j += C::VG, page += 2 * C::VG) {
         const int nj = n + j, st = nj % kStages;
         const PageRegs cur = regs;
-        const int limit = w.rows.limit - (w.k0 + j) * kPage;
-        if (j + C::VG < np) {
-          values.fetch(p, regs, page_tile(p, w, w.k0 + j + C::VG, entry));
-          entry = page_entry(p, w, w.k0 + j + 2 * C::VG);
+        if (j + C::VG < ns && (page + 2 * C::VG) * kPage < limit) {
+          values.fetch(p, regs, page_tile(p, w, page + 2 * C::VG, entry));
+          entry = page_entry(p, w, page + 4 * C::VG);
         }
         if (nj >= kStages) wait(bars.vempty[st], (nj / kStages - 1) & 1);
-        const uint32_t bad = values.store(p, cur, lut, sm + C::kOffV + st * C::kVStage, limit);
-        if (th < 8) bars.vbad[st][th] = (unsigned char)bad;
-        arrive_rows(bars.vfull[st]);
+        // a second page behind the limit enters as zeros
+        const uint32_t bad = values.store(p, cur, lut, sm + C::kOffV + st * C::kVStage + second * C::kVAtom, 64 * 128,
+                                          limit - page * kPage);
+        if ((th & 63) < 8) bars.vbad[st][8 * second + (th & 7)] = (unsigned char)bad;
+        arrive_first(bars.vfull[st]);
+        if ((tid & 31) == 0) mbar_arrive(smem_addr(&bars.vhere[st]));
       }
-      n += np;
+      n += ns;
     }
-  } else if (warp == C::kWarpS) {  // ---- S = Q K^T (the whole warp, so that control stays uniform)
-    constexpr uint32_t id = tc::idesc_f16(0, 0, 0, kTileRows, kPage);
+  } else if (rank == 0 && warp == C::kWarpS) {  // ---- S = Q K^T (the whole warp, so that control stays uniform)
+    constexpr uint32_t id = tc::idesc_f16(0, 0, 0, 2 * kTileRows, kStep);
     int n = 0, seg = 0, nt[NT] = {};
     while (w.next(p, set)) {
-      const int np = __shfl_sync(0xffffffffu, segment_pages(w), 0), count = __shfl_sync(0xffffffffu, w.rows.count, 0);
-      if (np == 0) continue;
-      wait(bars.qfull, seg & 1);
+      const int ns = __shfl_sync(0xffffffffu, segment_steps(w), 0), count = __shfl_sync(0xffffffffu, w.rows.count, 0);
+      if (ns == 0) continue;
+      wait_both(bars.qfull, seg & 1);
       ++seg;
-      for (int j = 0; j < np; ++j, ++n) {
+      for (int j = 0; j < ns; ++j, ++n) {
         const int st = n % kStages;
-        wait(bars.kfull[st], (n / kStages) & 1);
+        wait_both(bars.kfull[st], (n / kStages) & 1);
         const uint64_t kd = desc_sw128(sm + C::kOffK + st * C::kKStage);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          if (t * kTileRows >= count) continue;
-          const int b = nt[t] & 1;
-          if (nt[t] >= 2) wait(bars.pvdone[t][b], ((nt[t] >> 1) - 1) & 1);  // P of two pages before is read
+          if (t * 2 * kTileRows >= count) continue;
+          const int b = nt[t] % NB;
+          if (nt[t] >= NB) wait(bars.pvdone[t][b], (nt[t] / NB - 1) & 1);  // the P that lies there is read
           tc::fence_after();
           const uint64_t qd = desc_sw128(sm + t * C::kQTile);
 #pragma unroll
           for (int i = 0; i < DK / 64; ++i)
-            tc::umma_f16_x4(tmem + kColS + t * 128 + b * 64, qd + ((i * kTileRows * 128) >> 4), kd + ((i * kPage * 128) >> 4), id,
-                            i > 0);
-          tc::commit_elected(smem_addr(&bars.sfull[t][b]));
+            tc::pair_f16_x4(tmem + kColS + (t * NB + b) * kStep, qd + ((i * kTileRows * 128) >> 4), kd + ((i * C::kKAtom) >> 4),
+                            id, i > 0);
+          tc::pair_commit(smem_addr(&bars.sfull[t][b]));
           ++nt[t];
         }
-        tc::commit_elected(smem_addr(&bars.kempty[st]));
+        tc::pair_commit(smem_addr(&bars.kempty[st]));
       }
-      tc::commit_elected(smem_addr(&bars.qempty));
+      tc::pair_commit(smem_addr(&bars.qempty));
     }
-    tc::commit_elected(smem_addr(&bars.done[0]));
+    tc::pair_commit(smem_addr(&bars.done[0]));
     mbar_wait(smem_addr(&bars.done[0]), 0, p.wait_limit);
-  } else {  // ---- O += P V
-    constexpr uint32_t id = tc::idesc_f16(0, 0, 0, kTileRows, DV);
+  } else if (rank == 0) {  // ---- O += P V
+    constexpr uint32_t id = tc::idesc_f16(0, 0, 0, 2 * kTileRows, DV);
     int n = 0, nt[NT] = {};
     while (w.next(p, set)) {
-      const int np = __shfl_sync(0xffffffffu, segment_pages(w), 0), count = __shfl_sync(0xffffffffu, w.rows.count, 0);
-      for (int j = 0; j < np; ++j, ++n) {
+      const int ns = __shfl_sync(0xffffffffu, segment_steps(w), 0), count = __shfl_sync(0xffffffffu, w.rows.count, 0);
+      for (int j = 0; j < ns; ++j, ++n) {
         const int st = n % kStages;
-        wait(bars.vfull[st], (n / kStages) & 1);
+        wait_both(bars.vfull[st], (n / kStages) & 1);
         const uint64_t vd = desc_sw128(sm + C::kOffV + st * C::kVStage);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          if (t * kTileRows >= count) continue;
-          const int b = nt[t] & 1;
-          wait(bars.pready[t][b], (nt[t] >> 1) & 1);
+          if (t * 2 * kTileRows >= count) continue;
+          const int b = nt[t] % NB;
+          wait_both(bars.pready[t][b], (nt[t] / NB) & 1);
           tc::fence_after();
-          tc::umma_f16_ta_x4(tmem + t * DV, tmem + kColS + t * 128 + b * 64, vd, id, j > 0);
-          tc::commit_elected(smem_addr(&bars.pvdone[t][b]));
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            tc::pair_f16_ta_x4(tmem + t * DV, tmem + kColS + (t * NB + b) * kStep + 32 * i, vd + ((i * C::kVAtom) >> 4), id,
+                               j > 0 || i > 0);
+          tc::pair_commit(smem_addr(&bars.pvdone[t][b]));
           ++nt[t];
         }
-        tc::commit_elected(smem_addr(&bars.vempty[st]));
+        tc::pair_commit(smem_addr(&bars.vempty[st]));
       }
     }
-    tc::commit_elected(smem_addr(&bars.done[1]));
+    tc::pair_commit(smem_addr(&bars.done[1]));
     mbar_wait(smem_addr(&bars.done[1]), 0, p.wait_limit);
   }
   __syncwarp();
   tc::fence_before();
   __syncthreads();
+  cluster_sync();  // the products are done, and no arrival is on its way to a CTA that has left
   if (warp == 0) {
     tc::fence_after();
-    tc::dealloc(tmem, kTmemCols);
+    tc::pair_dealloc(tmem, kTmemCols);
   }
 }
 
@@ -417,13 +459,25 @@ cudaError_t launch(const ChunkParams& p, cudaStream_t s) {
   constexpr int smem = Cfg<KQ, VQ>::kOffEnd;
   const cudaError_t e = cudaFuncSetAttribute(chunk_umma<KQ, VQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  chunk_umma<KQ, VQ><<<p.ctas, Cfg<KQ, VQ>::kThreads, smem, s>>>(p);
-  return launched();
+  cudaLaunchConfig_t config = {};
+  config.gridDim = dim3(2 * p.set[kWide].ctas);
+  config.blockDim = dim3(Cfg<KQ, VQ>::kThreads);
+  config.dynamicSmemBytes = smem;
+  config.stream = s;
+  cudaLaunchAttribute pairs;
+  pairs.id = cudaLaunchAttributeClusterDimension;
+  pairs.val.clusterDim.x = 2;
+  pairs.val.clusterDim.y = pairs.val.clusterDim.z = 1;
+  config.attrs = &pairs;
+  config.numAttrs = 1;
+  const cudaError_t launch_error = cudaLaunchKernelEx(&config, chunk_umma<KQ, VQ>, p);
+  const cudaError_t counted = launched();
+  return launch_error != cudaSuccess ? launch_error : counted;
 }
 
 }  // namespace
 
-int chunk_umma_rows(bool v_qjl) { return kTileRows * (v_qjl ? Cfg<true, true>::NT : Cfg<true, false>::NT); }
+int chunk_umma_rows(bool v_qjl) { return 2 * kTileRows * (v_qjl ? Cfg<true, true>::NT : Cfg<true, false>::NT); }
 
 cudaError_t launch_chunk_umma(const ChunkParams& p, cudaStream_t s) {
   if (p.k.qjl) return p.v.qjl ? launch<true, true>(p, s) : launch<true, false>(p, s);

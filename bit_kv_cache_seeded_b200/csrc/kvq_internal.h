@@ -188,6 +188,7 @@ struct ChunkSet {
   int above, upto;          // rows of a request: above < rows <= upto
   int rows;                 // query rows of a row tile
   int unit;                 // tokens of a unit
+  int ctas;                 // CTAs (wide set: pairs of them) that share the units
   int max_tiles;            // row tiles of one kv-head the workspace holds
   long long* unit_start;    // [max_tiles + 1]
   int* tile_seq;            // [max_tiles]
@@ -219,8 +220,8 @@ struct ChunkParams {
   float logit_scale;        // softmax_scale * log2(e)
   int* err;
   long long wait_limit;
+  int sms;
   // workspace
-  int ctas;                 // CTAs that share a set's units
   int sets;
   ChunkSet set[2];
   void* qprep;              // rotated (and sketched) queries
@@ -230,10 +231,10 @@ struct ChunkParams {
 // A chunk call's workspace: its sets with byte offsets in place of the pointers.
 struct ChunkLayout {
   struct Set {
-    int above, upto, rows, unit, max_tiles;
+    int above, upto, rows, unit, ctas, max_tiles;
     size_t unit_start, tile_seq, tile_start, head, part;
   } set[2];
-  int ctas, sets;
+  int sets;
   size_t qprep, qscale, total;
 };
 
