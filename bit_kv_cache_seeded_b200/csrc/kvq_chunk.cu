@@ -707,7 +707,7 @@ ChunkLayout chunk_layout(int n_tokens, int batch, int Hq, int Hkv, bool k_qjl, b
     s.above = bf16 && i == kWide ? kNarrowRows : 0;
     s.upto = i == kNarrow ? kNarrowRows : 0x7fffffff;
     s.rows = i == kNarrow ? kNarrowRows : bf16 ? chunk_umma_rows(v_qjl) : kF32Rows;
-    s.unit = bf16 ? 2 * kPage : kPage;
+    s.unit = i == kNarrow ? 2 * kPage : kPage;
     s.ctas = bf16 && i == kWide ? std::max(sms / 2, 1) : sms;
     // requests of a set have above / group + 1 tokens at least, a tile each and one per `rows` rows
     s.max_tiles = std::min(batch, n_tokens / (s.above / group + 1));

@@ -2,20 +2,20 @@
 // queries of requests with many rows (kvq_chunk_narrow.cu takes the others). Work plan and the states it leaves:
 // kvq_chunk.cuh.
 //
-// A pair of CTAs (cta_group::2) walks its segments in steps of 128 tokens. Per step and tile of 256 query rows
-//   S [256 x 128] = Q [256 x DK] . K^T            (A, B from shared memory; DK = 128, + 128 of the key sketch)
-//   O [256 x DV] += P [256 x 128] . V              (A from tensor memory; DV = 128, + 128 of the value sketch)
-// with K and V dequantised from the packed pages into fp16 (kvq_chunk_dequant.cuh). Each CTA holds 128 rows of a
-// tile and makes half of either operand: keys, the tokens of one of the step's pages; values, half of the dims of
-// both. A CTA of its own makes all of them for as many rows and runs S in halves of 64 tokens, which read A from
-// shared memory twice (40-48 cycles a K step where the product takes 32): 2.72 ms on a 2048-token chunk of 64 heads
-// over 32768 tokens against MEASURED for pairs. NT row tiles share the operands: two where tensor memory holds their
-// sums (O takes 2 x 128 columns, S 2 x 128), one with a value sketch (O 256, S twice).
+// A pair of CTAs (cta_group::2) walks its segments page by page (64 tokens). Per page and tile of 256 query rows
+//   S [256 x 64] = Q [256 x DK] . K^T             (A, B from shared memory; DK = 128, + 128 of the key sketch)
+//   O [256 x DV] += P [256 x 64] . V               (A from tensor memory; DV = 128, + 128 of the value sketch)
+// with K and V dequantised from the packed page into fp16 (kvq_chunk_dequant.cuh). Each CTA holds 128 rows of a
+// tile and makes half of either operand: keys, 32 of the tokens; values, 64 of the dims. NT row tiles share the
+// operands: two where tensor memory holds their sums (O takes 2 x 128 columns, S 2 x 2 x 64), one with a value
+// sketch (O 256). Measured on a 2048-token chunk of 64 heads over 32768 tokens: MEASURED; a CTA of its own, which
+// dequantises everything for half as many rows, 2.72 ms; pairs with S over 128 tokens, which leaves tensor memory
+// for one S a tile and so puts S, softmax and P V of a tile in a row, 2.79.
 //
 // Warps: 4 per row tile for the softmax (thread = row), 4 or 8 that dequantise keys (and fetch the queries of
 // a segment), 4 or 8 for values, and in the first CTA 2 that issue the products, S and P V. K and V are staged
-// twice; two tiles, or two S of one, alternate, so that the softmax of one runs under the products of the other.
-// P overwrites the first half of its S. Barriers that the products wait for are the first CTA's, and the second
+// four times, S twice per tile, so that dequantisation, S, softmax and P V of neighbouring pages overlap. P
+// overwrites the first half of its S. Barriers that the products wait for are the first CTA's, and the second
 // arrives there; those that they complete are told to both.
 //
 // Softmax weights are p = 2^(x - m + 7), m the row's maximum but for steps under 2^8, by which it may lag
@@ -29,22 +29,21 @@ namespace {
 
 using namespace chunk;
 
-constexpr int kStages = 2;
+constexpr int kStages = 4;
 constexpr int kTileRows = 128;        // of a CTA
-constexpr int kStep = 2 * kPage;
 constexpr float kLag = 8.f, kShift = 7.f;
 constexpr uint32_t kColS = 256, kTmemCols = 512;
 
 template <bool KQ, bool VQ>
 struct Cfg {
-  static constexpr int NT = VQ ? 1 : 2, NB = 2 / NT;  // row tiles, and S of each
+  static constexpr int NT = VQ ? 1 : 2, NB = 2;  // row tiles, and S of each
   static constexpr int DK = KQ ? 256 : 128, DV = VQ ? 256 : 128;
-  // groups of 4 warps that dequantise a side, step n on group n % G: two where a sketch doubles the work
-  static constexpr int KG = KQ ? 2 : 1, VG = VQ ? 2 : 1;
-  static constexpr int kWarpK = 4 * NT, kWarpV = kWarpK + 4 * KG, kWarpS = kWarpV + 4 * VG, kWarpO = kWarpS + 1;
+  // groups of 2 warps that dequantise a side, page n on group n % G: twice as many where a sketch doubles the work
+  static constexpr int KG = KQ ? 4 : 2, VG = VQ ? 4 : 2;
+  static constexpr int kWarpK = 4 * NT, kWarpV = kWarpK + 2 * KG, kWarpS = kWarpV + 2 * VG, kWarpO = kWarpS + 1;
   static constexpr int kThreads = 32 * (kWarpO + 1);
-  static constexpr int kKAtom = kPage * 128, kVAtom = DV / 2 * 128;  // operand atoms of 64 K-elements, this CTA's rows
-  static constexpr int kQTile = kTileRows * DK * 2, kKStage = DK / 64 * kKAtom, kVStage = 2 * kVAtom;
+  static constexpr int kKAtom = kTile * 128, kVAtom = DV / 2 * 128;  // operand atoms of 64 K-elements, this CTA's rows
+  static constexpr int kQTile = kTileRows * DK * 2, kKStage = DK / 64 * kKAtom, kVStage = kVAtom;
   static constexpr int kOffK = NT * kQTile, kOffV = kOffK + kStages * kKStage, kOffEnd = kOffV + kStages * kVStage;
 };
 
@@ -53,7 +52,7 @@ struct Bars {
   uint64_t kfull[kStages], vfull[kStages], pready[NT][NB], qfull;                  // the first CTA's count both
   uint64_t kempty[kStages], vempty[kStages], sfull[NT][NB], pvdone[NT][NB], qempty, done[2];
   uint64_t vhere[kStages];          // this CTA's values (and mask) are there
-  unsigned char vbad[kStages][16];  // tokens of the step whose value norm is not finite, a bit each
+  unsigned char vbad[kStages][8];   // tokens of the page whose value norm is not finite, a bit each
   uint32_t tmem;
   int fail;
 };
@@ -104,9 +103,9 @@ __device__ __forceinline__ F2 ex2_fma(F2 x) {
   return mul(y, F2(__int_as_float(__float_as_int(a) * (1 << 23) + 0x3f800000), __int_as_float(__float_as_int(b) * (1 << 23) + 0x3f800000)));
 }
 
-__device__ __forceinline__ int segment_steps(const Walk& w) { return max(0, min(w.k1, (w.rows.limit + kStep - 1) / kStep) - w.k0); }
+__device__ __forceinline__ int segment_pages(const Walk& w) { return max(0, min(w.k1, (w.rows.limit + kPage - 1) / kPage) - w.k0); }
 
-// Of a warp whose threads have written operand rows (or P): visible to the pair's products, one arrival at the first CTA.
+// Of a warp whose threads have written operand rows: visible to the pair's products, one arrival at the first CTA.
 __device__ __forceinline__ void arrive_first(uint64_t& bar) {
   fence_proxy_async();
   __syncwarp();
@@ -125,11 +124,11 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
   const int rank = (int)cluster_rank(), pair = blockIdx.x >> 1;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_addr(&bars.kfull[i]), 8);
+      mbar_init(smem_addr(&bars.kfull[i]), 4);
       mbar_init(smem_addr(&bars.kempty[i]), 1);
-      mbar_init(smem_addr(&bars.vfull[i]), 8);
+      mbar_init(smem_addr(&bars.vfull[i]), 4);
       mbar_init(smem_addr(&bars.vempty[i]), 1);
-      mbar_init(smem_addr(&bars.vhere[i]), 4);
+      mbar_init(smem_addr(&bars.vhere[i]), 2);
     }
     for (int t = 0; t < NT; ++t)
       for (int b = 0; b < NB; ++b) {
@@ -137,7 +136,7 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
         mbar_init(smem_addr(&bars.pready[t][b]), 8);
         mbar_init(smem_addr(&bars.pvdone[t][b]), 1);
       }
-    mbar_init(smem_addr(&bars.qfull), 8 * C::KG);
+    mbar_init(smem_addr(&bars.qfull), 4 * C::KG);
     mbar_init(smem_addr(&bars.qempty), 1);
     mbar_init(smem_addr(&bars.done[0]), 1);
     mbar_init(smem_addr(&bars.done[1]), 1);
@@ -174,11 +173,11 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
     const int t = warp >> 2, row = t * 2 * kTileRows + rank * kTileRows + (tid & 127);  // of the NT * 256
     const int row0 = row & ~31;                                                    // of this warp
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t tO = tmem + lanes + t * DV, tS = tmem + lanes + kColS + t * NB * kStep;
-    int n = 0, nv = 0;  // steps this tile, and the pair, has seen
+    const uint32_t tO = tmem + lanes + t * DV, tS = tmem + lanes + kColS + t * NB * kPage;
+    int n = 0, nv = 0;  // pages this tile, and the pair, has seen
     while (w.next(p, set)) {
       const Rows r = w.rows;
-      const int ns = segment_steps(w);
+      const int ns = segment_pages(w);
       const bool used = t * 2 * kTileRows < r.count && ns > 0;
       const bool work = row0 < r.count;
       // rows of no token count as unmasked: what they compute is not kept, and the others' mask may still be empty
@@ -192,12 +191,12 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
         wait(bars.sfull[t][b], (n / NB) & 1);
         tc::fence_after();
         if (work) {
-          // quarters of 32 columns, read from tensor memory again for the second pass: rolled loops (the code of all
+          // halves of 32 columns, read from tensor memory again for the second pass: rolled loops (the code of all
           // roles has to stay in the instruction cache)
-          const int reach = last - (w.k0 + j) * kStep;  // the step's tokens 0 .. reach are attended
-          const bool full = __all_sync(0xffffffffu, reach >= kStep - 1);
+          const int reach = last - (w.k0 + j) * kPage;  // the page's tokens 0 .. reach are attended
+          const bool full = __all_sync(0xffffffffu, reach >= kPage - 1);
           auto logits = [&](uint32_t (&s)[32], int c) {
-            tc::tmem_ld32(tS + kStep * b + c, s);
+            tc::tmem_ld32(tS + kPage * b + c, s);
             tc::wait_ld();
             if (!full) {
 #pragma unroll
@@ -206,7 +205,7 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
           };
           float mx2[2] = {-INFINITY, -INFINITY};
 #pragma unroll 1
-          for (int c = 0; c < kStep; c += 32) {
+          for (int c = 0; c < kPage; c += 32) {
             uint32_t s[32];
             logits(s, c);
 #pragma unroll
@@ -240,7 +239,7 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
           F2 sum[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
           const F2 qs2(qs, qs), ref2(-ref, -ref);
 #pragma unroll 1
-          for (int c = 0; c < kStep; c += 32) {
+          for (int c = 0; c < kPage; c += 32) {
             uint32_t s[32], ph[16];
             logits(s, c);
 #pragma unroll
@@ -260,22 +259,19 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
               const __half2 h = __floats2half2_rn(a, d);
               ph[i] = *reinterpret_cast<const uint32_t*>(&h);
             }
-            tc::tmem_st16(tS + kStep * b + c / 2, ph);
+            tc::tmem_st16(tS + kPage * b + c / 2, ph);
           }
           float la, lb;
           add(sum[0], sum[1]).get(la, lb);
           l += la + lb;
           wait(bars.vhere[st], ((nv + j) / kStages) & 1);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const unsigned long long bad = reinterpret_cast<const volatile unsigned long long*>(bars.vbad[st])[h];
-            const int to = reach - 64 * h;
-            if (bad != 0 && to >= 0 && (bad & (~0ull >> (63 - min(to, 63)))) != 0) l = NAN;
-          }
+          const unsigned long long bad = *reinterpret_cast<const volatile unsigned long long*>(bars.vbad[st]);
+          if (bad != 0 && reach >= 0 && (bad & (~0ull >> (63 - min(reach, 63)))) != 0) l = NAN;
           tc::wait_st();
         }
         tc::fence_before();
-        arrive_first(bars.pready[t][b]);
+        __syncwarp();
+        if ((tid & 31) == 0) mbar_arrive_at_tmem(smem_addr(&bars.pready[t][b]), 0);
       }
       nv += ns;
       // the segment's state
@@ -305,27 +301,28 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
       }
       tc::fence_before();
     }
-  } else if (warp < C::kWarpV) {  // ---- keys of page `rank` of every step, and the queries of each segment
-    const int all = tid - 32 * C::kWarpK, th = all & 127, grp = all >> 7;
+  } else if (warp < C::kWarpV) {  // ---- keys of 32 tokens of a page, and the queries of each segment
+    const int all = tid - 32 * C::kWarpK, grp = all >> 6;
     KeyThread<KQ> keys;
-    keys.init(p, th, C::kKAtom);
+    keys.init(p, (all & 63) + 64 * rank, C::kKAtom);
+    keys.row_off -= rank * C::kKAtom;  // the page's second 32 rows come first here
     const uint2 lut = code_halves(p.k);
     int n = 0, seg = 0;
     PageRegs regs = {};
     while (w.next(p, set)) {
       const Rows r = w.rows;
-      const int ns = segment_steps(w);
+      const int ns = segment_pages(w);
       if (ns == 0) continue;
-      const int first = (grp + C::KG - n % C::KG) % C::KG;  // this group's first step of the segment
-      int page = 2 * (w.k0 + first) + rank;
-      if (page * kPage < r.limit) keys.fetch(p, regs, page_tile(p, w, page, page_entry(p, w, page)));
-      int entry = page_entry(p, w, page + 2 * C::KG);  // of the page after the one in regs
+      const int first = (grp + C::KG - n % C::KG) % C::KG;  // this group's first page of the segment
+      int page = w.k0 + first;
+      if (first < ns) keys.fetch(p, regs, page_tile(p, w, page, page_entry(p, w, page)));
+      int entry = page_entry(p, w, page + C::KG);  // of the page after the one in regs
       if (seg > 0) wait(bars.qempty, (seg - 1) & 1);
       ++seg;
       constexpr int kChunks = DK / 8;
       const size_t qrow0 = (size_t)(r.start + r.first) * p.Hq + w.hk * p.group;
 #pragma unroll 8
-      for (int i = all; i < NT * kTileRows * kChunks; i += 128 * C::KG) {
+      for (int i = all; i < NT * kTileRows * kChunks; i += 64 * C::KG) {
         const int here = i / kChunks, ch = i % kChunks;
         const int t = here / kTileRows, rr = here & (kTileRows - 1), row = t * 2 * kTileRows + rank * kTileRows + rr;
         uint4 v = make_uint4(0, 0, 0, 0);
@@ -336,59 +333,55 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
                                   (((ch & 7) ^ (rr & 7)) << 4)) = v;
       }
       arrive_first(bars.qfull);
-      for (int j = first; j < ns; j += C::KG, page += 2 * C::KG) {
+      for (int j = first; j < ns; j += C::KG, page += C::KG) {
         const int nj = n + j, st = nj % kStages;
         const PageRegs cur = regs;
-        if (j + C::KG < ns && (page + 2 * C::KG) * kPage < r.limit) {
-          keys.fetch(p, regs, page_tile(p, w, page + 2 * C::KG, entry));
-          entry = page_entry(p, w, page + 4 * C::KG);
+        if (j + C::KG < ns) {
+          keys.fetch(p, regs, page_tile(p, w, page + C::KG, entry));
+          entry = page_entry(p, w, page + 2 * C::KG);
         }
         if (nj >= kStages) wait(bars.kempty[st], (nj / kStages - 1) & 1);
-        if (page * kPage < r.limit) {  // a second page behind the limit stays as it was: its logits are masked
-          const uint32_t base = sm + C::kOffK + st * C::kKStage;
-          keys.codes(p, cur, lut, base);
-          if (KQ) keys.signs(cur, base + 2 * C::kKAtom);
-        }
+        const uint32_t base = sm + C::kOffK + st * C::kKStage;
+        keys.codes(p, cur, lut, base);
+        if (KQ) keys.signs(cur, base + 2 * C::kKAtom);
         arrive_first(bars.kfull[st]);
       }
       n += ns;
     }
-  } else if (warp < C::kWarpS) {  // ---- dims 64 rank .. + 63 of both pages' values
-    const int th = (tid - 32 * C::kWarpV) & 127, grp = (tid - 32 * C::kWarpV) >> 7, second = th >> 6;
+  } else if (warp < C::kWarpS) {  // ---- dims 64 rank .. + 63 of a page's values
+    const int th = (tid - 32 * C::kWarpV) & 63, grp = (tid - 32 * C::kWarpV) >> 6;
     ValueThread<VQ> values;
-    values.init(th & 7, 8 * rank + ((th >> 3) & 7), (th >> 3) & 7);
+    values.init(th & 7, 8 * rank + (th >> 3), th >> 3);
     const uint2 lut = code_halves(p.v);
     int n = 0;
     PageRegs regs = {};
     while (w.next(p, set)) {
-      const int ns = segment_steps(w), limit = w.rows.limit;
+      const int ns = segment_pages(w), limit = w.rows.limit;
       if (ns == 0) continue;
-      const int first = (grp + C::VG - n % C::VG) % C::VG;  // this group's first step of the segment
-      int page = 2 * (w.k0 + first) + second;
-      if (page * kPage < limit) values.fetch(p, regs, page_tile(p, w, page, page_entry(p, w, page)));
-      int entry = page_entry(p, w, page + 2 * C::VG);  // of the page after the one in regs
-      for (int j = first; j < ns; j += C::VG, page += 2 * C::VG) {
+      const int first = (grp + C::VG - n % C::VG) % C::VG;  // this group's first page of the segment
+      int page = w.k0 + first;
+      if (first < ns) values.fetch(p, regs, page_tile(p, w, page, page_entry(p, w, page)));
+      int entry = page_entry(p, w, page + C::VG);  // of the page after the one in regs
+      for (int j = first; j < ns; j += C::VG, page += C::VG) {
         const int nj = n + j, st = nj % kStages;
         const PageRegs cur = regs;
-        if (j + C::VG < ns && (page + 2 * C::VG) * kPage < limit) {
-          values.fetch(p, regs, page_tile(p, w, page + 2 * C::VG, entry));
-          entry = page_entry(p, w, page + 4 * C::VG);
+        if (j + C::VG < ns) {
+          values.fetch(p, regs, page_tile(p, w, page + C::VG, entry));
+          entry = page_entry(p, w, page + 2 * C::VG);
         }
         if (nj >= kStages) wait(bars.vempty[st], (nj / kStages - 1) & 1);
-        // a second page behind the limit enters as zeros
-        const uint32_t bad = values.store(p, cur, lut, sm + C::kOffV + st * C::kVStage + second * C::kVAtom, 64 * 128,
-                                          limit - page * kPage);
-        if ((th & 63) < 8) bars.vbad[st][8 * second + (th & 7)] = (unsigned char)bad;
+        const uint32_t bad = values.store(p, cur, lut, sm + C::kOffV + st * C::kVStage, 64 * 128, limit - page * kPage);
+        if (th < 8) bars.vbad[st][th] = (unsigned char)bad;
         arrive_first(bars.vfull[st]);
         if ((tid & 31) == 0) mbar_arrive(smem_addr(&bars.vhere[st]));
       }
       n += ns;
     }
   } else if (rank == 0 && warp == C::kWarpS) {  // ---- S = Q K^T (the whole warp, so that control stays uniform)
-    constexpr uint32_t id = tc::idesc_f16(0, 0, 0, 2 * kTileRows, kStep);
+    constexpr uint32_t id = tc::idesc_f16(0, 0, 0, 2 * kTileRows, kPage);
     int n = 0, seg = 0, nt[NT] = {};
     while (w.next(p, set)) {
-      const int ns = __shfl_sync(0xffffffffu, segment_steps(w), 0), count = __shfl_sync(0xffffffffu, w.rows.count, 0);
+      const int ns = __shfl_sync(0xffffffffu, segment_pages(w), 0), count = __shfl_sync(0xffffffffu, w.rows.count, 0);
       if (ns == 0) continue;
       wait_both(bars.qfull, seg & 1);
       ++seg;
@@ -405,7 +398,7 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
           const uint64_t qd = desc_sw128(sm + t * C::kQTile);
 #pragma unroll
           for (int i = 0; i < DK / 64; ++i)
-            tc::pair_f16_x4(tmem + kColS + (t * NB + b) * kStep, qd + ((i * kTileRows * 128) >> 4), kd + ((i * C::kKAtom) >> 4),
+            tc::pair_f16_x4(tmem + kColS + (t * NB + b) * kPage, qd + ((i * kTileRows * 128) >> 4), kd + ((i * C::kKAtom) >> 4),
                             id, i > 0);
           tc::pair_commit(smem_addr(&bars.sfull[t][b]));
           ++nt[t];
@@ -420,7 +413,7 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
     constexpr uint32_t id = tc::idesc_f16(0, 0, 0, 2 * kTileRows, DV);
     int n = 0, nt[NT] = {};
     while (w.next(p, set)) {
-      const int ns = __shfl_sync(0xffffffffu, segment_steps(w), 0), count = __shfl_sync(0xffffffffu, w.rows.count, 0);
+      const int ns = __shfl_sync(0xffffffffu, segment_pages(w), 0), count = __shfl_sync(0xffffffffu, w.rows.count, 0);
       for (int j = 0; j < ns; ++j, ++n) {
         const int st = n % kStages;
         wait_both(bars.vfull[st], (n / kStages) & 1);
@@ -431,10 +424,7 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
           const int b = nt[t] % NB;
           wait_both(bars.pready[t][b], (nt[t] / NB) & 1);
           tc::fence_after();
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            tc::pair_f16_ta_x4(tmem + t * DV, tmem + kColS + (t * NB + b) * kStep + 32 * i, vd + ((i * C::kVAtom) >> 4), id,
-                               j > 0 || i > 0);
+          tc::pair_f16_ta_x4(tmem + t * DV, tmem + kColS + (t * NB + b) * kPage, vd, id, j > 0);
           tc::pair_commit(smem_addr(&bars.pvdone[t][b]));
           ++nt[t];
         }
