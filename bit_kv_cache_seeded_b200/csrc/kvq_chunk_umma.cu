@@ -18,6 +18,9 @@
 // overwrites the first half of its S. Barriers that the products wait for are the first CTA's, and the second
 // arrives there; those that they complete are told to both.
 //
+// A row that attends to a value whose norm is not finite ends as NaN: rows attend to all of a segment's positions up
+// to their own, so the first such position decides.
+//
 // Softmax weights are p = 2^(x - m + 7), m the row's maximum but for steps under 2^8, by which it may lag
 // before O is rescaled: p stays under 2^15 in fp16, and a weight is dropped only below 2^-31 of the largest.
 #include "kvq_async.cuh"
@@ -31,6 +34,7 @@ using namespace chunk;
 
 constexpr int kStages = 4;
 constexpr int kTileRows = 128;        // of a CTA
+constexpr int kSlots = 16;            // of segments: values are never more than kStages pages, so segments, ahead
 constexpr float kLag = 8.f, kShift = 7.f;
 constexpr uint32_t kColS = 256, kTmemCols = 512;
 
@@ -41,7 +45,12 @@ struct Cfg {
   // groups of 2 warps that dequantise a side, page n on group n % G: twice as many where a sketch doubles the work
   static constexpr int KG = KQ ? 4 : 2, VG = VQ ? 4 : 2;
   static constexpr int kWarpK = 4 * NT, kWarpV = kWarpK + 2 * KG, kWarpS = kWarpV + 2 * VG, kWarpO = kWarpS + 1;
-  static constexpr int kThreads = 32 * (kWarpO + 1);
+  // With a key sketch 22 warps, and two more that only give their registers back: 80 a thread at launch, shared out
+  // so that nothing spills (shared memory leaves the L1 too small to hold local memory).
+  static constexpr bool kShare = KQ;
+  static constexpr int kRegsSoftmax = VQ ? 136 : 104, kRegsDequant = 72, kRegsIssue = 56;
+  static constexpr int kThreads = 32 * (kShare ? 24 : kWarpO + 1);
+  static_assert(!kShare || 4 * NT * kRegsSoftmax + 2 * (KG + VG) * kRegsDequant + 4 * kRegsIssue <= 24 * 80, "registers");
   static constexpr int kKAtom = kTile * 128, kVAtom = DV / 2 * 128;  // operand atoms of 64 K-elements, this CTA's rows
   static constexpr int kQTile = kTileRows * DK * 2, kKStage = DK / 64 * kKAtom, kVStage = kVAtom;
   static constexpr int kOffK = NT * kQTile, kOffV = kOffK + kStages * kKStage, kOffEnd = kOffV + kStages * kVStage;
@@ -51,8 +60,7 @@ template <int NT, int NB>
 struct Bars {
   uint64_t kfull[kStages], vfull[kStages], pready[NT][NB], qfull;                  // the first CTA's count both
   uint64_t kempty[kStages], vempty[kStages], sfull[NT][NB], pvdone[NT][NB], qempty, done[2];
-  uint64_t vhere[kStages];          // this CTA's values (and mask) are there
-  unsigned char vbad[kStages][8];   // tokens of the page whose value norm is not finite, a bit each
+  int bad[kSlots];                  // by segment: the first position whose value norm is not finite
   uint32_t tmem;
   int fail;
 };
@@ -112,6 +120,15 @@ __device__ __forceinline__ void arrive_first(uint64_t& bar) {
   if ((threadIdx.x & 31) == 0) mbar_arrive_at(smem_addr(&bar), 0);
 }
 
+template <bool SHARE, int REGS>
+__device__ __forceinline__ void more_registers() {
+  if (SHARE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(REGS));
+}
+template <bool SHARE, int REGS>
+__device__ __forceinline__ void fewer_registers() {
+  if (SHARE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(REGS));
+}
+
 template <bool KQ, bool VQ>
 __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __grid_constant__ ChunkParams p) {
   using C = Cfg<KQ, VQ>;
@@ -128,7 +145,6 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
       mbar_init(smem_addr(&bars.kempty[i]), 1);
       mbar_init(smem_addr(&bars.vfull[i]), 4);
       mbar_init(smem_addr(&bars.vempty[i]), 1);
-      mbar_init(smem_addr(&bars.vhere[i]), 2);
     }
     for (int t = 0; t < NT; ++t)
       for (int b = 0; b < NB; ++b) {
@@ -141,6 +157,7 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
     mbar_init(smem_addr(&bars.done[0]), 1);
     mbar_init(smem_addr(&bars.done[1]), 1);
     mbar_init_fence();
+    for (int i = 0; i < kSlots; ++i) bars.bad[i] = 0x7fffffff;
     bars.fail = 0;
   }
   if (warp == 0) tc::pair_alloc(smem_addr(&bars.tmem), kTmemCols);
@@ -170,11 +187,12 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
   w.init(p, set, pair);
 
   if (warp < C::kWarpK) {  // ---- softmax: thread = row
+    more_registers<C::kShare, C::kRegsSoftmax>();
     const int t = warp >> 2, row = t * 2 * kTileRows + rank * kTileRows + (tid & 127);  // of the NT * 256
     const int row0 = row & ~31;                                                    // of this warp
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tO = tmem + lanes + t * DV, tS = tmem + lanes + kColS + t * NB * kPage;
-    int n = 0, nv = 0;  // pages this tile, and the pair, has seen
+    int n = 0, seg = 0;  // pages this tile, and segments the pair, has seen
     while (w.next(p, set)) {
       const Rows r = w.rows;
       const int ns = segment_pages(w);
@@ -185,63 +203,63 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
       float qs = 1.f;
       if (row < r.count)
         qs = p.qscale[(size_t)(r.start + r.first + row / p.group) * p.Hq + w.hk * p.group + row % p.group];
-      float m = -INFINITY, ref = 0.f, l = 0.f;
+      const F2 qs2(qs, qs);
+      float m = -INFINITY, ref = 0.f;
+      F2 sum[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
       for (int j = 0; used && j < ns; ++j, ++n) {
-        const int b = n % NB, st = (nv + j) % kStages;
+        const int b = n % NB;
         wait(bars.sfull[t][b], (n / NB) & 1);
         tc::fence_after();
         if (work) {
-          // halves of 32 columns, read from tensor memory again for the second pass: rolled loops (the code of all
-          // roles has to stay in the instruction cache)
           const int reach = last - (w.k0 + j) * kPage;  // the page's tokens 0 .. reach are attended
           const bool full = __all_sync(0xffffffffu, reach >= kPage - 1);
-          auto logits = [&](uint32_t (&s)[32], int c) {
+          // 32 columns at a time, in a rolled loop (the code of all roles has to stay in the instruction cache)
+#pragma unroll 1
+          for (int c = 0; c < kPage; c += 32) {
+            uint32_t s[32], ph[16];
             tc::tmem_ld32(tS + kPage * b + c, s);
             tc::wait_ld();
             if (!full) {
 #pragma unroll
               for (int i = 0; i < 32; ++i) s[i] = c + i <= reach ? s[i] : 0xff800000u;
             }
-          };
-          float mx2[2] = {-INFINITY, -INFINITY};
-#pragma unroll 1
-          for (int c = 0; c < kPage; c += 32) {
-            uint32_t s[32];
-            logits(s, c);
+            float mx2[2] = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               mx2[i & 1] = max3(mx2[i & 1], __uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
-          }
-          const float mx = fmaxf(mx2[0], mx2[1]) * qs;
-          const bool grow = mx > m + kLag || (m == -INFINITY && mx > m);
-          if (__any_sync(0xffffffffu, grow)) {
-            const float alpha = grow ? ex2f(m - mx) : 1.f;
-            if (grow) {
-              m = mx;
-              ref = mx - kShift;
-            }
-            l *= alpha;
-            if (j > 0) {
-              wait(bars.pvdone[t][(n - 1) % NB], ((n - 1) / NB) & 1);
-              tc::fence_after();
-#pragma unroll 1
-              for (int c = 0; c < DV; c += 16) {
-                uint32_t o[16];
-                tc::tmem_ld16(tO + c, o);
-                tc::wait_ld();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                tc::tmem_st16(tO + c, o);
+            const float mx = fmaxf(mx2[0], mx2[1]) * qs;
+            const bool grow = mx > m + kLag || (m == -INFINITY && mx > m);
+            if (__any_sync(0xffffffffu, grow)) {  // a new reference: what came before is brought to it
+              const float alpha = grow ? ex2f(m - mx) : 1.f;
+              if (grow) {
+                m = mx;
+                ref = mx - kShift;
               }
-              tc::wait_st();
-            }
-          }
-          F2 sum[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
-          const F2 qs2(qs, qs), ref2(-ref, -ref);
+              sum[0] = mul(sum[0], F2(alpha, alpha));
+              sum[1] = mul(sum[1], F2(alpha, alpha));
+              if (c > 0) {  // this page's first weights
+                tc::wait_st();
+                tc::tmem_ld16(tS + kPage * b, ph);
+                tc::wait_ld();
+                const uint32_t a2 = half_bits(alpha) * 0x10001u;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) ph[i] = mul2(ph[i], a2);
+                tc::tmem_st16(tS + kPage * b, ph);
+              }
+              if (j > 0) {
+                wait(bars.pvdone[t][(n - 1) % NB], ((n - 1) / NB) & 1);
+                tc::fence_after();
 #pragma unroll 1
-          for (int c = 0; c < kPage; c += 32) {
-            uint32_t s[32], ph[16];
-            logits(s, c);
+                for (int o = 0; o < DV; o += 16) {
+                  tc::tmem_ld16(tO + o, ph);
+                  tc::wait_ld();
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) ph[i] = __float_as_uint(__uint_as_float(ph[i]) * alpha);
+                  tc::tmem_st16(tO + o, ph);
+                }
+              }
+            }
+            const F2 ref2(-ref, -ref);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               F2 x = fma(F2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), qs2, ref2);
@@ -261,28 +279,26 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
             }
             tc::tmem_st16(tS + kPage * b + c / 2, ph);
           }
-          float la, lb;
-          add(sum[0], sum[1]).get(la, lb);
-          l += la + lb;
-          wait(bars.vhere[st], ((nv + j) / kStages) & 1);
-          const unsigned long long bad = *reinterpret_cast<const volatile unsigned long long*>(bars.vbad[st]);
-          if (bad != 0 && reach >= 0 && (bad & (~0ull >> (63 - min(reach, 63)))) != 0) l = NAN;
           tc::wait_st();
         }
         tc::fence_before();
         __syncwarp();
         if ((tid & 31) == 0) mbar_arrive_at_tmem(smem_addr(&bars.pready[t][b]), 0);
       }
-      nv += ns;
       // the segment's state
       if (used) {
         wait(bars.pvdone[t][(n - 1) % NB], ((n - 1) / NB) & 1);
         tc::fence_after();
       }
       if (work) {
+        float la, l;
+        add(sum[0], sum[1]).get(la, l);
+        l += la;
+        if (m == -INFINITY && l == l) l = 0.f;  // ex2_fma leaves 2^-126 of a masked position
+        if (ns > 0 && *(volatile int*)&bars.bad[seg % kSlots] <= last && row < r.count) l = NAN;
         float* ml = segment_ml(set, w.item, pair, DV) + 2 * row;
         float* so = segment_o(set, w.item, pair, DV) + (size_t)row * DV;
-        if (row < r.count) *reinterpret_cast<float2*>(ml) = make_float2(m == -INFINITY ? m : ref, m == -INFINITY && l == l ? 0.f : l);
+        if (row < r.count) *reinterpret_cast<float2*>(ml) = make_float2(m == -INFINITY ? m : ref, l);
 #pragma unroll 1
         for (int c = 0; c < DV; c += 16) {
           uint32_t o[16];
@@ -299,9 +315,11 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
                   used ? make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]) : make_uint4(0, 0, 0, 0);
         }
       }
+      seg += ns > 0;
       tc::fence_before();
     }
   } else if (warp < C::kWarpV) {  // ---- keys of 32 tokens of a page, and the queries of each segment
+    fewer_registers<C::kShare, C::kRegsDequant>();
     const int all = tid - 32 * C::kWarpK, grp = all >> 6;
     KeyThread<KQ> keys;
     keys.init(p, (all & 63) + 64 * rank, C::kKAtom);
@@ -349,15 +367,17 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
       n += ns;
     }
   } else if (warp < C::kWarpS) {  // ---- dims 64 rank .. + 63 of a page's values
+    fewer_registers<C::kShare, C::kRegsDequant>();
     const int th = (tid - 32 * C::kWarpV) & 63, grp = (tid - 32 * C::kWarpV) >> 6;
     ValueThread<VQ> values;
     values.init(th & 7, 8 * rank + (th >> 3), th >> 3);
     const uint2 lut = code_halves(p.v);
-    int n = 0;
+    int n = 0, seg = 0;
     PageRegs regs = {};
     while (w.next(p, set)) {
       const int ns = segment_pages(w), limit = w.rows.limit;
       if (ns == 0) continue;
+      if (th == 0 && grp == 0) bars.bad[(seg + kSlots / 2) % kSlots] = 0x7fffffff;  // last used half a round ago
       const int first = (grp + C::VG - n % C::VG) % C::VG;  // this group's first page of the segment
       int page = w.k0 + first;
       if (first < ns) values.fetch(p, regs, page_tile(p, w, page, page_entry(p, w, page)));
@@ -371,68 +391,71 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
         }
         if (nj >= kStages) wait(bars.vempty[st], (nj / kStages - 1) & 1);
         const uint32_t bad = values.store(p, cur, lut, sm + C::kOffV + st * C::kVStage, 64 * 128, limit - page * kPage);
-        if (th < 8) bars.vbad[st][th] = (unsigned char)bad;
+        if (bad != 0 && th < 8) atomicMin(&bars.bad[seg % kSlots], page * kPage + 8 * th + __ffs(bad) - 1);
         arrive_first(bars.vfull[st]);
-        if ((tid & 31) == 0) mbar_arrive(smem_addr(&bars.vhere[st]));
       }
       n += ns;
-    }
-  } else if (rank == 0 && warp == C::kWarpS) {  // ---- S = Q K^T (the whole warp, so that control stays uniform)
-    constexpr uint32_t id = tc::idesc_f16(0, 0, 0, 2 * kTileRows, kPage);
-    int n = 0, seg = 0, nt[NT] = {};
-    while (w.next(p, set)) {
-      const int ns = __shfl_sync(0xffffffffu, segment_pages(w), 0), count = __shfl_sync(0xffffffffu, w.rows.count, 0);
-      if (ns == 0) continue;
-      wait_both(bars.qfull, seg & 1);
       ++seg;
-      for (int j = 0; j < ns; ++j, ++n) {
-        const int st = n % kStages;
-        wait_both(bars.kfull[st], (n / kStages) & 1);
-        const uint64_t kd = desc_sw128(sm + C::kOffK + st * C::kKStage);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          if (t * 2 * kTileRows >= count) continue;
-          const int b = nt[t] % NB;
-          if (nt[t] >= NB) wait(bars.pvdone[t][b], (nt[t] / NB - 1) & 1);  // the P that lies there is read
-          tc::fence_after();
-          const uint64_t qd = desc_sw128(sm + t * C::kQTile);
-#pragma unroll
-          for (int i = 0; i < DK / 64; ++i)
-            tc::pair_f16_x4(tmem + kColS + (t * NB + b) * kPage, qd + ((i * kTileRows * 128) >> 4), kd + ((i * C::kKAtom) >> 4),
-                            id, i > 0);
-          tc::pair_commit(smem_addr(&bars.sfull[t][b]));
-          ++nt[t];
-        }
-        tc::pair_commit(smem_addr(&bars.kempty[st]));
-      }
-      tc::pair_commit(smem_addr(&bars.qempty));
     }
-    tc::pair_commit(smem_addr(&bars.done[0]));
-    mbar_wait(smem_addr(&bars.done[0]), 0, p.wait_limit);
-  } else if (rank == 0) {  // ---- O += P V
-    constexpr uint32_t id = tc::idesc_f16(0, 0, 0, 2 * kTileRows, DV);
-    int n = 0, nt[NT] = {};
-    while (w.next(p, set)) {
-      const int ns = __shfl_sync(0xffffffffu, segment_pages(w), 0), count = __shfl_sync(0xffffffffu, w.rows.count, 0);
-      for (int j = 0; j < ns; ++j, ++n) {
-        const int st = n % kStages;
-        wait_both(bars.vfull[st], (n / kStages) & 1);
-        const uint64_t vd = desc_sw128(sm + C::kOffV + st * C::kVStage);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          if (t * 2 * kTileRows >= count) continue;
-          const int b = nt[t] % NB;
-          wait_both(bars.pready[t][b], (nt[t] / NB) & 1);
-          tc::fence_after();
-          tc::pair_f16_ta_x4(tmem + t * DV, tmem + kColS + (t * NB + b) * kPage, vd, id, j > 0);
-          tc::pair_commit(smem_addr(&bars.pvdone[t][b]));
-          ++nt[t];
+  } else {
+    fewer_registers<C::kShare, C::kRegsIssue>();
+    if (rank == 0 && warp == C::kWarpS) {  // ---- S = Q K^T (the whole warp, so that control stays uniform)
+      constexpr uint32_t id = tc::idesc_f16(0, 0, 0, 2 * kTileRows, kPage);
+      int n = 0, seg = 0, nt[NT] = {};
+      while (w.next(p, set)) {
+        const int ns = __shfl_sync(0xffffffffu, segment_pages(w), 0), count = __shfl_sync(0xffffffffu, w.rows.count, 0);
+        if (ns == 0) continue;
+        wait_both(bars.qfull, seg & 1);
+        ++seg;
+        for (int j = 0; j < ns; ++j, ++n) {
+          const int st = n % kStages;
+          wait_both(bars.kfull[st], (n / kStages) & 1);
+          const uint64_t kd = desc_sw128(sm + C::kOffK + st * C::kKStage);
+  #pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            if (t * 2 * kTileRows >= count) continue;
+            const int b = nt[t] % NB;
+            if (nt[t] >= NB) wait(bars.pvdone[t][b], (nt[t] / NB - 1) & 1);  // the P that lies there is read
+            tc::fence_after();
+            const uint64_t qd = desc_sw128(sm + t * C::kQTile);
+  #pragma unroll
+            for (int i = 0; i < DK / 64; ++i)
+              tc::pair_f16_x4(tmem + kColS + (t * NB + b) * kPage, qd + ((i * kTileRows * 128) >> 4), kd + ((i * C::kKAtom) >> 4),
+                              id, i > 0);
+            tc::pair_commit(smem_addr(&bars.sfull[t][b]));
+            ++nt[t];
+          }
+          tc::pair_commit(smem_addr(&bars.kempty[st]));
         }
-        tc::pair_commit(smem_addr(&bars.vempty[st]));
+        tc::pair_commit(smem_addr(&bars.qempty));
       }
+      tc::pair_commit(smem_addr(&bars.done[0]));
+      mbar_wait(smem_addr(&bars.done[0]), 0, p.wait_limit);
+    } else if (rank == 0 && warp == C::kWarpO) {  // ---- O += P V
+      constexpr uint32_t id = tc::idesc_f16(0, 0, 0, 2 * kTileRows, DV);
+      int n = 0, nt[NT] = {};
+      while (w.next(p, set)) {
+        const int ns = __shfl_sync(0xffffffffu, segment_pages(w), 0), count = __shfl_sync(0xffffffffu, w.rows.count, 0);
+        for (int j = 0; j < ns; ++j, ++n) {
+          const int st = n % kStages;
+          wait_both(bars.vfull[st], (n / kStages) & 1);
+          const uint64_t vd = desc_sw128(sm + C::kOffV + st * C::kVStage);
+  #pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            if (t * 2 * kTileRows >= count) continue;
+            const int b = nt[t] % NB;
+            wait_both(bars.pready[t][b], (nt[t] / NB) & 1);
+            tc::fence_after();
+            tc::pair_f16_ta_x4(tmem + t * DV, tmem + kColS + (t * NB + b) * kPage, vd, id, j > 0);
+            tc::pair_commit(smem_addr(&bars.pvdone[t][b]));
+            ++nt[t];
+          }
+          tc::pair_commit(smem_addr(&bars.vempty[st]));
+        }
+      }
+      tc::pair_commit(smem_addr(&bars.done[1]));
+      mbar_wait(smem_addr(&bars.done[1]), 0, p.wait_limit);
     }
-    tc::pair_commit(smem_addr(&bars.done[1]));
-    mbar_wait(smem_addr(&bars.done[1]), 0, p.wait_limit);
   }
   __syncwarp();
   tc::fence_before();
