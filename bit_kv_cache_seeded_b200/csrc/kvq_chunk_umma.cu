@@ -48,7 +48,7 @@ struct Cfg {
   // With a key sketch 22 warps, and two more that only give their registers back: 80 a thread at launch, shared out
   // so that nothing spills (shared memory leaves the L1 too small to hold local memory).
   static constexpr bool kShare = KQ;
-  static constexpr int kRegsSoftmax = VQ ? 136 : 104, kRegsDequant = 72, kRegsIssue = 56;
+  static constexpr int kRegsSoftmax = VQ ? 104 : 88, kRegsDequant = 80 /* as launched */, kRegsIssue = 56;
   static constexpr int kThreads = 32 * (kShare ? 24 : kWarpO + 1);
   static_assert(!kShare || 4 * NT * kRegsSoftmax + 2 * (KG + VG) * kRegsDequant + 4 * kRegsIssue <= 24 * 80, "registers");
   static constexpr int kKAtom = kTile * 128, kVAtom = DV / 2 * 128;  // operand atoms of 64 K-elements, this CTA's rows
@@ -95,7 +95,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // 2^x on the FMA pipe, for x < 126: x = k + f, k the nearest integer, 2^f by a cubic fitted to |f| <= 1/2 with
 // the least largest relative error (2^-13.7, under the weights' own rounding to fp16, 2^-11). Below 2^-126
 // stays 2^-126; a NaN stays one. The special-function unit makes 4 powers a cycle and quarter of an SM, which
-// bounds the softmax; a quarter of them is made here instead.
+// bounds the softmax where nothing else does; a quarter of them is made here then (one-bit chunks 374 -> 368 us;
+// beside the dequantisation of key sketches it costs more than it gives, 2.39 -> 2.48 ms).
 __device__ __forceinline__ F2 ex2_fma(F2 x) {
   float a, b;
   x.get(a, b);
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
             for (int i = 0; i < 16; ++i) {
               F2 x = fma(F2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), qs2, ref2);
               float a, d;
-              if ((i & 3) == 3) {
+              if (!KQ && (i & 3) == 3) {
                 x = ex2_fma(x);
                 x.get(a, d);
               } else {
@@ -319,7 +320,6 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
       tc::fence_before();
     }
   } else if (warp < C::kWarpV) {  // ---- keys of 32 tokens of a page, and the queries of each segment
-    fewer_registers<C::kShare, C::kRegsDequant>();
     const int all = tid - 32 * C::kWarpK, grp = all >> 6;
     KeyThread<KQ> keys;
     keys.init(p, (all & 63) + 64 * rank, C::kKAtom);
@@ -367,7 +367,6 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
       n += ns;
     }
   } else if (warp < C::kWarpS) {  // ---- dims 64 rank .. + 63 of a page's values
-    fewer_registers<C::kShare, C::kRegsDequant>();
     const int th = (tid - 32 * C::kWarpV) & 63, grp = (tid - 32 * C::kWarpV) >> 6;
     ValueThread<VQ> values;
     values.init(th & 7, 8 * rank + (th >> 3), th >> 3);
