@@ -14,6 +14,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "kvq_async.cuh"
 #include "kvq_chunk.cuh"
 #include "kvq_internal.h"
 #include "kvq_lm_common.cuh"
@@ -185,6 +186,7 @@ __device__ void plan(const ChunkParams& p, const ChunkSet& s) {
       }
       s.tile_seq[t] = lo;
       const Rows r = tile_rows(p, s, lo, t - s.tile_start[lo]);
+      s.tile_rows[t] = make_int2(r.start + r.first, r.count);
       units = max(1, (r.limit + s.unit - 1) / s.unit);
     }
     const long long at = scan(units);
@@ -397,6 +399,7 @@ __global__ void __launch_bounds__(256) chunk_f32(const __grid_constant__ ChunkPa
   Smem& sm = *reinterpret_cast<Smem*>(smem);
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
   const ChunkSet& set = p.set[kWide];
+  grid_dep_wait();
   Walk w;
   w.init(p, set, blockIdx.x);
   while (w.next(p, set)) {
@@ -529,13 +532,14 @@ __global__ void __launch_bounds__(kMergeThreads, VQ ? 2 : 3) chunk_merge(const _
   __shared__ __align__(16) float s_z[VQ ? kMergeRows : 1][kPad];   // sketch sums; bf16: their products
   __shared__ __align__(16) __half s_a[VQ && BF16 ? kMergeRows : 1][kPadH];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Frags frags;
+  if (VQ && BF16) load_frags(frags, p.S, p.s_exp, warp, lane);
+  grid_dep_wait();
   int groups = 0, first[2];  // groups of both sets, one after the other
   for (int i = 0; i < p.sets; ++i) {
     first[i] = groups;
     groups += (int)p.set[i].head[0] * p.Hkv * (p.set[i].rows / kMergeRows);
   }
-  Frags frags;
-  if (VQ && BF16 && blockIdx.x < groups) load_frags(frags, p.S, p.s_exp, warp, lane);
   for (int g = blockIdx.x; g < groups; g += gridDim.x) {
     const int in = p.sets > 1 && g >= first[1];
     const ChunkSet& set = p.set[in];
@@ -544,11 +548,11 @@ __global__ void __launch_bounds__(kMergeThreads, VQ ? 2 : 3) chunk_merge(const _
     const int item = group / per;
     const int hk = item / tiles, tile = item % tiles;
     const int group0 = group % per * kMergeRows, row0 = group0 + 4 * warp;
-    const int b = set.tile_seq[tile];
-    const Rows r = tile_rows(p, set, b, tile - set.tile_start[b]);
-    if (group0 >= r.count) continue;
-    const int c0 = cta_of(hk * units + set.unit_start[tile], T, G);
-    const int c1 = cta_of(hk * units + set.unit_start[tile + 1] - 1, T, G);
+    const int2 r = set.tile_rows[tile];  // token of the first row, rows
+    const long long u0 = set.unit_start[tile], u1 = set.unit_start[tile + 1];
+    if (group0 >= r.y) continue;
+    const int c0 = cta_of(hk * units + u0, T, G);
+    const int c1 = cta_of(hk * units + u1 - 1, T, G);
     // the segments' maxima and sums first, a lane per segment; then their rows, four in flight
     float acc[4][4], accz[4][4], l[4], m[4];
 #pragma unroll
@@ -562,7 +566,7 @@ __global__ void __launch_bounds__(kMergeThreads, VQ ? 2 : 3) chunk_merge(const _
       const float2* ml = reinterpret_cast<const float2*>(segment_ml(set, item, c, DV)) + row0;
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        if (row0 + v >= r.count) continue;
+        if (row0 + v >= r.y) continue;
         const float2 s = ml[v];
         const float top = fmaxf(m[v], s.x);
         // a NaN sum (a logit that is NaN: the maximum passes over it) stays, an empty part adds nothing
@@ -588,7 +592,7 @@ __global__ void __launch_bounds__(kMergeThreads, VQ ? 2 : 3) chunk_merge(const _
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         f[v] = -INFINITY;
-        if (row0 + v >= r.count) continue;
+        if (row0 + v >= r.y) continue;
         f[v] = ml[v].x;
         load4(o[v], so + v * DV, false, lane);
         if (VQ) load4(z[v], so + v * DV + kHeadDim, false, lane);
@@ -648,9 +652,9 @@ __global__ void __launch_bounds__(kMergeThreads, VQ ? 2 : 3) chunk_merge(const _
     for (int v = 0; v < 4; ++v) {
       fwht(acc[v], lane);
       const int row = row0 + v;
-      if (row >= r.count) continue;
+      if (row >= r.y) continue;
       const float f = l[v] > 0.f ? (BF16 ? kCodeScale : 1.f) / (kHeadDim * l[v]) : l[v];  // 0: nothing attended; or NaN
-      const size_t at = ((size_t)(r.start + r.first + row / p.group) * p.Hq + hk * p.group + row % p.group) * kHeadDim;
+      const size_t at = ((size_t)(r.x + row / p.group) * p.Hq + hk * p.group + row % p.group) * kHeadDim;
 #pragma unroll
       for (int k = 0; k < 4; ++k) acc[v][k] *= f * sg[k];
       if (BF16)
@@ -674,8 +678,7 @@ template <bool VQ, bool BF16>
 cudaError_t launch_merge(const ChunkParams& p, cudaStream_t s) {
   long long groups = 0;
   for (int i = 0; i < p.sets; ++i) groups += (long long)p.set[i].max_tiles * p.Hkv * (p.set[i].rows / kMergeRows);
-  chunk_merge<VQ, BF16><<<(unsigned)std::min(groups, (VQ ? 2ll : 3ll) * p.sms), kMergeThreads, 0, s>>>(p);
-  return launched();
+  return launch_after(chunk_merge<VQ, BF16>, p, (unsigned)std::min(groups, (VQ ? 2ll : 3ll) * p.sms), kMergeThreads, 0, 1, s);
 }
 
 template <bool KQ, bool VQ>
@@ -683,8 +686,7 @@ cudaError_t launch_f32(const ChunkParams& p, cudaStream_t s) {
   constexpr int smem = (int)sizeof(F32Smem<KQ, VQ>);
   const cudaError_t e = cudaFuncSetAttribute(chunk_f32<KQ, VQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  chunk_f32<KQ, VQ><<<p.set[kWide].ctas, 256, smem, s>>>(p);
-  return launched();
+  return launch_after(chunk_f32<KQ, VQ>, p, p.set[kWide].ctas, 256, smem, 1, s);
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -716,6 +718,7 @@ ChunkLayout chunk_layout(int n_tokens, int batch, int Hq, int Hkv, bool k_qjl, b
     s.head = take(2 * sizeof(long long));
     s.unit_start = take(sizeof(long long) * ((size_t)s.max_tiles + 1));
     s.tile_seq = take(sizeof(int) * (size_t)s.max_tiles);
+    s.tile_rows = take(sizeof(int2) * (size_t)s.max_tiles);
     s.tile_start = take(sizeof(int) * ((size_t)batch + 1));
     const size_t segments = s.max_tiles ? (size_t)s.max_tiles * Hkv + s.ctas : 0;
     s.part = take(sizeof(float) * segments * s.rows * (2 + kHeadDim * (v_qjl ? 2 : 1)));

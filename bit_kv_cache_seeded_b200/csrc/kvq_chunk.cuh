@@ -117,6 +117,27 @@ __device__ __forceinline__ int query_pos(int order, int lane) {
 }
 constexpr float kCodeScale = 8.f, kSketchScale = 16.f;  // their operands hold 1/8 of a code, 1/16 of a sketch entry
 
+// Launches a kernel of the call that starts while its predecessor ends (grid_dep_wait before it reads what that wrote).
+inline cudaError_t launch_after(void (*kernel)(ChunkParams), const ChunkParams& p, unsigned blocks, unsigned threads, int smem,
+                                int cluster, cudaStream_t s) {
+  cudaLaunchConfig_t config = {};
+  config.gridDim = dim3(blocks);
+  config.blockDim = dim3(threads);
+  config.dynamicSmemBytes = smem;
+  config.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  config.attrs = attr;
+  config.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&config, kernel, p);
+  const cudaError_t counted = launched();
+  return e != cudaSuccess ? e : counted;
+}
+
 }  // namespace chunk
 
 // The bf16 path's segment kernels: kvq_chunk_umma.cu for the wide set (and the query rows of its tile),

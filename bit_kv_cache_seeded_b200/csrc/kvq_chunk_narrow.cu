@@ -74,6 +74,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow(const __grid_constan
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ __align__(16) Bars bars;
   const ChunkSet& set = p.set[kNarrow];
+  grid_dep_wait();
   if (set.head[1] == 0) return;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   if (tid == 0) {
@@ -408,8 +409,7 @@ cudaError_t launch(const ChunkParams& p, cudaStream_t s) {
   constexpr int smem = Cfg<KQ, VQ>::kOffEnd;
   const cudaError_t e = cudaFuncSetAttribute(chunk_narrow<KQ, VQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  chunk_narrow<KQ, VQ><<<p.set[kNarrow].ctas, kThreads, smem, s>>>(p);
-  return launched();
+  return launch_after(chunk_narrow<KQ, VQ>, p, p.set[kNarrow].ctas, kThreads, smem, 1, s);
 }
 
 }  // namespace

@@ -137,6 +137,7 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ __align__(16) Bars<NT, NB> bars;
   const ChunkSet& set = p.set[kWide];
+  grid_dep_wait();
   if (set.head[1] == 0) return;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int rank = (int)cluster_rank(), pair = blockIdx.x >> 1;
@@ -471,20 +472,7 @@ cudaError_t launch(const ChunkParams& p, cudaStream_t s) {
   constexpr int smem = Cfg<KQ, VQ>::kOffEnd;
   const cudaError_t e = cudaFuncSetAttribute(chunk_umma<KQ, VQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t config = {};
-  config.gridDim = dim3(2 * p.set[kWide].ctas);
-  config.blockDim = dim3(Cfg<KQ, VQ>::kThreads);
-  config.dynamicSmemBytes = smem;
-  config.stream = s;
-  cudaLaunchAttribute pairs;
-  pairs.id = cudaLaunchAttributeClusterDimension;
-  pairs.val.clusterDim.x = 2;
-  pairs.val.clusterDim.y = pairs.val.clusterDim.z = 1;
-  config.attrs = &pairs;
-  config.numAttrs = 1;
-  const cudaError_t launch_error = cudaLaunchKernelEx(&config, chunk_umma<KQ, VQ>, p);
-  const cudaError_t counted = launched();
-  return launch_error != cudaSuccess ? launch_error : counted;
+  return launch_after(chunk_umma<KQ, VQ>, p, 2 * p.set[kWide].ctas, Cfg<KQ, VQ>::kThreads, smem, 2, s);
 }
 
 }  // namespace
