@@ -131,9 +131,9 @@ def _on_device(fn: str, **tensors):
 
 
 def _stream(stream=None):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    if stream is None:  # torch.cuda.current_stream().cuda_stream without the object: 0.3 us instead of 3.4
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def make_cfg(head_dim=128, n_q_heads=1, n_kv_heads=1, k_mode="lm_qjl", v_mode="lm_qjl", k_bits=2,
@@ -675,7 +675,7 @@ class KvqCache:
         # memory of the current stream: a workspace it outgrows is reused in its order
         if torch.cuda.is_current_stream_capturing():
             return torch.empty(need, dtype=torch.uint8, device=device)
-        kept, at = self.__dict__.setdefault("chunk_workspaces", {}), torch.cuda.current_stream().cuda_stream
+        kept, at = self.__dict__.setdefault("chunk_workspaces", {}), _stream()
         have = kept.get(at)
         if have is None or have.numel() < need:
             have = kept[at] = torch.empty(need, dtype=torch.uint8, device=device)

@@ -1275,6 +1275,7 @@ kvq_status kvq_quantize_slots(kvq_cache* c, const void* K, const void* V, kvq_dt
   p.signs = c->d_signs;
   p.signs_stride = c->signs_stride;
   p.St = c->d_St;
+  p.s_exp = c->s_exp;
   p.err = c->d_status;
   return launch_quantize_slots(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }

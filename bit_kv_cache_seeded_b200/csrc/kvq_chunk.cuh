@@ -54,7 +54,13 @@ __device__ __forceinline__ Rows tile_rows(const ChunkParams& p, const ChunkSet& 
 // floor(c T / G) <= u.
 __device__ __forceinline__ long long cta_count(const ChunkSet& s, long long T) { return min((long long)s.ctas, T); }
 __device__ __forceinline__ long long cta_first(long long c, long long T, long long G) { return c * T / G; }
-__device__ __forceinline__ int cta_of(long long u, long long T, long long G) { return (int)(((u + 1) * G - 1) / T); }
+__device__ __forceinline__ int cta_of(long long u, long long T, long long G) {
+  const long long x = (u + 1) * G;  // the largest c with c T < x: c is small, so fp32 is within one of it
+  int c = (int)__fdividef((float)x, (float)T);
+  if (c * T >= x) --c;
+  if ((c + 1) * T < x) ++c;
+  return c;
+}
 
 // Walks the segments of one CTA. Every thread (or one per warp) keeps its own copy.
 struct Walk {

@@ -179,6 +179,7 @@ struct SlotQuantizeParams {
   const float* signs;
   int signs_stride;
   const float* St;
+  int s_exp;                // S / 2^s_exp is within fp16's range
   int* err;
 };
 

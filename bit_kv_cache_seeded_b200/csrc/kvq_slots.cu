@@ -13,18 +13,20 @@
 // 64 * table[b][position / 64] + position % 64. One thread per token; bound by the 16 bytes it writes.
 //
 // quantize_slots. The codec's steps 1-7 (kvq_quantize.cu) on vectors [token][kv-head][128], written to
-// slots[token]. A block codes TOK tokens of one (kv-head, side): warps code a token each, the sketch of
-// all TOK residuals is one product with S^T staged in shared memory (as in kvq_quantize_tile.cuh), and
-// the bits go out per run of slots in one octet: a whole octet of a key plane is stored, a part of one
-// is merged with atomics, since other tokens of the octet may belong to another block. The sketch
-// product on the CUDA cores bounds it (128 x 128 FMAs a vector), so small calls take TOK = 8, which
-// spreads them over four times as many blocks as TOK = 32, and large calls 32, which reads S^T a
-// quarter as often.
+// slots[token]. A block codes TOK tokens of one (kv-head, side) at a time: warps code a token each; the sketch of
+// all TOK residuals is one product with S^T on the tensor cores (mma.sync); and the bits go out per run of slots in
+// one octet, a run and plane per warp: a whole octet of a key plane is stored, a part of one is merged with
+// atomics, since other tokens of the octet may belong to another block.
+//
+// The product decides signs, so it has to be as good as fp32: residuals and S are each two fp16 numbers, the
+// second 2^11 times what the first leaves (22 bits together), and the three products that matter are summed in
+// fp32, the small ones apart. On the CUDA cores it took half of the instructions, and the packing on one warp a
+// plane a quarter (2200 tokens of 8 heads, 3 bits, a sketch on the keys: 52.3 us; MEASURED now). Small calls take
+// TOK = 8, which spreads them over four times as many blocks as TOK = 32.
 #include <algorithm>
 
 #include <cuda_fp16.h>
 
-#include "kvq_async.cuh"
 #include "kvq_internal.h"
 #include "kvq_quantize_lm.cuh"
 #include "kvq_tiles.cuh"
@@ -178,37 +180,60 @@ __global__ void set_lengths(const __grid_constant__ LengthParams p) {
 
 constexpr int kAppWarps = 8;
 constexpr int kAppThreads = kAppWarps * 32;
+constexpr int kPadH = kHeadDim + 8;  // row stride of a half row: the 8 rows that ldmatrix reads lie in distinct banks
+constexpr float kSecond = 2048.f;
 
 template <int TOK>
 struct AppSmem {
-  float rho[TOK][kHeadDim];
+  static constexpr int kRows = TOK < 16 ? 16 : TOK;  // a matrix tile has 16; those past TOK are not looked at
+  __half rho[2][kRows][kPadH];
   uint32_t planes[TOK][kMaxBits + 1][4];  // code planes, then the sign words
   float n[TOK], gamma[TOK];
   long long slot[TOK];  // -1: not written
 };
 
+// x = first + second / 2^11, as halves.
+__device__ __forceinline__ __half first_half(float x) { return __float2half_rn(x); }
+__device__ __forceinline__ __half second_half(float x) { return __float2half_rn((x - __half2float(__float2half_rn(x))) * kSecond); }
+__device__ __forceinline__ uint32_t half_pair(__half a, __half b) {
+  const __half2 h = __halves2half2(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
 template <int TOK>
-__global__ void __launch_bounds__(kAppThreads) quantize_slots(const __grid_constant__ SlotQuantizeParams p) {
-  constexpr int R = TOK / 8;            // sketch rows per lane: 32 / TOK warps share the 128 rows of 4 tokens
-  constexpr int kShare = 32 / TOK;
-  extern __shared__ __align__(16) unsigned char smem[];
-  AppSmem<TOK>& sm = *reinterpret_cast<AppSmem<TOK>*>(smem);
-  float* st_s = reinterpret_cast<float*>(smem + (sizeof(AppSmem<TOK>) + 15) / 16 * 16);
+__global__ void __launch_bounds__(kAppThreads, 2) quantize_slots(const __grid_constant__ SlotQuantizeParams p) {
+  __shared__ __align__(16) AppSmem<TOK> sm;
   const int side = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const SideLayout& L = p.side[side];
   const int nthr = (1 << L.bits) - 1;
   const int chunks = (p.n_tokens + TOK - 1) / TOK;
   const long long total = (long long)chunks * p.heads;
   if (blockIdx.x >= total) return;
+  // this warp's rows 16 warp .. + 15 of S (columns of S^T), divided by 2^s_exp
+  uint32_t frag[2][2][8][2];
   if (L.qjl) {
-    for (int c = tid; c < kHeadDim * kHeadDim / 4; c += kAppThreads) cp_async16(st_s + 4 * c, p.St + 4 * c);
-    cp_async_commit();
+    const float mul = exp2f((float)-p.s_exp);
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float* at = p.St + (16 * k + 2 * (lane & 3) + 8 * h) * kHeadDim + 16 * warp + 8 * n + (lane >> 2);
+          const float a = __ldg(at) * mul, b = __ldg(at + kHeadDim) * mul;
+          frag[0][n][k][h] = half_pair(first_half(a), first_half(b));
+          frag[1][n][k][h] = half_pair(second_half(a), second_half(b));
+        }
   }
   float thr[7];
 #pragma unroll
   for (int i = 0; i < 7; ++i) thr[i] = i < nthr ? L.thr[i] : INFINITY;
   const float cent_lane = L.cent[(lane & 7) <= nthr ? (lane & 7) : 0];
-  bool st_ready = false;
 
   for (long long g = blockIdx.x; g < total; g += gridDim.x) {
     const int h = (int)(g % p.heads), first = (int)(g / p.heads) * TOK;
@@ -271,48 +296,48 @@ __global__ void __launch_bounds__(kAppThreads) quantize_slots(const __grid_const
       }
       if (L.qjl)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) sm.rho[i][32 * q + lane] = rho[q];
-    }
-    if (L.qjl && !st_ready) {
-      cp_async_wait<0>();
-      st_ready = true;
+        for (int q = 0; q < 4; ++q) {
+          sm.rho[0][i][32 * q + lane] = first_half(rho[q]);
+          sm.rho[1][i][32 * q + lane] = second_half(rho[q]);
+        }
     }
     __syncthreads();
 
-    if (L.qjl) {  // projections of 4 tokens onto rows 32 (R * share + r) + lane
-      const int quad = warp / kShare, share = warp % kShare;
-      float acc[4][R];
+    if (L.qjl) {
+#pragma unroll 1
+      for (int m = 0; m < AppSmem<TOK>::kRows / 16; ++m) {
+        float big[2][4] = {}, small[2][4] = {};
+        const uint32_t a0 = (uint32_t)__cvta_generic_to_shared(&sm.rho[0][16 * m + (lane & 15)][8 * (lane >> 4)]);
 #pragma unroll
-      for (int v = 0; v < 4; ++v)
+        for (int k = 0; k < 8; ++k) {
+          uint32_t a[2][4];
 #pragma unroll
-        for (int r = 0; r < R; ++r) acc[v][r] = 0.f;
-      const float* r0 = sm.rho[4 * quad];
-      const float* sc = st_s + 32 * R * share + lane;
-#pragma unroll 4
-      for (int i = 0; i < kHeadDim; i += 4) {
-        float4 rv[4];
+          for (int h = 0; h < 2; ++h)
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                         : "=r"(a[h][0]), "=r"(a[h][1]), "=r"(a[h][2]), "=r"(a[h][3])
+                         : "r"(a0 + h * (uint32_t)sizeof(sm.rho[0]) + 32 * k) : "memory");
 #pragma unroll
-        for (int v = 0; v < 4; ++v) rv[v] = *reinterpret_cast<const float4*>(r0 + v * kHeadDim + i);
-#pragma unroll
-        for (int ii = 0; ii < 4; ++ii) {
-          float sv[R];
-#pragma unroll
-          for (int r = 0; r < R; ++r) sv[r] = sc[(i + ii) * kHeadDim + 32 * r];
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const float x = ii == 0 ? rv[v].x : ii == 1 ? rv[v].y : ii == 2 ? rv[v].z : rv[v].w;
-#pragma unroll
-            for (int r = 0; r < R; ++r) acc[v][r] = fmaf(sv[r], x, acc[v][r]);
+          for (int n = 0; n < 2; ++n) {
+            mma16(big[n], a[0], frag[0][n][k]);
+            mma16(small[n], a[0], frag[1][n][k]);
+            mma16(small[n], a[1], frag[0][n][k]);
           }
         }
-      }
+        // rows lane / 4 (+ 8), columns 8 n + 2 (lane % 4) + {0, 1} of this warp's 16: half a sign word a row
 #pragma unroll
-      for (int v = 0; v < 4; ++v)
+        for (int h = 0; h < 2; ++h) {
+          uint32_t bits = 0;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const uint32_t w = __ballot_sync(0xffffffffu, acc[v][r] >= 0.f);
-          if (lane == r) sm.planes[4 * quad + v][kMaxBits][R * share + r] = w;
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (fmaf(small[n][2 * h + e], 1.f / kSecond, big[n][2 * h + e]) >= 0.f) bits |= 1u << (8 * n + 2 * (lane & 3) + e);
+          bits |= __shfl_xor_sync(0xffffffffu, bits, 1);
+          bits |= __shfl_xor_sync(0xffffffffu, bits, 2);
+          const int tok = 16 * m + 8 * h + (lane >> 2);
+          if ((lane & 3) == 0 && tok < TOK) reinterpret_cast<unsigned short*>(sm.planes[tok][kMaxBits])[warp] = (unsigned short)bits;
         }
+      }
       __syncthreads();
     }
 
@@ -320,43 +345,47 @@ __global__ void __launch_bounds__(kAppThreads) quantize_slots(const __grid_const
     auto tile_base = [&](long long slot) {
       return p.region[side] + (size_t)((slot / kPage * p.heads + h) * 2 + (slot % kPage) / kTile) * L.tile_bytes;
     };
-    for (int pp = warp; pp < nplanes; pp += kAppWarps) {
-      const int src = pp < L.bits ? pp : kMaxBits;
-      const int off = pp < L.bits ? L.off_planes + pp * (kTile * 16) : L.off_sketch;
-      if (L.order == kOrderOctet) {
-        // lane = word 8t + 2m + hh of an octet: byte i is coordinate 32m + 16hh + 4t + i, bit j token j.
-        // Tokens of one octet that follow one another in the batch leave together.
-        const int wt = lane >> 3, wm = (lane >> 1) & 3, wh = lane & 1;
+    if (L.order == kOrderOctet) {
+      // lane = word 8t + 2m + hh of an octet: byte i is coordinate 32m + 16hh + 4t + i, bit j token j.
+      // Tokens of one octet that follow one another in the batch (a run) leave together.
+      const int wt = lane >> 3, wm = (lane >> 1) & 3, wh = lane & 1;
+      const long long mine = lane < TOK && sm.slot[lane] >= 0 ? sm.slot[lane] >> 3 : -1;
+      const long long before = __shfl_up_sync(0xffffffffu, mine, 1);
+      const uint32_t starts = __ballot_sync(0xffffffffu, lane < TOK && (lane == 0 || mine != before));
+      const int runs = __popc(starts);
+      for (int u = warp; u < nplanes * runs; u += kAppWarps) {
+        const int pp = u / runs, src = pp < L.bits ? pp : kMaxBits;
+        uint32_t left = starts;
+        for (int r = u % runs; r > 0; --r) left &= left - 1;
+        const int from = __ffs(left) - 1;
+        left &= left - 1;
+        const int to = left ? __ffs(left) - 1 : TOK;
+        const long long slot0 = sm.slot[from];
+        if (slot0 < 0) continue;
         uint32_t word = 0, mask = 0;
-        long long octet = -1;
-        for (int i = 0; i <= TOK; ++i) {
-          const long long slot = i < TOK ? sm.slot[i] : -1;
-          const long long o = slot < 0 ? -1 : slot >> 3;
-          if (o != octet) {
-            if (octet >= 0) {
-              uint32_t* dst = reinterpret_cast<uint32_t*>(tile_base(octet << 3) + off) + (octet & 3) * 32 + lane;
-              if (mask == 0xffffffffu) {
-                *dst = word;
-              } else {
-                atomicAnd(dst, ~(mask & ~word));
-                atomicOr(dst, word);
-              }
-            }
-            octet = o;
-            word = mask = 0;
-          }
-          if (slot >= 0) {
-            const int j = (int)(slot & 7);
-            const uint32_t nib = (sm.planes[i][src][wm] >> (16 * wh + 4 * wt)) & 0xFu;
-            word = (word & ~(0x01010101u << j)) | (qlm::spread_nibble(nib) << j);
-            mask |= 0x01010101u << j;
-          }
+        for (int i = from; i < to; ++i) {
+          const int j = (int)(sm.slot[i] & 7);
+          const uint32_t nib = (sm.planes[i][src][wm] >> (16 * wh + 4 * wt)) & 0xFu;
+          word = (word & ~(0x01010101u << j)) | (qlm::spread_nibble(nib) << j);
+          mask |= 0x01010101u << j;
         }
-      } else {
-        for (int i = lane / 16; i < TOK; i += 2) {  // byte k of the row: two tokens a step
+        const int off = pp < L.bits ? L.off_planes + pp * (kTile * 16) : L.off_sketch;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(tile_base(slot0 & ~7ll) + off) + ((slot0 >> 3) & 3) * 32 + lane;
+        if (mask == 0xffffffffu) {
+          *dst = word;
+        } else {
+          atomicAnd(dst, ~(mask & ~word));
+          atomicOr(dst, word);
+        }
+      }
+    } else {
+      constexpr int kShares = TOK / 8;  // of a plane: 8 tokens, byte k of the row, two tokens a step
+      for (int u = warp; u < nplanes * kShares; u += kAppWarps) {
+        const int pp = u / kShares, src = pp < L.bits ? pp : kMaxBits, k = lane & 15;
+        const int off = pp < L.bits ? L.off_planes + pp * (kTile * 16) : L.off_sketch;
+        for (int i = 8 * (u % kShares) + lane / 16; i < 8 * (u % kShares) + 8; i += 2) {
           const long long slot = sm.slot[i];
           if (slot < 0) continue;
-          const int k = lane & 15;
           const char byte = (char)((sm.planes[i][src][k >> 2] >> (8 * (k & 3))) & 0xFFu);
           char* tb = tile_base(slot) + off;
           const int t = (int)(slot % kTile);
@@ -379,12 +408,9 @@ __global__ void __launch_bounds__(kAppThreads) quantize_slots(const __grid_const
 
 template <int TOK>
 cudaError_t launch_slots(const SlotQuantizeParams& p, cudaStream_t s) {
-  const bool sketch = p.side[0].qjl || p.side[1].qjl;
-  const size_t smem = (sizeof(AppSmem<TOK>) + 15) / 16 * 16 + (sketch ? sizeof(float) * kHeadDim * kHeadDim : 0);
-  cudaError_t e = cudaFuncSetAttribute(quantize_slots<TOK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
   const long long blocks = (long long)((p.n_tokens + TOK - 1) / TOK) * p.heads;
-  quantize_slots<TOK><<<dim3((unsigned)std::min<long long>(blocks, 148 * 4), 2), kAppThreads, smem, s>>>(p);
+  // two blocks fit an SM: as many of a side, which keep their fragments of S from one group to the next
+  quantize_slots<TOK><<<dim3((unsigned)std::min<long long>(blocks, 148 * 2), 2), kAppThreads, 0, s>>>(p);
   return launched();
 }
 

@@ -251,7 +251,8 @@ kvq_status kvq_slot_map(const int32_t* held, const int32_t* seq_start, const int
                         int32_t* seq_ids, int32_t* positions, int64_t* slots, void* stream);
 
 /* Quantize a token-major batch K, V [n_tokens, n_kv_heads, head_dim] (f32 or bf16) into slots[t] (device
- * int64) of a paged cache: the same codes, norms and sketch bits as kvq_quantize. A negative slot is
+ * int64) of a paged cache: the same codes and norms as kvq_quantize, and sketch bits that differ at most where
+ * a projection is within its fp32 rounding of zero. A negative slot is
  * skipped; one past the pool sets KVQ_STATUS_BAD_PAGE and is skipped. The slots of a call are distinct:
  * a slot named twice ends up with unspecified content (its neighbours keep theirs). The cache's lengths
  * do not change: give them to kvq_chunk_attention, or set them with kvq_cache_set_lengths. Caches that
