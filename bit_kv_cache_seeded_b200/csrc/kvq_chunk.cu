@@ -329,56 +329,73 @@ __global__ void __launch_bounds__(kPrepThreads, 2) chunk_prep(const __grid_const
 // value dims) for 16 (16 per 64 dims) FMAs. fp32 throughout.
 constexpr int kF32Rows = 64;
 
-__device__ __forceinline__ uint32_t plane_nibble(const unsigned char* plane, int order, int tok, int quad) {
-  // bits of token `tok` (of 32), coordinates 4 quad .. 4 quad + 3
-  if (order == kOrderOctet) {
-    const int t = quad & 3, h = (quad >> 2) & 1, m = quad >> 3;
-    const uint32_t w = reinterpret_cast<const uint32_t*>(plane)[(tok >> 3) * 32 + 8 * t + 2 * m + h] >> (tok & 7);
-    return (w & 1u) | ((w >> 7) & 2u) | ((w >> 14) & 4u) | ((w >> 21) & 8u);
+// Bits of token `tok` (of 32) at the coordinates 4 quad .. + 3 of the 8 quads part, part + 4, ..: 4 bits each, the first
+// lowest. All of a thread's loads are in flight at once: small calls have a page or two a CTA.
+__device__ __forceinline__ uint32_t plane_nibbles(const unsigned char* plane, int order, int tok, int part) {
+  uint32_t out = 0;
+  if (order == kOrderOctet) {  // quads of one t = part: 8 words on end
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(plane) + (tok >> 3) * 32 + 8 * part;
+    uint32_t x[8];
+#pragma unroll
+    for (int n = 0; n < 8; ++n) x[n] = __ldg(w + n) >> (tok & 7);
+#pragma unroll
+    for (int n = 0; n < 8; ++n)  // word 2 m + h is quad 8 m + 4 h + t
+      out |= ((x[n] & 1u) | ((x[n] >> 7) & 2u) | ((x[n] >> 14) & 4u) | ((x[n] >> 21) & 8u)) << (4 * n);
+    return out;
   }
-  const unsigned char byte = order == kOrderToken ? plane[tok * 16 + (quad >> 1)] : plane[(quad >> 1) * kTile + tok];
-  return (byte >> (4 * (quad & 1))) & 0xFu;
+  const int step = order == kOrderToken ? 1 : kTile;
+  const unsigned char* b = plane + (order == kOrderToken ? tok * 16 : tok) + (part >> 1) * step;
+  uint32_t x[8];
+#pragma unroll
+  for (int n = 0; n < 8; ++n) x[n] = __ldg(b + 2 * n * step);
+#pragma unroll
+  for (int n = 0; n < 8; ++n) out |= ((x[n] >> (4 * (part & 1))) & 0xFu) << (4 * n);
+  return out;
 }
 
 // Page `page` of one side as fp32, k-major dst: keys [dim][token], values [token][dim]. Sketch entries are
 // +-gamma; tokens at or behind `tokens` give zeros. scale[token] = norm.
 template <bool VALUES, bool QJL>
 __device__ __forceinline__ void dequant_f32(const ChunkParams& p, const SideLayout& L, const char* region, const Walk& w,
-                                            int page, int tokens, float* dst, float* scale) {
+                                            int page, int tokens, const float* cent, float* dst, float* scale) {
   const int tid = threadIdx.x;
-  const int tok = tid & 63, part = tid >> 6;
+  // neighbouring lanes: tokens of a key row, quads of a value row
+  const int tok = VALUES ? tid >> 2 : tid & 63, part = VALUES ? tid & 3 : tid >> 6;
   const long ti = tile_index_read(p.table, p.pages_per_seq, p.n_pages, p.tiles_per_seq, p.Hkv, w.rows.b, w.hk, 2 * page, p.err);
   const unsigned char* tb = reinterpret_cast<const unsigned char*>(region) + (size_t)(ti + (tok >> 5)) * L.tile_bytes;
   const int slot = tok & 31;
   constexpr int DIMS = QJL ? 2 * kHeadDim : kHeadDim;
   const bool in = tok < tokens;
-  float gamma = 0.f;
-  if (QJL && in) gamma = __half2float(reinterpret_cast<const __half*>(tb + L.off_gamma)[slot]);
+  uint32_t code[kMaxBits] = {}, sign = 0;
+#pragma unroll
+  for (int pp = 0; pp < kMaxBits; ++pp)
+    if (pp < L.bits) code[pp] = plane_nibbles(tb + L.off_planes + pp * (kTile * 16), L.order, slot, part);
+  if (QJL) sign = plane_nibbles(tb + L.off_sketch, L.order, slot, part);
+  float gamma = QJL ? __half2float(reinterpret_cast<const __half*>(tb + L.off_gamma)[slot]) : 0.f;
+  const float norm = __half2float(reinterpret_cast<const __half*>(tb + L.off_norm)[slot]);
+  if (!in) gamma = 0.f;
   // a residual norm that is not finite (a coded infinity or NaN) makes NaN of the rows that attend to the
   // token, through its scale, and must not reach the rows whose weight is 0 as 0 * NaN
   const bool bad = VALUES && QJL && !isfinite(gamma);
   if (bad) gamma = 0.f;
-  if (part == 0)
-    scale[tok] = bad ? NAN : in ? __half2float(reinterpret_cast<const __half*>(tb + L.off_norm)[slot]) : 0.f;
-  for (int quad = part; quad < DIMS / 4; quad += 4) {
-    float x[4] = {0.f, 0.f, 0.f, 0.f};
-    if (in) {
-      if (quad < kHeadDim / 4) {
-        uint32_t bits[kMaxBits];
+  if (part == 0) scale[tok] = bad ? NAN : in ? norm : 0.f;
 #pragma unroll
-        for (int pp = 0; pp < kMaxBits; ++pp)
-          bits[pp] = pp < L.bits ? plane_nibble(tb + L.off_planes + pp * (kTile * 16), L.order, slot, quad) : 0u;
+  for (int n = 0; n < DIMS / 16; ++n) {
+    const int quad = part + 4 * n, at = 4 * (n & 7);
+    float x[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          x[i] = L.cent[((bits[0] >> i) & 1u) | (((bits[1] >> i) & 1u) << 1) | (((bits[2] >> i) & 1u) << 2)];
-      } else {
-        const uint32_t z = plane_nibble(tb + L.off_sketch, L.order, slot, quad - kHeadDim / 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = (z >> i) & 1u ? gamma : -gamma;
-      }
+    for (int i = 0; i < 4; ++i) {
+      const int b = at + i;
+      if (n < 8) x[i] = cent[((code[0] >> b) & 1u) | (((code[1] >> b) & 1u) << 1) | (((code[2] >> b) & 1u) << 2)];
+      else x[i] = (sign >> b) & 1u ? gamma : -gamma;
+      if (!in) x[i] = 0.f;
     }
+    if (VALUES) {
+      *reinterpret_cast<float4*>(dst + tok * DIMS + 4 * quad) = make_float4(x[0], x[1], x[2], x[3]);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) dst[VALUES ? tok * DIMS + 4 * quad + i : (4 * quad + i) * 64 + tok] = x[i];
+      for (int i = 0; i < 4; ++i) dst[(4 * quad + i) * 64 + tok] = x[i];
+    }
   }
 }
 
@@ -389,6 +406,7 @@ struct F32Smem {
   float kv[(DK > DV ? DK : DV) * 64];
   float w[64][kF32Rows];
   float kn[64], vn[64];
+  float cent[2][8];  // codes: lanes look up different ones, which constant memory would serve in turn
 };
 
 template <bool KQ, bool VQ>
@@ -399,6 +417,7 @@ __global__ void __launch_bounds__(256) chunk_f32(const __grid_constant__ ChunkPa
   Smem& sm = *reinterpret_cast<Smem*>(smem);
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
   const ChunkSet& set = p.set[kWide];
+  if (tid < 16) sm.cent[tid >> 3][tid & 7] = (tid < 8 ? p.k : p.v).cent[tid & 7];
   grid_dep_wait();
   Walk w;
   w.init(p, set, blockIdx.x);
@@ -406,12 +425,11 @@ __global__ void __launch_bounds__(256) chunk_f32(const __grid_constant__ ChunkPa
     const Rows r = w.rows;
     const size_t qrow0 = (size_t)(r.start + r.first) * p.Hq + w.hk * p.group;
     __syncthreads();
-    for (int i = tid; i < kF32Rows * DK; i += 256) {
+    // rows past the last stay as they were: what they give is not kept
+#pragma unroll 4
+    for (int i = tid; i < r.count * DK; i += 256) {
       const int row = i / DK, k = i % DK;
-      float v = 0.f;
-      if (row < r.count)
-        v = static_cast<const float*>(p.qprep)[(qrow0 + (size_t)(row / p.group) * p.Hq + row % p.group) * DK + k];
-      sm.q[k][row] = v;
+      sm.q[k][row] = static_cast<const float*>(p.qprep)[(qrow0 + (size_t)(row / p.group) * p.Hq + row % p.group) * DK + k];
     }
     float m[4], l[4], o[4][C][4];
     int last[4];  // last position row i attends to
@@ -430,7 +448,7 @@ __global__ void __launch_bounds__(256) chunk_f32(const __grid_constant__ ChunkPa
       const int tokens = min(kPage, r.limit - k * kPage);
       if (tokens <= 0) break;  // a tile with no position at all
       __syncthreads();
-      dequant_f32<false, KQ>(p, p.k, p.kreg, w, k, tokens, sm.kv, sm.kn);
+      dequant_f32<false, KQ>(p, p.k, p.kreg, w, k, tokens, sm.cent[0], sm.kv, sm.kn);
       __syncthreads();
       float s[4][4];
 #pragma unroll
@@ -473,7 +491,7 @@ __global__ void __launch_bounds__(256) chunk_f32(const __grid_constant__ ChunkPa
         l[i] = fmaf(l[i], alpha[i], sum);
       }
       __syncthreads();  // every read of the key page is done
-      dequant_f32<true, VQ>(p, p.v, p.vreg, w, k, tokens, sm.kv, sm.vn);
+      dequant_f32<true, VQ>(p, p.v, p.vreg, w, k, tokens, sm.cent[1], sm.kv, sm.vn);
       __syncthreads();
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -584,7 +602,7 @@ __global__ void __launch_bounds__(kMergeThreads, VQ ? 2 : 3) chunk_merge(const _
       for (int x = 16; x > 0; x >>= 1) l[v] += __shfl_xor_sync(0xffffffffu, l[v], x);
       m[v] = top;
     }
-#pragma unroll 2
+#pragma unroll(BF16 ? 2 : 4)
     for (int c = c0; c <= c1; ++c) {
       const float2* ml = reinterpret_cast<const float2*>(segment_ml(set, item, c, DV)) + row0;
       const float* so = segment_o(set, item, c, DV) + (size_t)row0 * DV;
