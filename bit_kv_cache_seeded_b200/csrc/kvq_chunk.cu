@@ -267,17 +267,25 @@ __global__ void __launch_bounds__(kPrepThreads, 2) chunk_prep(const __grid_const
       }
     } else if (KQ) {  // rows j = 4 lane .. + 3 of S q~, from S^T [i][j]
       __syncwarp();
-#pragma unroll 16
-      for (int i = 0; i < kHeadDim; ++i) {
-        const float4 st = __ldg(reinterpret_cast<const float4*>(p.St + i * kHeadDim) + lane);
+#pragma unroll 1
+      for (int i0 = 0; i0 < kHeadDim; i0 += 16) {
+        float part[4][4] = {};
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const float x = s_q[4 * warp + v][i];
-          sk[v][0] = fmaf(st.x, x, sk[v][0]);
-          sk[v][1] = fmaf(st.y, x, sk[v][1]);
-          sk[v][2] = fmaf(st.z, x, sk[v][2]);
-          sk[v][3] = fmaf(st.w, x, sk[v][3]);
+        for (int i = i0; i < i0 + 16; ++i) {
+          const float4 st = __ldg(reinterpret_cast<const float4*>(p.St + i * kHeadDim) + lane);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const float x = s_q[4 * warp + v][i];
+            part[v][0] = fmaf(st.x, x, part[v][0]);
+            part[v][1] = fmaf(st.y, x, part[v][1]);
+            part[v][2] = fmaf(st.z, x, part[v][2]);
+            part[v][3] = fmaf(st.w, x, part[v][3]);
+          }
         }
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sk[v][k] += part[v][k];
       }
       __syncwarp();
     }
@@ -455,15 +463,23 @@ __global__ void __launch_bounds__(256) chunk_f32(const __grid_constant__ ChunkPa
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 1
+      for (int d0 = 0; d0 < DK; d0 += 32) {  // 32 products at a time: the sum's rounding grows with the steps behind one
+        float part[4][4] = {};
 #pragma unroll 8
-      for (int d = 0; d < DK; ++d) {
-        const float4 a = *reinterpret_cast<const float4*>(&sm.q[d][4 * ty]);
-        const float4 b = *reinterpret_cast<const float4*>(&sm.kv[d * 64 + 4 * tx]);
-        const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+        for (int d = d0; d < d0 + 32; ++d) {
+          const float4 a = *reinterpret_cast<const float4*>(&sm.q[d][4 * ty]);
+          const float4 b = *reinterpret_cast<const float4*>(&sm.kv[d * 64 + 4 * tx]);
+          const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) part[i][j] = fmaf(av[i], bv[j], part[i][j]);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s[i][j] = fmaf(av[i], bv[j], s[i][j]);
+          for (int j = 0; j < 4; ++j) s[i][j] += part[i][j];
       }
       float alpha[4];
 #pragma unroll
@@ -650,17 +666,25 @@ __global__ void __launch_bounds__(kMergeThreads, VQ ? 2 : 3) chunk_merge(const _
       }
     } else if (VQ) {
       __syncwarp();
-#pragma unroll 16
-      for (int j = 0; j < kHeadDim; ++j) {
-        const float4 sj = __ldg(reinterpret_cast<const float4*>(p.S + j * kHeadDim) + lane);
+#pragma unroll 1
+      for (int j0 = 0; j0 < kHeadDim; j0 += 16) {
+        float part[4][4] = {};
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const float x = s_z[4 * warp + v][j];
-          acc[v][0] = fmaf(sj.x, x, acc[v][0]);
-          acc[v][1] = fmaf(sj.y, x, acc[v][1]);
-          acc[v][2] = fmaf(sj.z, x, acc[v][2]);
-          acc[v][3] = fmaf(sj.w, x, acc[v][3]);
+        for (int j = j0; j < j0 + 16; ++j) {
+          const float4 sj = __ldg(reinterpret_cast<const float4*>(p.S + j * kHeadDim) + lane);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const float x = s_z[4 * warp + v][j];
+            part[v][0] = fmaf(sj.x, x, part[v][0]);
+            part[v][1] = fmaf(sj.y, x, part[v][1]);
+            part[v][2] = fmaf(sj.z, x, part[v][2]);
+            part[v][3] = fmaf(sj.w, x, part[v][3]);
+          }
         }
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[v][k] += part[v][k];
       }
       __syncwarp();
     }
