@@ -121,7 +121,7 @@ __device__ __forceinline__ int query_pos(int order, int lane) {
   if (order == kOrderOctet) return 32 * (lane & 3) + 8 * (lane >> 3) + 4 * ((lane >> 2) & 1);
   return 64 * (lane >> 4) + 32 * (lane & 1) + ((lane >> 1) & 7);
 }
-constexpr float kCodeScale = 8.f, kSketchScale = 16.f;  // their operands hold 1/8 of a code, 1/16 of a sketch entry
+constexpr float kCodeScale = 4.f, kSketchScale = 16.f;  // their operands hold 1/4 of a code, 1/16 of a sketch entry
 
 // Launches a kernel of the call that starts while its predecessor ends (grid_dep_wait before it reads what that wrote).
 inline cudaError_t launch_after(void (*kernel)(ChunkParams), const ChunkParams& p, unsigned blocks, unsigned threads, int smem,

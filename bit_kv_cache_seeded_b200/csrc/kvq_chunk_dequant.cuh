@@ -7,8 +7,9 @@
 // octet order give a thread coordinates 32 m + 16 h + 4 t + i of 8 tokens; the queries are stored in that
 // order (query_pos), since the product does not mind which way its K-elements are numbered.
 //
-// Entries are n c / 8 (a code times the token's norm) and +-n gamma / 16 (a sign bit): the powers of two keep
-// every fp16 norm's entries in range, and the queries and the merge carry their inverses. A value whose norm is
+// Entries are n c / 4 (a code times the token's norm) and +-n gamma / 16 (a sign bit): the powers of two keep
+// every fp16 norm's entries in range, and the queries and the merge carry their inverses. (Norms under 2^-10 give
+// entries among fp16's subnormal numbers, with fewer bits.) A value whose norm is
 // not finite enters as zeros (0 p would be NaN in every row); the rows that attend to it get a NaN sum from the
 // page's mask instead.
 #pragma once
@@ -85,15 +86,15 @@ struct Codes {
   }
 };
 
-// A side's codes as halves (Codes::next), eighths of them.
+// A side's codes as halves (Codes::next), quarters of them.
 __device__ __forceinline__ uint2 code_halves(const SideLayout& L) {
   uint32_t lo, hi;
   if (L.bits == 1) {
-    lo = hi = half_bits(L.cent[1] * 0.125f) * 0x10001u;
+    lo = hi = half_bits(L.cent[1] * 0.25f) * 0x10001u;
   } else {
     const int at = L.bits == 3 ? 4 : 0;
-    lo = half_bits(L.cent[at] * 0.125f) | half_bits(L.cent[at + 1] * 0.125f) << 16;
-    hi = half_bits(L.cent[at + 2] * 0.125f) | half_bits(L.cent[at + 3] * 0.125f) << 16;
+    lo = half_bits(L.cent[at] * 0.25f) | half_bits(L.cent[at + 1] * 0.25f) << 16;
+    hi = half_bits(L.cent[at + 2] * 0.25f) | half_bits(L.cent[at + 3] * 0.25f) << 16;
   }
   return make_uint2(lo, hi);
 }

@@ -276,7 +276,8 @@ kvq_status kvq_cache_set_lengths(kvq_cache* c, const int32_t* lens, void* stream
  * with no position to attend to (ctx_lens[b] < n_new) gets zeros; rows before seq_start[0] or behind the
  * last request are left as they are. ctx_lens is cut to [0, capacity]. Logits and softmax as for
  * kvq_decode_attention (n_new = 1 for every request computes the same attention); f32 queries are
- * computed in fp32, bf16 ones on the tensor cores in fp16 with fp32 sums and statistics.
+ * computed in fp32, bf16 ones on the tensor cores in fp16 with fp32 sums and statistics (value norms under 2^-10
+ * keep fewer than fp16's 11 bits there).
  * LM, LM_QJL and SIGN1 caches without a window, paged or not; others KVQ_ERR_UNSUPPORTED. n_tokens * n_q_heads may not
  * exceed 2^30. A block-table entry outside the pool sets KVQ_STATUS_BAD_PAGE and reads page 0. The
  * workspace (kvq_chunk_workspace_bytes for this type and n_tokens) is in use until the call's work is

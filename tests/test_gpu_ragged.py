@@ -420,3 +420,81 @@ def test_the_same_call_gives_the_same_bits():
     for _ in range(4):
         assert torch.equal(x.cache.chunk_attention(x.q, x.seq_start, x.ctx_lens), first)
     x.cache.close()
+
+
+@pytest.mark.parametrize("name,group", [("2q2q", 4), ("3q3", 8), ("22", 1), ("23q", 2)])
+@pytest.mark.parametrize("rows", [24, 32, 40, 128, 136, 256, 264, 512, 520, 1032])
+def test_row_counts_around_the_tiles(rows, name, group):
+    """The last rows of the narrow kernel's tile, of a CTA's half, of a tile and of a pair of them, and one token
+    more: beside a request of a single token."""
+    x = Batch(make_cfg(group, 1, *MODES[name]), [77, 300], [rows // group, 1], seed=rows)
+    out = x.cache.chunk_attention(x.q, x.seq_start, x.ctx_lens)
+    assert kvq.kvq_cache_status(x.cache.handle) == 0
+    assert_close(out, x.reference(), BF16)
+    x.cache.close()
+
+
+@pytest.mark.parametrize("batch", [255, 257, 520])
+def test_chunk_attention_of_many_requests(batch):
+    """More requests than a block of the plan has threads, some without tokens, some with a wide tile."""
+    rng = np.random.default_rng(batch)
+    new = rng.integers(0, 4, batch)
+    new[[5, batch - 2]] = [50, 70]
+    x = Batch(make_cfg(2, 1, 2, True, 2, True), rng.integers(0, 150, batch), new, seed=batch)
+    for q in (x.q, x.q.float()):
+        assert_close(x.cache.chunk_attention(q, x.seq_start, x.ctx_lens), x.reference(q), q.dtype)
+    x.cache.close()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("new", [3, 30, 200])
+@pytest.mark.parametrize("name", ["2q2q", "33"])
+def test_maxima_that_grow_along_the_context(name, new, dtype):
+    """Keys that point more and more along the queries: a row's maximum grows by far more than the lag that its
+    reference may have, in every part of a page and many times over, so that what was summed before has to
+    follow. At the end one position holds nearly all of the weight; before, several."""
+    cfg = make_cfg(4, 1, *MODES[name])
+    held = 700
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    way = torch.randn(128, generator=gen, device="cuda")
+    n = held + new
+    size = torch.linspace(0.02, 3.0, n, device="cuda")[:, None, None]
+    k = (way * size + 0.3 * torch.randn(n, 1, 128, generator=gen, device="cuda")).to(dtype)
+    v = torch.randn(n, 1, 128, generator=gen, device="cuda").to(dtype)
+    x = Batch(cfg, [0], [n], dtype, seed=21, k=k, v=v)
+    q = (way * 0.8 + 0.3 * torch.randn(new, 4, 128, generator=gen, device="cuda")).to(dtype)
+    x.new = np.array([new])
+    out = x.cache.chunk_attention(q, cuda_ints([0, new]), x.ctx_lens)
+    ref = x.reference(q)
+    # logits up to 0.8 * 3 * |way|^2 / sqrt(128), about 27: an operand's half step of 2^-11 on each product, three of them
+    # and of either sign, moves one by up to 3 * 2^-11 * 27 / sqrt(128) * 4 (four sigma) = 0.014, the weights that
+    # share a row by as much of their size
+    top = np.abs(ref).max(-1, keepdims=True)
+    tol = 2e-4 * top if dtype == F32 else 0.03 * top + 2.0 ** -8 * np.abs(ref)
+    assert (np.abs(out.double().cpu().numpy() - ref) <= tol).all()
+    x.cache.close()
+
+
+def test_long_context_of_one_token():
+    """A single token over a context that every CTA of the narrow kernel shares."""
+    x = Batch(make_cfg(4, 1, 2, True, 2, True), [40000], [1], seed=22)
+    out = x.cache.chunk_attention(x.q, x.seq_start, x.ctx_lens)
+    x.cache.set_lengths([40001])
+    ref = x.cache.decode(x.q)
+    top = ref.abs().amax(-1, keepdim=True)
+    # decode is within 2e-3 of a row's largest entry (its own tests); this call as in assert_close
+    assert ((out.double() - ref.double()).abs() <= (7e-3 * top + 2.0 ** -8 * ref.abs())).all()
+    x.cache.close()
+
+
+def test_on_a_stream_given_by_name():
+    x = Batch(make_cfg(8, 2, 2, True, 2, True), [600, 3], [40, 2], seed=23)
+    want = x.cache.chunk_attention(x.q, x.seq_start, x.ctx_lens)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out = torch.zeros_like(x.q)
+    x.cache.chunk_attention(x.q, x.seq_start, x.ctx_lens, out=out, stream=s)
+    s.synchronize()
+    assert torch.equal(out, want)
+    assert len(x.cache.chunk_workspaces) == 2
+    x.cache.close()
