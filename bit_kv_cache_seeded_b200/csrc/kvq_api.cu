@@ -1346,8 +1346,7 @@ kvq_status kvq_chunk_attention(const kvq_cache* c, const void* q, kvq_dtype dtyp
     to.ctas = from.ctas;
     to.max_tiles = from.max_tiles;
     to.unit_start = reinterpret_cast<long long*>(w + from.unit_start);
-    to.tile_seq = reinterpret_cast<int*>(w + from.tile_seq);
-    to.tile_rows = reinterpret_cast<int2*>(w + from.tile_rows);
+    to.tile_rows = reinterpret_cast<int4*>(w + from.tile_rows);
     to.tile_start = reinterpret_cast<int*>(w + from.tile_start);
     to.head = reinterpret_cast<long long*>(w + from.head);
     to.part = reinterpret_cast<float*>(w + from.part);

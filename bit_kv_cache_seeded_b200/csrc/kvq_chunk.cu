@@ -134,6 +134,17 @@ __device__ __forceinline__ float store_row(__half* a, const float (&u)[4], int l
   return pow2(e);
 }
 
+// Brings a 128 x 128 fp32 matrix into the L1 (256 threads): its rows are needed one after another, and a small call
+// has nothing else to hide their latency under.
+__device__ __forceinline__ void warm_l1(const float* m) {
+#pragma unroll
+  for (int i = 0; i < kHeadDim * kHeadDim / 4 / 256; ++i) {
+    float a, b, c, d;
+    asm volatile("ld.global.v4.f32 {%0,%1,%2,%3}, [%4];\n"
+                 : "=f"(a), "=f"(b), "=f"(c), "=f"(d) : "l"(m + 4 * (256 * i + (int)threadIdx.x)));
+  }
+}
+
 // One block's plan of a set: row tiles per request, their units, prefix sums of both.
 __device__ void plan(const ChunkParams& p, const ChunkSet& s) {
   __shared__ long long s_warp[kPrepThreads / 32];
@@ -184,9 +195,8 @@ __device__ void plan(const ChunkParams& p, const ChunkSet& s) {
         if (s.tile_start[mid] <= t) lo = mid;
         else hi = mid;
       }
-      s.tile_seq[t] = lo;
       const Rows r = tile_rows(p, s, lo, t - s.tile_start[lo]);
-      s.tile_rows[t] = make_int2(r.start + r.first, r.count);
+      store_rows(s, t, r);
       units = max(1, (r.limit + s.unit - 1) / s.unit);
     }
     const long long at = scan(units);
@@ -217,6 +227,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) chunk_prep(const __grid_const
   constexpr int DK = KQ ? 2 * kHeadDim : kHeadDim;
   Frags frags;
   if (KQ && BF16) load_frags(frags, p.St, p.s_exp, warp, lane);
+  else if (KQ) warm_l1(p.St);
   float next[4][4];  // the next group's queries, loaded a group ahead
   auto fetch = [&](int group) {
 #pragma unroll
@@ -429,7 +440,7 @@ __global__ void __launch_bounds__(256) chunk_f32(const __grid_constant__ ChunkPa
   grid_dep_wait();
   Walk w;
   w.init(p, set, blockIdx.x);
-  while (w.next(p, set)) {
+  while (w.next(set)) {
     const Rows r = w.rows;
     const size_t qrow0 = (size_t)(r.start + r.first) * p.Hq + w.hk * p.group;
     __syncthreads();
@@ -463,8 +474,9 @@ __global__ void __launch_bounds__(256) chunk_f32(const __grid_constant__ ChunkPa
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+      const bool rows_here = 4 * (ty & ~1) < r.count;  // of this warp's 8
 #pragma unroll 1
-      for (int d0 = 0; d0 < DK; d0 += 32) {  // 32 products at a time: the sum's rounding grows with the steps behind one
+      for (int d0 = 0; rows_here && d0 < DK; d0 += 32) {  // 32 products at a time: the sum's rounding grows with the steps behind one
         float part[4][4] = {};
 #pragma unroll 8
         for (int d = d0; d < d0 + 32; ++d) {
@@ -528,7 +540,7 @@ __global__ void __launch_bounds__(256) chunk_f32(const __grid_constant__ ChunkPa
 #pragma unroll
           for (int j = 0; j < 4; ++j) o[i][c][j] *= alpha[i];
 #pragma unroll 4
-      for (int t = 0; t < kPage; ++t) {
+      for (int t = 0; rows_here && t < kPage; ++t) {
         const float4 a = *reinterpret_cast<const float4*>(&sm.w[t][4 * ty]);
         const float av[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
@@ -568,6 +580,7 @@ __global__ void __launch_bounds__(kMergeThreads, VQ ? 2 : 3) chunk_merge(const _
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Frags frags;
   if (VQ && BF16) load_frags(frags, p.S, p.s_exp, warp, lane);
+  else if (VQ) warm_l1(p.S);
   grid_dep_wait();
   int groups = 0, first[2];  // groups of both sets, one after the other
   for (int i = 0; i < p.sets; ++i) {
@@ -582,9 +595,9 @@ __global__ void __launch_bounds__(kMergeThreads, VQ ? 2 : 3) chunk_merge(const _
     const int item = group / per;
     const int hk = item / tiles, tile = item % tiles;
     const int group0 = group % per * kMergeRows, row0 = group0 + 4 * warp;
-    const int2 r = set.tile_rows[tile];  // token of the first row, rows
+    const int4 r = set.tile_rows[2 * tile];  // request, first token in it, rows, the request's first token
     const long long u0 = set.unit_start[tile], u1 = set.unit_start[tile + 1];
-    if (group0 >= r.y) continue;
+    if (group0 >= r.z) continue;
     const int c0 = cta_of(hk * units + u0, T, G);
     const int c1 = cta_of(hk * units + u1 - 1, T, G);
     // the segments' maxima and sums first, a lane per segment; then their rows, four in flight
@@ -600,7 +613,7 @@ __global__ void __launch_bounds__(kMergeThreads, VQ ? 2 : 3) chunk_merge(const _
       const float2* ml = reinterpret_cast<const float2*>(segment_ml(set, item, c, DV)) + row0;
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        if (row0 + v >= r.y) continue;
+        if (row0 + v >= r.z) continue;
         const float2 s = ml[v];
         const float top = fmaxf(m[v], s.x);
         // a NaN sum (a logit that is NaN: the maximum passes over it) stays, an empty part adds nothing
@@ -626,7 +639,7 @@ __global__ void __launch_bounds__(kMergeThreads, VQ ? 2 : 3) chunk_merge(const _
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         f[v] = -INFINITY;
-        if (row0 + v >= r.y) continue;
+        if (row0 + v >= r.z) continue;
         f[v] = ml[v].x;
         load4(o[v], so + v * DV, false, lane);
         if (VQ) load4(z[v], so + v * DV + kHeadDim, false, lane);
@@ -694,9 +707,9 @@ __global__ void __launch_bounds__(kMergeThreads, VQ ? 2 : 3) chunk_merge(const _
     for (int v = 0; v < 4; ++v) {
       fwht(acc[v], lane);
       const int row = row0 + v;
-      if (row >= r.y) continue;
+      if (row >= r.z) continue;
       const float f = l[v] > 0.f ? (BF16 ? kCodeScale : 1.f) / (kHeadDim * l[v]) : l[v];  // 0: nothing attended; or NaN
-      const size_t at = ((size_t)(r.x + row / p.group) * p.Hq + hk * p.group + row % p.group) * kHeadDim;
+      const size_t at = ((size_t)(r.w + r.y + row / p.group) * p.Hq + hk * p.group + row % p.group) * kHeadDim;
 #pragma unroll
       for (int k = 0; k < 4; ++k) acc[v][k] *= f * sg[k];
       if (BF16)
@@ -759,8 +772,7 @@ ChunkLayout chunk_layout(int n_tokens, int batch, int Hq, int Hkv, bool k_qjl, b
     if (n_tokens * (long long)group <= s.above) s.max_tiles = 0;
     s.head = take(2 * sizeof(long long));
     s.unit_start = take(sizeof(long long) * ((size_t)s.max_tiles + 1));
-    s.tile_seq = take(sizeof(int) * (size_t)s.max_tiles);
-    s.tile_rows = take(sizeof(int2) * (size_t)s.max_tiles);
+    s.tile_rows = take(2 * sizeof(int4) * (size_t)s.max_tiles);
     s.tile_start = take(sizeof(int) * ((size_t)batch + 1));
     const size_t segments = s.max_tiles ? (size_t)s.max_tiles * Hkv + s.ctas : 0;
     s.part = take(sizeof(float) * segments * s.rows * (2 + kHeadDim * (v_qjl ? 2 : 1)));

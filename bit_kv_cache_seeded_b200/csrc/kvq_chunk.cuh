@@ -2,8 +2,9 @@
 // segments leave behind.
 //
 // Rows. A kv-head of request b has n_b * group query rows, row r = token r / group, head r % group. A set (ChunkSet)
-// takes the requests whose rows are within its bounds. (A pair of CTAs counts as one CTA here.) Row tiles of `rows` rows never cross a request; tile t of a
-// kv-head belongs to request tile_seq[t], the tiles of request b being tile_start[b] .. tile_start[b + 1] - 1.
+// takes the requests whose rows are within its bounds. (A pair of CTAs counts as one CTA here.) Row tiles of `rows` rows never cross a request; the tiles of
+// request b are tile_start[b] .. tile_start[b + 1] - 1, and tile_rows[t] describes tile t, so that a segment starts one
+// load after it knows its tile.
 //
 // Units. Tile t attends to the positions below its limit, the last row's position + 1, in units of one or two
 // 64-token pages; unit_start[t] is the prefix sum of max(1, ceil(limit / unit)). The units of all kv-heads
@@ -50,6 +51,15 @@ __device__ __forceinline__ Rows tile_rows(const ChunkParams& p, const ChunkSet& 
   return r;
 }
 
+__device__ __forceinline__ void store_rows(const ChunkSet& s, int tile, const Rows& r) {
+  s.tile_rows[2 * tile] = make_int4(r.b, r.first, r.count, r.start);
+  s.tile_rows[2 * tile + 1] = make_int4(r.pos0, r.ctx, r.limit, 0);
+}
+__device__ __forceinline__ Rows load_rows(const ChunkSet& s, int tile) {
+  const int4 x = s.tile_rows[2 * tile], y = s.tile_rows[2 * tile + 1];
+  return Rows{x.x, x.y, x.z, x.w, y.x, y.y, y.z};
+}
+
 // CTAs that share T units (each has one at least), and the CTA that owns unit u: the largest c with
 // floor(c T / G) <= u.
 __device__ __forceinline__ long long cta_count(const ChunkSet& s, long long T) { return min((long long)s.ctas, T); }
@@ -88,7 +98,7 @@ struct Walk {
     }
     tile = lo;
   }
-  __device__ __forceinline__ bool next(const ChunkParams& p, const ChunkSet& s) {
+  __device__ __forceinline__ bool next(const ChunkSet& s) {
     if (u >= end) return false;
     if (tile == tiles) {
       tile = 0;
@@ -100,8 +110,7 @@ struct Walk {
     k0 = (int)(u - t0);
     k1 = (int)(stop - t0);
     item = (long long)hk * tiles + tile;
-    const int b = s.tile_seq[tile];
-    rows = tile_rows(p, s, b, tile - s.tile_start[b]);
+    rows = load_rows(s, tile);
     u = stop;
     if (stop == t1) ++tile;
     return true;

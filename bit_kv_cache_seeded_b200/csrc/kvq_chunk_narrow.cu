@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow(const __grid_constan
     const uint32_t lanes = (uint32_t)(32 * warp) << 16;
     const uint32_t tS = tmem + lanes, tO = tmem + lanes + kColO;
     int n = 0;
-    while (w.next(p, set)) {
+    while (w.next(set)) {
       const Rows r = w.rows;
       const int ns = segment_steps(w);
       if (tid < N) {
@@ -271,25 +271,30 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow(const __grid_constan
     const uint2 lut = code_halves(p.k);
     int n = 0, seg = 0;  // n: parts handed over
     PageRegs regs = {};
-    while (w.next(p, set)) {
+    while (w.next(set)) {
       const Rows r = w.rows;
       const int ns = segment_steps(w);
       if (ns == 0) continue;
       int page = 2 * w.k0 + second;
       if (page * kPage < r.limit) keys.fetch(p, regs, page_tile(p, w, page, page_entry(p, w, page)));
       int entry = page_entry(p, w, page + 2);  // of the page after the one in regs
+      constexpr int kChunks = DK / 8, kOwn = N * kChunks / 256;
+      const size_t qrow0 = (size_t)(r.start + r.first) * p.Hq + w.hk * p.group;
+      uint4 v[kOwn];  // loaded while the last segment's products still read theirs
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) {
+        const int row = (all + 256 * i) / kChunks, ch = all % kChunks;
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (row < r.count)
+          v[i] = *(reinterpret_cast<const uint4*>(static_cast<const __half*>(p.qprep) +
+                                                  (qrow0 + (size_t)(row / p.group) * p.Hq + row % p.group) * DK) + ch);
+      }
       if (seg > 0) wait(bars.qempty, (seg - 1) & 1);
       ++seg;
-      constexpr int kChunks = DK / 8;
-      const size_t qrow0 = (size_t)(r.start + r.first) * p.Hq + w.hk * p.group;
 #pragma unroll
-      for (int i = all; i < N * kChunks; i += 256) {
-        const int row = i / kChunks, ch = i % kChunks;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (row < r.count)
-          v = *(reinterpret_cast<const uint4*>(static_cast<const __half*>(p.qprep) +
-                                               (qrow0 + (size_t)(row / p.group) * p.Hq + row % p.group) * DK) + ch);
-        *reinterpret_cast<uint4*>(smem + (ch >> 3) * (N * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = v;
+      for (int i = 0; i < kOwn; ++i) {
+        const int row = (all + 256 * i) / kChunks, ch = all % kChunks;
+        *reinterpret_cast<uint4*>(smem + (ch >> 3) * (N * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = v[i];
       }
       arrive_rows(bars.qfull);
       for (int j = 0; j < ns; ++j, page += 2) {
@@ -319,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow(const __grid_constan
     const uint2 lut = code_halves(p.v);
     int n = 0;
     PageRegs regs = {};
-    while (w.next(p, set)) {
+    while (w.next(set)) {
       const int ns = segment_steps(w), limit = w.rows.limit;
       if (ns == 0) continue;
       int page = 2 * w.k0 + second;
@@ -344,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow(const __grid_constan
     if (warp == kWarpS) {  // ---- S^T = K Q^T (the whole warp, so that control stays uniform)
       constexpr uint32_t id = tc::idesc_f16(0, 0, 0, kStep, N);
       int n = 0, seg = 0;
-      while (w.next(p, set)) {
+      while (w.next(set)) {
         const int ns = __shfl_sync(0xffffffffu, segment_steps(w), 0);
         if (ns == 0) continue;
         wait(bars.qfull, seg & 1);
@@ -372,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow(const __grid_constan
     } else if (warp == kWarpO) {  // ---- O^T += V^T P^T
       constexpr uint32_t id = tc::idesc_f16(0, 0, 1, 128, N);
       int n = 0;
-      while (w.next(p, set)) {
+      while (w.next(set)) {
         const int ns = __shfl_sync(0xffffffffu, segment_steps(w), 0);
         for (int j = 0; j < ns; ++j, ++n) {
           const int st = n % C::VS, b = n & 1;

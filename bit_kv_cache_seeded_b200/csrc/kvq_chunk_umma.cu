@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tO = tmem + lanes + t * DV, tS = tmem + lanes + kColS + t * NB * kPage;
     int n = 0, seg = 0;  // pages this tile, and segments the pair, has seen
-    while (w.next(p, set)) {
+    while (w.next(set)) {
       const Rows r = w.rows;
       const int ns = segment_pages(w);
       const bool used = t * 2 * kTileRows < r.count && ns > 0;
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
     const uint2 lut = code_halves(p.k);
     int n = 0, seg = 0;
     PageRegs regs = {};
-    while (w.next(p, set)) {
+    while (w.next(set)) {
       const Rows r = w.rows;
       const int ns = segment_pages(w);
       if (ns == 0) continue;
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
     const uint2 lut = code_halves(p.v);
     int n = 0, seg = 0;
     PageRegs regs = {};
-    while (w.next(p, set)) {
+    while (w.next(set)) {
       const int ns = segment_pages(w), limit = w.rows.limit;
       if (ns == 0) continue;
       if (th == 0 && grp == 0) bars.bad[(seg + kSlots / 2) % kSlots] = 0x7fffffff;  // last used half a round ago
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
     if (rank == 0 && warp == C::kWarpS) {  // ---- S = Q K^T (the whole warp, so that control stays uniform)
       constexpr uint32_t id = tc::idesc_f16(0, 0, 0, 2 * kTileRows, kPage);
       int n = 0, seg = 0, nt[NT] = {};
-      while (w.next(p, set)) {
+      while (w.next(set)) {
         const int ns = __shfl_sync(0xffffffffu, segment_pages(w), 0), count = __shfl_sync(0xffffffffu, w.rows.count, 0);
         if (ns == 0) continue;
         wait_both(bars.qfull, seg & 1);
@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
     } else if (rank == 0 && warp == C::kWarpO) {  // ---- O += P V
       constexpr uint32_t id = tc::idesc_f16(0, 0, 0, 2 * kTileRows, DV);
       int n = 0, nt[NT] = {};
-      while (w.next(p, set)) {
+      while (w.next(set)) {
         const int ns = __shfl_sync(0xffffffffu, segment_pages(w), 0), count = __shfl_sync(0xffffffffu, w.rows.count, 0);
         for (int j = 0; j < ns; ++j, ++n) {
           const int st = n % kStages;

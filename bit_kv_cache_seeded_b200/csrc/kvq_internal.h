@@ -192,8 +192,7 @@ struct ChunkSet {
   int ctas;                 // CTAs (wide set: pairs of them) that share the units
   int max_tiles;            // row tiles of one kv-head the workspace holds
   long long* unit_start;    // [max_tiles + 1]
-  int* tile_seq;            // [max_tiles]
-  int2* tile_rows;          // [max_tiles]: first row's token in the batch, rows in use (for the merge)
+  int4* tile_rows;          // [max_tiles][2]: the row tiles (chunk::Rows)
   int* tile_start;          // [B + 1]
   long long* head;          // row tiles of a kv-head, units of a kv-head
   float* part;              // softmax states of the segments
@@ -234,7 +233,7 @@ struct ChunkParams {
 struct ChunkLayout {
   struct Set {
     int above, upto, rows, unit, ctas, max_tiles;
-    size_t unit_start, tile_seq, tile_rows, tile_start, head, part;
+    size_t unit_start, tile_rows, tile_start, head, part;
   } set[2];
   int sets;
   size_t qprep, qscale, total;
