@@ -445,10 +445,20 @@ __global__ void __launch_bounds__(256) chunk_f32(const __grid_constant__ ChunkPa
     const size_t qrow0 = (size_t)(r.start + r.first) * p.Hq + w.hk * p.group;
     __syncthreads();
     // rows past the last stay as they were: what they give is not kept
-#pragma unroll 4
-    for (int i = tid; i < r.count * DK; i += 256) {
-      const int row = i / DK, k = i % DK;
-      sm.q[k][row] = static_cast<const float*>(p.qprep)[(qrow0 + (size_t)(row / p.group) * p.Hq + row % p.group) * DK + k];
+    for (int i0 = tid; i0 < r.count * DK; i0 += 8 * 256) {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int i = i0 + e * 256, row = i / DK;
+        v[e] = 0.f;
+        if (i < r.count * DK)
+          v[e] = static_cast<const float*>(p.qprep)[(qrow0 + (size_t)(row / p.group) * p.Hq + row % p.group) * DK + i % DK];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int i = i0 + e * 256;
+        if (i < r.count * DK) sm.q[i % DK][i / DK] = v[e];
+      }
     }
     float m[4], l[4], o[4][C][4];
     int last[4];  // last position row i attends to

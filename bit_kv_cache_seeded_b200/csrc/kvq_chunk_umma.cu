@@ -340,17 +340,21 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
       ++seg;
       constexpr int kChunks = DK / 8;
       const size_t qrow0 = (size_t)(r.start + r.first) * p.Hq + w.hk * p.group;
-#pragma unroll 8
+      // copied asynchronously: loads that wait for one another's stores took 19000 cycles a segment, registers to hold
+      // them spilled
+#pragma unroll 4
       for (int i = all; i < NT * kTileRows * kChunks; i += 64 * C::KG) {
         const int here = i / kChunks, ch = i % kChunks;
         const int t = here / kTileRows, rr = here & (kTileRows - 1), row = t * 2 * kTileRows + rank * kTileRows + rr;
-        uint4 v = make_uint4(0, 0, 0, 0);
+        unsigned char* dst = smem + t * C::kQTile + (ch >> 3) * (kTileRows * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4);
         if (row < r.count)
-          v = *(reinterpret_cast<const uint4*>(static_cast<const __half*>(p.qprep) +
-                                               (qrow0 + (size_t)(row / p.group) * p.Hq + row % p.group) * DK) + ch);
-        *reinterpret_cast<uint4*>(smem + t * C::kQTile + (ch >> 3) * (kTileRows * 128) + rr * 128 +
-                                  (((ch & 7) ^ (rr & 7)) << 4)) = v;
+          cp_async16(dst, static_cast<const __half*>(p.qprep) +
+                              (qrow0 + (size_t)(row / p.group) * p.Hq + row % p.group) * DK + 8 * ch);
+        else
+          *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
       }
+      cp_async_commit();
+      cp_async_wait<0>();
       arrive_first(bars.qfull);
       for (int j = first; j < ns; j += C::KG, page += C::KG) {
         const int nj = n + j, st = nj % kStages;
