@@ -339,7 +339,9 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
       if (seg > 0) wait(bars.qempty, (seg - 1) & 1);
       ++seg;
       constexpr int kChunks = DK / 8;
-      const size_t qrow0 = (size_t)(r.start + r.first) * p.Hq + w.hk * p.group;
+      const unsigned char* q0 = static_cast<const unsigned char*>(p.qprep) +
+                                ((size_t)(r.start + r.first) * p.Hq + w.hk * p.group) * DK * sizeof(__half);
+      const int shift = 31 - __clz(p.group);  // groups are powers of two
       // copied asynchronously: loads that wait for one another's stores took 19000 cycles a segment, registers to hold
       // them spilled
 #pragma unroll 4
@@ -347,11 +349,8 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
         const int here = i / kChunks, ch = i % kChunks;
         const int t = here / kTileRows, rr = here & (kTileRows - 1), row = t * 2 * kTileRows + rank * kTileRows + rr;
         unsigned char* dst = smem + t * C::kQTile + (ch >> 3) * (kTileRows * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4);
-        if (row < r.count)
-          cp_async16(dst, static_cast<const __half*>(p.qprep) +
-                              (qrow0 + (size_t)(row / p.group) * p.Hq + row % p.group) * DK + 8 * ch);
-        else
-          *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
+        if (row < r.count) cp_async16(dst, q0 + (size_t)(((row >> shift) * p.Hq + (row & (p.group - 1))) * (DK * 2) + 16 * ch));
+        else *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
       }
       cp_async_commit();
       cp_async_wait<0>();
