@@ -119,14 +119,13 @@ __device__ __forceinline__ uint4 load16(const unsigned char* at) {
 }
 
 template <bool QJL>
-__device__ __forceinline__ void load_page(PageRegs& r, const SideLayout& L, const unsigned char* tile, int off8, int slot) {
-  const unsigned char* planes = tile + L.off_planes + off8;
+__device__ __forceinline__ void load_page(PageRegs& r, const SideLayout& L, const unsigned char* planes, const unsigned char* norms) {
   r.plane[0] = load8(planes);
   if (L.bits > 1) r.plane[1] = load8(planes + kTile * 16);
   if (L.bits > 2) r.plane[2] = load8(planes + 2 * kTile * 16);
-  if (QJL) r.sketch = load8(tile + L.off_sketch + off8);
-  r.norm = load16(tile + L.off_norm + 2 * slot);
-  if (QJL) r.gamma = load16(tile + L.off_gamma + 2 * slot);
+  if (QJL) r.sketch = load8(planes + (L.off_sketch - L.off_planes));
+  r.norm = load16(norms);
+  if (QJL) r.gamma = load16(norms + (L.off_gamma - L.off_norm));
 }
 
 __device__ __forceinline__ uint32_t half_at(const uint4& v, int i) {  // i-th of 8
@@ -153,55 +152,49 @@ __device__ __forceinline__ void next_rows(uint32_t (&n)[4]) {
   }
 }
 
-template <int BITS, bool ROWS>
-__device__ __forceinline__ void expand_codes(const PageRegs& r, uint2 lut, const uint32_t (&nn)[4], uint32_t d, int step, uint32_t x) {
+// Codes (BITS > 0), signs times ng (SIGNS; `signs` bytes behind the codes' rows, or at d alone), or both in one loop.
+template <int BITS, bool SIGNS, bool ROWS>
+__device__ __forceinline__ void expand(const PageRegs& r, uint2 lut, const uint32_t (&nn)[4], const uint32_t (&ng)[4], uint32_t d,
+                                       int step, uint32_t x, int signs) {
   Codes<BITS> a, b;
-  a.set(r.plane[0].x, r.plane[1].x, r.plane[2].x);
-  b.set(r.plane[0].y, r.plane[1].y, r.plane[2].y);
-  uint32_t n[4] = {nn[0], nn[1], nn[2], nn[3]};
-  uint32_t top = 0x8000u, at = d + (x << 4);  // rows are 128 bytes: x ^ s only turns bits of the chunk within one
+  if (BITS > 0) {
+    a.set(r.plane[0].x, r.plane[1].x, r.plane[2].x);
+    b.set(r.plane[0].y, r.plane[1].y, r.plane[2].y);
+  }
+  const uint32_t za = SIGNS ? sign_word(r.sketch.x) : 0u, zb = SIGNS ? sign_word(r.sketch.y) : 0u;
+  uint32_t n[4] = {nn[0], nn[1], nn[2], nn[3]}, g[4] = {ng[0], ng[1], ng[2], ng[3]};
+  uint32_t top = 0x8000u;
 #pragma unroll 1
-  for (int q = 0; q < 4; ++q) {
+  for (uint32_t s = 0; s < 128; s += 32, d += 2 * step) {  // 16 times the first of two s
+    const uint32_t at = d + ((x << 4) ^ s);                 // rows are 128 bytes: x ^ s only turns bits of the chunk within one
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      uint32_t v[4], m[4];
-      a.next(e, lut.x, lut.y, top >> e, top >> (8 + e), v[0], v[1]);
-      b.next(e, lut.x, lut.y, top >> e, top >> (8 + e), v[2], v[3]);
-      row_factors<ROWS>(n, e, m);
-      sts16((at ^ (e << 4)) + e * step, mul2(v[0], m[0]), mul2(v[1], m[1]), mul2(v[2], m[2]), mul2(v[3], m[3]));
+      const uint32_t to = (at ^ (e << 4)) + e * step, m01 = top >> e, m23 = top >> (8 + e);
+      uint32_t m[4];
+      if (BITS > 0) {
+        uint32_t v[4];
+        a.next(e, lut.x, lut.y, m01, m23, v[0], v[1]);
+        b.next(e, lut.x, lut.y, m01, m23, v[2], v[3]);
+        row_factors<ROWS>(n, e, m);
+        sts16(to, mul2(v[0], m[0]), mul2(v[1], m[1]), mul2(v[2], m[2]), mul2(v[3], m[3]));
+      }
+      if (SIGNS) {
+        row_factors<ROWS>(g, e, m);
+        sts16(to + signs, m[0] ^ (za * m01 & kSigns), m[1] ^ (za * m23 & kSigns), m[2] ^ (zb * m01 & kSigns),
+              m[3] ^ (zb * m23 & kSigns));
+      }
     }
     top >>= 2;
-    at = (at ^ ((q ^ (q + 1)) << 5)) + 2 * step;
-    next_rows<ROWS>(n);
+    if (BITS > 0) next_rows<ROWS>(n);
+    if (SIGNS) next_rows<ROWS>(g);
   }
 }
-template <bool ROWS>
-__device__ __forceinline__ void expand_codes(int bits, const PageRegs& r, uint2 lut, const uint32_t (&nn)[4], uint32_t d, int step,
-                                             uint32_t x) {
-  if (bits == 2) expand_codes<2, ROWS>(r, lut, nn, d, step, x);
-  else if (bits == 3) expand_codes<3, ROWS>(r, lut, nn, d, step, x);
-  else expand_codes<1, ROWS>(r, lut, nn, d, step, x);
-}
-// The same of the sketch's signs: +-ng.
-template <bool ROWS>
-__device__ __forceinline__ void expand_signs(const PageRegs& r, const uint32_t (&ng)[4], uint32_t d, int step, uint32_t x) {
-  const uint32_t za = sign_word(r.sketch.x), zb = sign_word(r.sketch.y);
-  uint32_t g[4] = {ng[0], ng[1], ng[2], ng[3]};
-  uint32_t top = 0x8000u, at = d + (x << 4);
-#pragma unroll 1
-  for (int q = 0; q < 4; ++q) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const uint32_t m01 = top >> e, m23 = top >> (8 + e);
-      uint32_t h[4];
-      row_factors<ROWS>(g, e, h);
-      sts16((at ^ (e << 4)) + e * step, h[0] ^ (za * m01 & kSigns), h[1] ^ (za * m23 & kSigns), h[2] ^ (zb * m01 & kSigns),
-            h[3] ^ (zb * m23 & kSigns));
-    }
-    top >>= 2;
-    at = (at ^ ((q ^ (q + 1)) << 5)) + 2 * step;
-    next_rows<ROWS>(g);
-  }
+template <bool SIGNS, bool ROWS>
+__device__ __forceinline__ void expand_codes(int bits, const PageRegs& r, uint2 lut, const uint32_t (&nn)[4], const uint32_t (&ng)[4],
+                                             uint32_t d, int step, uint32_t x, int signs) {
+  if (bits == 2) expand<2, SIGNS, ROWS>(r, lut, nn, ng, d, step, x, signs);
+  else if (bits == 3) expand<3, SIGNS, ROWS>(r, lut, nn, ng, d, step, x, signs);
+  else expand<1, SIGNS, ROWS>(r, lut, nn, ng, d, step, x, signs);
 }
 
 // Of a warp whose threads have written operand rows: visible to the products, one arrival.
@@ -215,52 +208,69 @@ __device__ __forceinline__ void arrive_rows(uint64_t& bar) {
 // 2 g, 2 g + 1; token order: token th / 2, half a row.
 template <bool KQ>
 struct KeyThread {
+  const unsigned char *planes, *norms;  // of a page's first tile 0
   uint32_t row_off, x;
-  int tile, off8, slot, step, tok;
+  int step, tok;
   bool octet;
   // atom: bytes of an operand's atom of 64 K-elements
   __device__ __forceinline__ void init(const ChunkParams& p, int th, int atom) {
     octet = p.k.order == kOrderOctet;
     const int o = th >> 4, g = th & 15;
     tok = th >> 1;
-    tile = octet ? o >> 2 : tok >> 5;
-    off8 = octet ? (o & 3) * 128 + g * 8 : (tok & 31) * 16 + (th & 1) * 8;
-    slot = octet ? 8 * (o & 3) : tok & 24;
+    const unsigned char* tile = reinterpret_cast<const unsigned char*>(p.kreg) + (octet ? o >> 2 : tok >> 5) * p.k.tile_bytes;
+    planes = tile + p.k.off_planes + (octet ? (o & 3) * 128 + g * 8 : (tok & 31) * 16 + (th & 1) * 8);
+    norms = tile + p.k.off_norm + 2 * (octet ? 8 * (o & 3) : tok & 24);
     row_off = octet ? (g >> 3) * atom + o * 1024 : (th & 1) * atom + tok * 128;
     step = octet ? 128 : 0;
     x = octet ? g & 7 : tok & 7;
   }
   __device__ __forceinline__ void fetch(const ChunkParams& p, PageRegs& r, long ti) const {
-    load_page<KQ>(r, p.k, reinterpret_cast<const unsigned char*>(p.kreg) + (size_t)(ti + tile) * p.k.tile_bytes, off8, slot);
+    load_page<KQ>(r, p.k, planes + ti * p.k.tile_bytes, norms + ti * p.k.tile_bytes);
   }
-  // the page's rows from `base` on: its codes, then (where the caller wants them) its signs
-  __device__ __forceinline__ void codes(const ChunkParams& p, const PageRegs& cur, uint2 lut, uint32_t base) const {
-    uint32_t nn[4] = {cur.norm.x, cur.norm.y, cur.norm.z, cur.norm.w};
+  __device__ __forceinline__ void code_norms(const PageRegs& cur, uint32_t (&nn)[4]) const {
+    nn[0] = cur.norm.x; nn[1] = cur.norm.y; nn[2] = cur.norm.z; nn[3] = cur.norm.w;
     if (!octet) nn[0] = nn[1] = nn[2] = nn[3] = half_at(cur.norm, tok & 7) * 0x10001u;  // one token
-    expand_codes<true>(p.k.bits, cur, lut, nn, base + row_off, step, x);
+  }
+  __device__ __forceinline__ void sign_norms(const PageRegs& cur, uint32_t (&ng)[4]) const {
+    const uint32_t nn[4] = {cur.norm.x, cur.norm.y, cur.norm.z, cur.norm.w};
+    const uint32_t gg[4] = {cur.gamma.x, cur.gamma.y, cur.gamma.z, cur.gamma.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ng[i] = mul2(nn[i], mul2(gg[i], 0x2C002C00u));  // n * (gamma / 16)
+    if (!octet) ng[0] = ng[1] = ng[2] = ng[3] = half_at(make_uint4(ng[0], ng[1], ng[2], ng[3]), tok & 7) * 0x10001u;
+  }
+  // the page's rows from `base` on: its codes, its signs, or both, the signs `signs` bytes behind
+  __device__ __forceinline__ void codes(const ChunkParams& p, const PageRegs& cur, uint2 lut, uint32_t base) const {
+    uint32_t nn[4];
+    code_norms(cur, nn);
+    expand_codes<false, true>(p.k.bits, cur, lut, nn, nn, base + row_off, step, x, 0);
   }
   __device__ __forceinline__ void signs(const PageRegs& cur, uint32_t base) const {
-    const uint32_t nn[4] = {cur.norm.x, cur.norm.y, cur.norm.z, cur.norm.w};
-    uint32_t ng[4] = {cur.gamma.x, cur.gamma.y, cur.gamma.z, cur.gamma.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) ng[i] = mul2(nn[i], mul2(ng[i], 0x2C002C00u));  // n * (gamma / 16)
-    if (!octet) ng[0] = ng[1] = ng[2] = ng[3] = half_at(make_uint4(ng[0], ng[1], ng[2], ng[3]), tok & 7) * 0x10001u;
-    expand_signs<true>(cur, ng, base + row_off, step, x);
+    uint32_t ng[4];
+    sign_norms(cur, ng);
+    expand<0, true, true>(cur, make_uint2(0, 0), ng, ng, base + row_off, step, x, 0);
+  }
+  __device__ __forceinline__ void both(const ChunkParams& p, const PageRegs& cur, uint2 lut, uint32_t base, int signs) const {
+    uint32_t nn[4], ng[4] = {};
+    code_norms(cur, nn);
+    if (KQ) sign_norms(cur, ng);
+    expand_codes<KQ, true>(p.k.bits, cur, lut, nn, ng, base + row_off, step, x, signs);
   }
 };
 
 // One of the threads that dequantise values: rows are dims, dims 8 k .. + 7 in rows 8 row8 .. + 7, of tokens 8 c .. + 7.
 template <bool VQ>
 struct ValueThread {
-  int c, k, row8;
-  __device__ __forceinline__ void init(int chunk, int octet, int rows8) {
+  const unsigned char *planes, *norms;  // of a page's first tile 0
+  int c, row8;
+  __device__ __forceinline__ void init(const ChunkParams& p, int chunk, int k, int rows8) {
     c = chunk;
-    k = octet;
     row8 = rows8;
+    const unsigned char* tile = reinterpret_cast<const unsigned char*>(p.vreg) + (c >> 2) * p.v.tile_bytes;
+    planes = tile + p.v.off_planes + k * kTile + 8 * (c & 3);
+    norms = tile + p.v.off_norm + 2 * 8 * (c & 3);
   }
   __device__ __forceinline__ void fetch(const ChunkParams& p, PageRegs& r, long ti) const {
-    load_page<VQ>(r, p.v, reinterpret_cast<const unsigned char*>(p.vreg) + (size_t)(ti + (c >> 2)) * p.v.tile_bytes,
-                  k * kTile + 8 * (c & 3), 8 * (c & 3));
+    load_page<VQ>(r, p.v, planes + ti * p.v.tile_bytes, norms + ti * p.v.tile_bytes);
   }
   // the page's dims from `base` on (the signs' `signs` bytes behind the codes'); tokens from `limit` on enter as zeros.
   // Returns this thread's 8 tokens whose norms are not finite, a bit each (zeros too).
@@ -286,12 +296,11 @@ struct ValueThread {
         }
       }
     }
-    expand_codes<false>(p.v.bits, cur, lut, nn, base + row8 * 1024, 128, c);
     if (VQ) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) ng[i] = mul2(nn[i], mul2(ng[i], 0x2C002C00u));  // n * (gamma / 16)
-      expand_signs<false>(cur, ng, base + signs + row8 * 1024, 128, c);
     }
+    expand_codes<VQ, false>(p.v.bits, cur, lut, nn, ng, base + row8 * 1024, 128, c, signs);
     return bad;
   }
 };

@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow(const __grid_constan
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsDequant));
     const int all = tid - 32 * kWarpV, second = all >> 7, th = all & 127;
     ValueThread<VQ> values;
-    values.init(th & 7, th >> 3, th >> 3);
+    values.init(p, th & 7, th >> 3, th >> 3);
     const uint2 lut = code_halves(p.v);
     int n = 0;
     PageRegs regs = {};

@@ -364,8 +364,7 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
         }
         if (nj >= kStages) wait(bars.kempty[st], (nj / kStages - 1) & 1);
         const uint32_t base = sm + C::kOffK + st * C::kKStage;
-        keys.codes(p, cur, lut, base);
-        if (KQ) keys.signs(cur, base + 2 * C::kKAtom);
+        keys.both(p, cur, lut, base, 2 * C::kKAtom);
         arrive_first(bars.kfull[st]);
       }
       n += ns;
@@ -373,7 +372,7 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
   } else if (warp < C::kWarpS) {  // ---- dims 64 rank .. + 63 of a page's values
     const int th = (tid - 32 * C::kWarpV) & 63, grp = (tid - 32 * C::kWarpV) >> 6;
     ValueThread<VQ> values;
-    values.init(th & 7, 8 * rank + (th >> 3), th >> 3);
+    values.init(p, th & 7, 8 * rank + (th >> 3), th >> 3);
     const uint2 lut = code_halves(p.v);
     int n = 0, seg = 0;
     PageRegs regs = {};
