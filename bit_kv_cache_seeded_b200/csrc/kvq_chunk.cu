@@ -224,6 +224,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) chunk_prep(const __grid_const
   __shared__ __align__(16) __half s_a[KQ && BF16 ? kPrepRows : 1][kPadH];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rows = p.n_tokens * p.Hq;  // at most 2^30
+  const int shift = 31 - __clz(p.group);  // groups are powers of two
   constexpr int DK = KQ ? 2 * kHeadDim : kHeadDim;
   Frags frags;
   if (KQ && BF16) load_frags(frags, p.St, p.s_exp, warp, lane);
@@ -255,7 +256,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) chunk_prep(const __grid_const
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       float sg[4];
-      load4(sg, p.signs + head / p.group * p.signs_stride, false, lane);
+      load4(sg, p.signs + (head >> shift) * p.signs_stride, false, lane);
       if (++head == p.Hq) head = 0;
 #pragma unroll
       for (int k = 0; k < 4; ++k) rot[v][k] *= sg[k];
@@ -588,6 +589,7 @@ __global__ void __launch_bounds__(kMergeThreads, VQ ? 2 : 3) chunk_merge(const _
   __shared__ __align__(16) float s_z[VQ ? kMergeRows : 1][kPad];   // sketch sums; bf16: their products
   __shared__ __align__(16) __half s_a[VQ && BF16 ? kMergeRows : 1][kPadH];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int shift = 31 - __clz(p.group);
   Frags frags;
   if (VQ && BF16) load_frags(frags, p.S, p.s_exp, warp, lane);
   else if (VQ) warm_l1(p.S);
@@ -719,7 +721,7 @@ __global__ void __launch_bounds__(kMergeThreads, VQ ? 2 : 3) chunk_merge(const _
       const int row = row0 + v;
       if (row >= r.z) continue;
       const float f = l[v] > 0.f ? (BF16 ? kCodeScale : 1.f) / (kHeadDim * l[v]) : l[v];  // 0: nothing attended; or NaN
-      const size_t at = ((size_t)(r.w + r.y + row / p.group) * p.Hq + hk * p.group + row % p.group) * kHeadDim;
+      const size_t at = ((size_t)(r.w + r.y + (row >> shift)) * p.Hq + hk * p.group + (row & (p.group - 1))) * kHeadDim;
 #pragma unroll
       for (int k = 0; k < 4; ++k) acc[v][k] *= f * sg[k];
       if (BF16)
