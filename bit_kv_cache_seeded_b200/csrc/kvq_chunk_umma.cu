@@ -8,9 +8,10 @@
 // with K and V dequantised from the packed page into fp16 (kvq_chunk_dequant.cuh). Each CTA holds 128 rows of a
 // tile and makes half of either operand: keys, 32 of the tokens; values, 64 of the dims. NT row tiles share the
 // operands: two where tensor memory holds their sums (O takes 2 x 128 columns, S 2 x 2 x 64), one with a value
-// sketch (O 256). Measured on a 2048-token chunk of 64 heads over 32768 tokens: MEASURED; a CTA of its own, which
-// dequantises everything for half as many rows, 2.72 ms; pairs with S over 128 tokens, which leaves tensor memory
-// for one S a tile and so puts S, softmax and P V of a tile in a row, 2.79.
+// sketch (O 256). Measured on a 2048-token chunk of 64 heads over 32768 tokens (3 bits, a key sketch): 2.37 ms, 1.3
+// PFLOP/s with the sketch's products. A CTA of its own, which dequantises everything for half as many rows, took
+// 2.72 ms at the same stage of the work; pairs with S over 128 tokens, which leaves tensor memory for one S a tile
+// and so puts S, softmax and P V of a tile in a row, 2.79. The softmax's issue bounds it, and the tensor pipe next.
 //
 // Warps: 4 per row tile for the softmax (thread = row), 4 or 8 that dequantise keys (and fetch the queries of
 // a segment), 4 or 8 for values, and in the first CTA 2 that issue the products, S and P V. K and V are staged
