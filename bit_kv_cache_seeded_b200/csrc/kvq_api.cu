@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "kvq_internal.h"
+#include "kvq_ragged.h"
 #include "kvq_window.cuh"
 #include "kvq_plan.h"
 
@@ -451,7 +452,7 @@ kvq_status cache_init(kvq_cache** out, const kvq_cfg* cfg, int32_t batch, int32_
     c->d_S = reinterpret_cast<float*>(c->dev + P.S_off);
     c->d_St = reinterpret_cast<float*>(c->dev + P.St_off);
     const size_t m = need_sketch ? (size_t)cfg->qjl_dim : 0;
-    c->h_tables.resize(n_signs + 2 * m * kHeadDim);
+    c->h_tables.resize(n_signs + 2 * m * kHeadDim + 1);
     float* hs = c->h_tables.data();
     for (int i = 0; i < n_signs; ++i) hs[i] = (float)rot_signs[i];
     float* hS = hs + n_signs;
@@ -463,7 +464,7 @@ kvq_status cache_init(kvq_cache** out, const kvq_cfg* cfg, int32_t batch, int32_
       }
     float top = 0.f;
     for (size_t i = 0; i < m * kHeadDim; ++i) top = std::max(top, std::fabs(hS[i]));
-    c->s_exp = top > 0.f && std::isfinite(top) ? std::min(std::max(std::ilogb(top) - 9, -126), 118) : 0;
+    c->h_tables.back() = top > 0.f && std::isfinite(top) ? (float)std::min(std::max(std::ilogb(top) - 9, -126), 118) : 0.f;
     // Synchronous copies: the tables are tiny and this keeps the staging buffer's lifetime
     // trivially safe.
     if (cudaMemcpy(c->d_signs, hs, sizeof(float) * n_signs, cudaMemcpyHostToDevice) != cudaSuccess ||
@@ -1174,6 +1175,8 @@ extern "C" kvq_status kvq_decode_attention_static(const kvq_cache* c, const void
 // ---- ragged serving path: block tables, slot maps, appends by slots, chunk attention ----------------
 
 namespace {
+// Exponent of two that brings S's largest entry to [2^9, 2^10), kept behind the staged tables (0 without a sketch).
+int sketch_exp(const kvq_cache* c) { return c->h_tables.empty() ? 0 : (int)c->h_tables.back(); }
 // The cache kinds the ragged path handles: rotated codes, no bf16 window.
 bool ragged_supported(const kvq_cache* c) { return !c->is_fp4 && !has_window(c); }
 bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -1275,7 +1278,7 @@ kvq_status kvq_quantize_slots(kvq_cache* c, const void* K, const void* V, kvq_dt
   p.signs = c->d_signs;
   p.signs_stride = c->signs_stride;
   p.St = c->d_St;
-  p.s_exp = c->s_exp;
+  p.s_exp = sketch_exp(c);
   p.err = c->d_status;
   return launch_quantize_slots(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
@@ -1329,7 +1332,7 @@ kvq_status kvq_chunk_attention(const kvq_cache* c, const void* q, kvq_dtype dtyp
   p.signs_stride = c->signs_stride;
   p.S = c->d_S;
   p.St = c->d_St;
-  p.s_exp = c->s_exp;
+  p.s_exp = sketch_exp(c);
   p.logit_scale = default_scale(c->cfg) * 1.4426950408889634f;
   p.err = c->d_status;
   p.wait_limit = kWaitLimitCycles;

@@ -37,20 +37,6 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t byt
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
-// One arrival on the barrier at the same place in CTA `rank` of the cluster (this CTA's own included), releasing this
-// thread's earlier accesses to the cluster; a wait that takes them over is mbar_wait_cluster.
-__device__ __forceinline__ void mbar_arrive_at(uint32_t bar, uint32_t rank) {
-  asm volatile(
-      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, %1;\n"
-      " mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}\n" ::"r"(bar), "r"(rank) : "memory");
-}
-// The same without ordering memory at cluster scope, which costs several hundred cycles: for tensor memory, whose
-// accesses tcgen05's own waits and fences order.
-__device__ __forceinline__ void mbar_arrive_at_tmem(uint32_t bar, uint32_t rank) {
-  asm volatile(
-      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, %1;\n mbarrier.arrive.shared::cluster.b64 _, [a];\n}\n"
-      ::"r"(bar), "r"(rank) : "memory");
-}
 // Orders this thread's earlier generic-proxy shared-memory accesses (after a barrier, those of
 // the whole CTA) before later bulk copies into the same buffer.
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
@@ -94,27 +80,6 @@ __device__ __forceinline__ bool mbar_wait_spin(uint32_t bar, uint32_t parity, lo
     if (done) return true;
     if (clock64() - t0 > limit) return false;
   }
-}
-
-// mbar_wait_spin for arrivals from other CTAs of the cluster.
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, long long limit) {
-  const long long t0 = clock64();
-  while (true) {
-    uint32_t done;
-    asm volatile(
-        "{\n .reg .pred q;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 q, [%1], %2;\n selp.u32 %0, 1, 0, q;\n}\n"
-        : "=r"(done) : "r"(bar), "r"(parity) : "memory");
-    if (done) return true;
-    if (clock64() - t0 > limit) return false;
-  }
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
 
 // The same wait polling with the non-blocking test (and a short sleep between tests), for warps

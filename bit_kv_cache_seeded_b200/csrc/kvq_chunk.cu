@@ -16,9 +16,9 @@
 
 #include "kvq_async.cuh"
 #include "kvq_chunk.cuh"
-#include "kvq_internal.h"
 #include "kvq_lm_common.cuh"
 #include "kvq_quantize_lm.cuh"
+#include "kvq_ragged.h"
 
 namespace kvq {
 namespace {

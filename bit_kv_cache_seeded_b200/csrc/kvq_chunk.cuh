@@ -16,7 +16,7 @@
 // folds the value sketch and rotates back.
 #pragma once
 
-#include "kvq_internal.h"
+#include "kvq_ragged.h"
 #include "kvq_tiles.cuh"
 
 namespace kvq {

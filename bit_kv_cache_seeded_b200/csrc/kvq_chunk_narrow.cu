@@ -13,9 +13,8 @@
 // and signs are handed over apart: the products with the codes run while the signs are made, and free the codes'
 // half for the next step. 16 requests of 4-32 rows over 7000 tokens, 8 kv-heads, 2 bits and sketches: 116 us, 0.83
 // TB/s of packed pages; the wide kernel takes 223.
-#include "kvq_async.cuh"
 #include "kvq_chunk_dequant.cuh"
-#include "kvq_tcgen05.cuh"
+#include "kvq_pair.cuh"
 
 namespace kvq {
 namespace {

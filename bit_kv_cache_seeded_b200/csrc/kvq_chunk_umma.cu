@@ -24,9 +24,8 @@
 //
 // Softmax weights are p = 2^(x - m + 7), m the row's maximum but for steps under 2^8, by which it may lag
 // before O is rescaled: p stays under 2^15 in fp16, and a weight is dropped only below 2^-31 of the largest.
-#include "kvq_async.cuh"
 #include "kvq_chunk_dequant.cuh"
-#include "kvq_tcgen05.cuh"
+#include "kvq_pair.cuh"
 
 namespace kvq {
 namespace {

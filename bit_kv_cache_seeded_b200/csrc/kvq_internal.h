@@ -160,85 +160,6 @@ struct MlaParams {
   long long wait_limit;   // SM clock cycles a kernel waits before giving up
 };
 
-// Lengths of up to kMaxSeqPerLaunch sequences, passed by value.
-struct LengthParams {
-  int* lens;
-  int first, n;
-  int value[kMaxSeqPerLaunch];
-};
-
-// Append of a token-major batch [n_tokens][heads][d] into page slots (kvq_slots.cu).
-struct SlotQuantizeParams {
-  const void* src[2];       // K, V
-  int bf16;
-  int n_tokens, heads;
-  const long long* slots;   // 64 * page + token of the page; negative: not written
-  char* region[2];
-  int n_pages;
-  SideLayout side[2];
-  const float* signs;
-  int signs_stride;
-  const float* St;
-  int s_exp;                // S / 2^s_exp is within fp16's range
-  int* err;
-};
-
-// Chunk attention (kvq_chunk.cu): the workspace is laid out by chunk_layout(). The requests of one set are those
-// whose query rows of a kv-head lie within its bounds; each set has its own plan, segment kernel and states.
-struct ChunkSet {
-  int above, upto;          // rows of a request: above < rows <= upto
-  int rows;                 // query rows of a row tile
-  int unit;                 // tokens of a unit
-  int ctas;                 // CTAs (wide set: pairs of them) that share the units
-  int max_tiles;            // row tiles of one kv-head the workspace holds
-  long long* unit_start;    // [max_tiles + 1]
-  int4* tile_rows;          // [max_tiles][2]: the row tiles (chunk::Rows)
-  int* tile_start;          // [B + 1]
-  long long* head;          // row tiles of a kv-head, units of a kv-head
-  float* part;              // softmax states of the segments
-};
-constexpr int kWide = 0, kNarrow = 1;  // sets (fp32 calls have the first alone)
-
-struct ChunkParams {
-  const void* q;            // [n_tokens, Hq, d]
-  void* out;                // the same, in q's type
-  int bf16;
-  int n_tokens, B, Hq, Hkv, group;
-  const int* seq_start;     // [B + 1]
-  const int* ctx_lens;      // [B]
-  int capacity;             // tokens a sequence can hold
-  const char* kreg;
-  const char* vreg;
-  int tiles_per_seq;
-  const int* table;
-  int pages_per_seq, n_pages;
-  SideLayout k, v;
-  const float* signs;
-  int signs_stride;
-  const float* S;
-  const float* St;
-  int s_exp;                // S / 2^s_exp is within fp16's range
-  float logit_scale;        // softmax_scale * log2(e)
-  int* err;
-  long long wait_limit;
-  int sms;
-  // workspace
-  int sets;
-  ChunkSet set[2];
-  void* qprep;              // rotated (and sketched) queries
-  float* qscale;            // [n_tokens * Hq] (bf16)
-};
-
-// A chunk call's workspace: its sets with byte offsets in place of the pointers.
-struct ChunkLayout {
-  struct Set {
-    int above, upto, rows, unit, ctas, max_tiles;
-    size_t unit_start, tile_rows, tile_start, head, part;
-  } set[2];
-  int sets;
-  size_t qprep, qscale, total;
-};
-
 // Reads cudaGetLastError() right after a kernel launch and, when it is cudaSuccess, adds one to
 // the library's launch counter (kvq_kernel_launches).
 cudaError_t launched();
@@ -291,16 +212,6 @@ cudaError_t launch_decode_kivi(const DecodeParams& p, cudaStream_t s);
 cudaError_t launch_window_decode(const DecodeParams& p, cudaStream_t s);
 cudaError_t launch_combine_partials(const float* parts, int n_parts, int rows, int dv, float* out, cudaStream_t s);
 cudaError_t launch_decode_mla_umma(const MlaParams& p, cudaStream_t s);
-cudaError_t launch_extend_block_table(const int* held, const int* n_new, int batch, const int* free_pages, int n_free,
-                                      const int* cursor, int* table, int pages_per_seq, int* seq_start, int* ctx_lens,
-                                      int* taken, cudaStream_t s);
-cudaError_t launch_slot_map(const int* held, const int* seq_start, const int* ctx_lens, int batch, const int* table,
-                            int pages_per_seq, int n_pages, int n_tokens, int* seq_ids, int* positions, long long* slots,
-                            cudaStream_t s);
-cudaError_t launch_set_lengths(const LengthParams& p, cudaStream_t s);
-cudaError_t launch_quantize_slots(const SlotQuantizeParams& p, cudaStream_t s);
-ChunkLayout chunk_layout(int n_tokens, int batch, int Hq, int Hkv, bool k_qjl, bool v_qjl, bool bf16, int sms);
-cudaError_t launch_chunk_attention(const ChunkParams& p, cudaStream_t s);
 cudaError_t launch_decode_mla_mma(const MlaParams& p, cudaStream_t s);
 
 // Host Lloyd-Max tables (lloyd_max.cpp): fp64 fixed-point iteration rounded to fp32.
@@ -334,7 +245,6 @@ struct kvq_cache {
   float* d_signs = nullptr;
   float* d_S = nullptr;
   float* d_St = nullptr;
-  int s_exp = 0;            // power of two that brings S's largest entry to [2^9, 2^10)
   char* d_k = nullptr;
   char* d_v = nullptr;
   size_t k_region = 0, v_region = 0;

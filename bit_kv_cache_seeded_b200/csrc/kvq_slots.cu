@@ -27,8 +27,8 @@
 
 #include <cuda_fp16.h>
 
-#include "kvq_internal.h"
 #include "kvq_quantize_lm.cuh"
+#include "kvq_ragged.h"
 #include "kvq_tiles.cuh"
 
 namespace kvq {
