@@ -150,6 +150,7 @@ __device__ __forceinline__ void warm_l1(const float* m) {
 __device__ void plan(const ChunkParams& p, const ChunkSet& s) {
   __shared__ long long s_warp[kPrepThreads / 32];
   __shared__ long long s_run;
+  __shared__ int s_most;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = s.rows / p.group;
   auto scan = [&](long long v) {  // exclusive prefix of v over the block, carried in s_run
@@ -168,18 +169,24 @@ __device__ void plan(const ChunkParams& p, const ChunkSet& s) {
     __syncthreads();
     return before + x - v;
   };
-  if (tid == 0) s_run = 0;
+  if (tid == 0) {
+    s_run = 0;
+    s_most = 0;
+  }
   __syncthreads();
+  int most = 0;  // tokens of the fullest tile
   for (int b0 = 0; b0 < p.B; b0 += kPrepThreads) {
     const int b = b0 + tid;
     int n = 0;
     if (b < p.B) n = max(clamp_start(p, b + 1) - clamp_start(p, b), 0);
     if (n * p.group <= s.above || n * p.group > s.upto) n = 0;
+    most = max(most, min(n, per));
     const long long at = scan((n + per - 1) / per);
     // max_tiles holds every tile of a seq_start that does not decrease; another one is cut there
     if (b < p.B) s.tile_start[b] = (int)min(at, (long long)s.max_tiles);
   }
   const int tiles = (int)min(s_run, (long long)s.max_tiles);
+  if (most > 0) atomicMax(&s_most, most);
   __syncthreads();
   if (tid == 0) {
     s.tile_start[p.B] = tiles;
@@ -207,6 +214,7 @@ __device__ void plan(const ChunkParams& p, const ChunkSet& s) {
     s.unit_start[tiles] = s_run;
     s.head[0] = tiles;
     s.head[1] = s_run;
+    s.head[2] = (long long)s_most * p.group;
   }
 }
 
@@ -607,7 +615,8 @@ __global__ void __launch_bounds__(kMergeThreads, VQ ? 2 : 3) chunk_merge(const _
     const long long units = set.head[1], T = units * p.Hkv, G = cta_count(set, T);
     const int item = group / per;
     const int hk = item / tiles, tile = item % tiles;
-    const int group0 = group % per * kMergeRows, row0 = group0 + 4 * warp;
+    // rotated, so that a block (a number of blocks that `per` may divide) meets full and empty groups in turn
+    const int group0 = (group + item) % per * kMergeRows, row0 = group0 + 4 * warp;
     const int4 r = set.tile_rows[2 * tile];  // request, first token in it, rows, the request's first token
     const long long u0 = set.unit_start[tile], u1 = set.unit_start[tile + 1];
     if (group0 >= r.z) continue;
@@ -774,7 +783,7 @@ ChunkLayout chunk_layout(int n_tokens, int batch, int Hq, int Hkv, bool k_qjl, b
   for (int i = 0; i < L.sets; ++i) {
     ChunkLayout::Set& s = L.set[i];
     // up to kNarrowRows rows of a kv-head: the narrow kernel (bf16). A call with 16 requests of 7000 tokens, 2 bits and
-    // sketches: narrow 125 / wide 232 us at 4 rows, 129 / 236 at 32; at 48 the wide kernel's 242
+    // sketches: narrow 129 / wide 232 us at 4 rows, 134 / 236 at 32, 157 / 242 at 48 and 160 at 64, its widest tile
     s.above = bf16 && i == kWide ? kNarrowRows : 0;
     s.upto = i == kNarrow ? kNarrowRows : 0x7fffffff;
     s.rows = i == kNarrow ? kNarrowRows : bf16 ? chunk_umma_rows(v_qjl) : kF32Rows;
@@ -784,7 +793,7 @@ ChunkLayout chunk_layout(int n_tokens, int batch, int Hq, int Hkv, bool k_qjl, b
     s.max_tiles = std::min(batch, n_tokens / (s.above / group + 1));
     if (i == kWide) s.max_tiles += n_tokens / (s.rows / group);
     if (n_tokens * (long long)group <= s.above) s.max_tiles = 0;
-    s.head = take(2 * sizeof(long long));
+    s.head = take(3 * sizeof(long long));
     s.unit_start = take(sizeof(long long) * ((size_t)s.max_tiles + 1));
     s.tile_rows = take(2 * sizeof(int4) * (size_t)s.max_tiles);
     s.tile_start = take(sizeof(int) * ((size_t)batch + 1));

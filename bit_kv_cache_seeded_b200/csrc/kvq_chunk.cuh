@@ -159,7 +159,7 @@ inline cudaError_t launch_after(void (*kernel)(ChunkParams), const ChunkParams& 
 // kvq_chunk_narrow.cu for the narrow one.
 int chunk_umma_rows(bool v_qjl);
 cudaError_t launch_chunk_umma(const ChunkParams& p, cudaStream_t s);
-constexpr int kNarrowRows = 32;
+constexpr int kNarrowRows = 64;
 cudaError_t launch_chunk_narrow(const ChunkParams& p, cudaStream_t s);
 
 }  // namespace kvq

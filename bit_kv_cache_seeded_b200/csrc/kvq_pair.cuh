@@ -62,6 +62,19 @@ __device__ __forceinline__ void umma_f16_x4(uint32_t d_tmem, uint64_t a_desc, ui
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n}\n"
       ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(AS / 16), "n"(BS / 16) : "memory");
 }
+// The same with one A of 16 K-elements in tensor memory (two a column) for all four steps.
+template <int BS>
+__device__ __forceinline__ void umma_f16_ta_x4(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, t, e;\n .reg .b64 b1, b2, b3;\n"
+      " elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, 0, 0;\n"
+      " add.s64 b1, %2, %5;\n add.s64 b2, b1, %5;\n add.s64 b3, b2, %5;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b1, %3, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b2, %3, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b3, %3, t;\n}\n"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(BS / 16) : "memory");
+}
 // umma_f16_x4 for a pair of CTAs (cta_group::2), issued in the pair's first: each holds half of A's rows and of D's, and
 // half of B's, at the same addresses. pair_f16_ta_x4: A in tensor memory, two elements per column.
 __device__ __forceinline__ void pair_f16_x4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {

@@ -39,7 +39,7 @@ struct ChunkSet {
   long long* unit_start;    // [max_tiles + 1]
   int4* tile_rows;          // [max_tiles][2]: the row tiles (chunk::Rows)
   int* tile_start;          // [B + 1]
-  long long* head;          // row tiles of a kv-head, units of a kv-head
+  long long* head;          // row tiles of a kv-head, their units, rows of the fullest one
   float* part;              // softmax states of the segments
 };
 constexpr int kWide = 0, kNarrow = 1;  // sets (fp32 calls have the first alone)

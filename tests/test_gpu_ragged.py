@@ -475,6 +475,42 @@ def test_maxima_that_grow_along_the_context(name, new, dtype):
     x.cache.close()
 
 
+@pytest.mark.parametrize("name,group", [("2q2q", 4), ("3q3", 8), ("22", 1), ("23q", 2)])
+@pytest.mark.parametrize("rows", [40, 48, 56, 64, 72])
+def test_narrow_tiles_of_more_than_32_rows(rows, name, group):
+    """Tiles of 33 to 64 rows in one call with smaller ones, over contexts that end in the first or the second page of a
+    step and that several CTAs share; 72 rows go to the wide kernel, the rest of the call stays."""
+    x = Batch(make_cfg(2 * group, 2, *MODES[name]), [77, 300, 1500, 2, 0],
+              [rows // group, 1, 40 // group, 32 // group, 48 // group], seed=rows)
+    out = x.cache.chunk_attention(x.q, x.seq_start, x.ctx_lens)
+    assert kvq.kvq_cache_status(x.cache.handle) == 0
+    assert_close(out, x.reference(), BF16)
+    assert torch.equal(x.cache.chunk_attention(x.q, x.seq_start, x.ctx_lens), out)
+    x.cache.close()
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("where", ["k", "v"])
+@pytest.mark.parametrize("bad", [3, 12])
+def test_a_token_that_is_not_finite_in_a_tile_of_64_rows(bad, where, value):
+    """Rows of either half of the tile before the token, behind it, and another request's: only those behind change."""
+    cfg = make_cfg(4, 1, 2, True, 2, True)
+    kv = {n: torch.randn(16 + 3, 1, 128, device="cuda").to(BF16) for n in "kv"}
+    kv[where][bad, 0, 3] = value
+    x = Batch(cfg, [120, 30], [16, 3], seed=23, **kv)
+    out, ref = x.cache.chunk_attention(x.q, x.seq_start, x.ctx_lens), x.reference()
+    assert_close(out[:bad], ref[:bad], BF16)
+    assert_close(out[16:], ref[16:], BF16)
+    if where == "v" or value != value:
+        assert out[bad:16].isnan().all(-1).all()
+    x.cache.close()
+
+
+@pytest.mark.parametrize("name", ["2q2q", "33"])
+def test_maxima_that_grow_in_a_tile_of_64_rows(name):
+    test_maxima_that_grow_along_the_context(name, 13, BF16)
+
+
 def test_long_context_of_one_token():
     """A single token over a context that every CTA of the narrow kernel shares."""
     x = Batch(make_cfg(4, 1, 2, True, 2, True), [40000], [1], seed=22)
