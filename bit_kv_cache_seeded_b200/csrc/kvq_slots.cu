@@ -151,8 +151,10 @@ __global__ void __launch_bounds__(kSlotThreads)
 slot_map(const int* __restrict__ held, const int* __restrict__ seq_start, const int* __restrict__ ctx_lens, int batch,
          const int* __restrict__ table, int pages_per_seq, int n_pages, int n_tokens, int* __restrict__ seq_ids,
          int* __restrict__ positions, long long* __restrict__ slots) {
-  const int t = blockIdx.x * kSlotThreads + threadIdx.x;
-  if (t >= n_tokens || t >= seq_start[batch]) return;  // rows behind the last request stay as they are
+  const unsigned at = blockIdx.x * kSlotThreads + threadIdx.x;
+  if (at >= (unsigned)n_tokens) return;
+  const int t = (int)at;
+  if (t < seq_start[0] || t >= seq_start[batch]) return;  // rows of no request stay as they are
   int lo = 0, hi = batch;  // the last b with seq_start[b] <= t
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -427,7 +429,7 @@ cudaError_t launch_extend_block_table(const int* held, const int* n_new, int bat
 cudaError_t launch_slot_map(const int* held, const int* seq_start, const int* ctx_lens, int batch, const int* table,
                             int pages_per_seq, int n_pages, int n_tokens, int* seq_ids, int* positions, long long* slots,
                             cudaStream_t s) {
-  slot_map<<<(n_tokens + kSlotThreads - 1) / kSlotThreads, kSlotThreads, 0, s>>>(
+  slot_map<<<(unsigned)((n_tokens + (long long)kSlotThreads - 1) / kSlotThreads), kSlotThreads, 0, s>>>(
       held, seq_start, ctx_lens, batch, table, pages_per_seq, n_pages, n_tokens, seq_ids, positions, slots);
   return launched();
 }

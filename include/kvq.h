@@ -240,12 +240,12 @@ kvq_status kvq_extend_block_table(const int32_t* held, const int32_t* n_new, int
                                   int32_t n_free, const int32_t* cursor, int32_t* block_table, int32_t pages_per_seq,
                                   int32_t* seq_start, int32_t* ctx_lens, int32_t* taken, void* stream);
 
-/* For every new token t < min(n_tokens, seq_start[batch]), in request b: seq_ids[t] = b, positions[t] =
+/* For every new token t, seq_start[0] <= t < min(n_tokens, seq_start[batch]), in request b: seq_ids[t] = b, positions[t] =
  * held[b] + t - seq_start[b] and slots[t] = 64 page + positions[t] % 64, page = block_table[b][position
  * / 64]; the slot is -1 when the request was refused (ctx_lens[b] is not held[b] + its new tokens), or
  * when the entry is not a page of a pool of n_pages, or the position is outside the table. seq_ids and
- * positions (int32 [n_tokens]) may be NULL. Rows from seq_start[batch] on are left as they are. seq_start
- * must not decrease. Outputs as above; n_tokens == 0 is a no-op. */
+ * positions (int32 [n_tokens]) may be NULL. Rows before seq_start[0] and from seq_start[batch] on are left as they
+ * are. seq_start must not decrease. Outputs as above; n_tokens == 0 is a no-op. */
 kvq_status kvq_slot_map(const int32_t* held, const int32_t* seq_start, const int32_t* ctx_lens, int32_t batch,
                         const int32_t* block_table, int32_t pages_per_seq, int32_t n_pages, int32_t n_tokens,
                         int32_t* seq_ids, int32_t* positions, int64_t* slots, void* stream);

@@ -74,6 +74,18 @@ def test_tables_and_slots_of_many_requests(batch):
     check_tables(held, new, 8, rng.permutation(need + 9).astype(np.int32), 4)
 
 
+def test_rows_before_the_first_request_get_no_slot():
+    """seq_start need not begin at 0: rows before it belong to no request, and an append must not see a slot there."""
+    held, start, ctx = cuda_ints([70, 3]), cuda_ints([5, 7, 10]), cuda_ints([72, 6])
+    table = cuda_ints([[4, 1], [0, 3]])
+    outs = [cuda_ints(np.full(12, 55), t) for t in (torch.int32, torch.int32, torch.int64)]
+    kvq.kvq_slot_map(held, start, ctx, table, 6, *outs)
+    ids, pos, slots = (o.tolist() for o in outs)
+    assert ids == [55] * 5 + [0, 0, 1, 1, 1] + [55] * 2
+    assert pos == [55] * 5 + [70, 71, 3, 4, 5] + [55] * 2
+    assert slots == [55] * 5 + [64 + 6, 64 + 7, 3, 4, 5] + [55] * 2
+
+
 # ---- appends by slots
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
