@@ -123,6 +123,14 @@ __device__ __forceinline__ float* segment_ml(const ChunkSet& s, long long item, 
 __device__ __forceinline__ float* segment_o(const ChunkSet& s, long long item, int cta, int dv) {
   return segment_ml(s, item, cta, dv) + 2 * s.rows;
 }
+// Where a row's value dim lies in o: [dim / 16][row][dim % 16], since the wide kernel's lanes hold a row each and write
+// whole sectors of neighbouring rows so, while the merge still reads 64 bytes at once. Mixed batch, wide kernel and
+// merge: rows of all dims, 16 bytes a store, 222 and 53 us; 32 bytes a store in blocks of 32 dims 210 and 58, of 16
+// 192 and 56, of 8 187 and 61.
+constexpr int kStateDims = 16;
+__device__ __forceinline__ int state_pos(int rows, int row, int dim) {
+  return (dim / kStateDims * rows + row) * kStateDims + dim % kStateDims;
+}
 
 // Where the tensor-core kernels keep coordinate 4 lane + k of a query (or of its sketch), so that the keys' order
 // in a tile need not change (kvq_chunk_dequant.cuh): the place of k = 0; k is k further in octet order, 8 k in token order.

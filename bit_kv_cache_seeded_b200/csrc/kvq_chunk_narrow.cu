@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow(const __grid_constan
           wait(bars.pvdone[(n - 1) & 1], ((n - 1) >> 1) & 1);
           tc::fence_after();
         }
-        float* so = segment_o(set, walk.w.item, blockIdx.x, DV) + (size_t)c0 * DV + tok;
+        float* so = segment_o(set, walk.w.item, blockIdx.x, DV);
         float l = 0.f;
 #pragma unroll 1
         for (int i = 0; i < (C::kSums + 1) * (kPart / 8); ++i) {
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow(const __grid_constan
           for (int c = 0; c < 8; ++c) {
             const float x = ns > 0 ? __uint_as_float(o[c]) : 0.f;
             if (block == C::kSums) l = row0 + c == lane ? x : l;
-            else if (row0 + c < count) so[(size_t)(row0 + c) * DV + block * 128] = x;
+            else if (row0 + c < count) so[state_pos(kNarrowRows, c0 + row0 + c, block * 128 + tok)] = x;
           }
         }
         if (quarter == 0 && lane < count) {

@@ -130,6 +130,12 @@ __device__ __forceinline__ void fewer_registers() {
   if (SHARE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(REGS));
 }
 
+// 32 bytes, a whole sector, at once.
+__device__ __forceinline__ void store8(float* at, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]) : "memory");
+}
+
 template <bool KQ, bool VQ>
 __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __grid_constant__ ChunkParams p) {
   using C = Cfg<KQ, VQ>;
@@ -299,7 +305,7 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
         if (m == -INFINITY && l == l) l = 0.f;  // ex2_fma leaves 2^-126 of a masked position
         if (ns > 0 && *(volatile int*)&bars.bad[seg % kSlots] <= last && row < r.count) l = NAN;
         float* ml = segment_ml(set, w.item, pair, DV) + 2 * row;
-        float* so = segment_o(set, w.item, pair, DV) + (size_t)row * DV;
+        float* so = segment_o(set, w.item, pair, DV);
         if (row < r.count) *reinterpret_cast<float2*>(ml) = make_float2(m == -INFINITY ? m : ref, l);
 #pragma unroll 1
         for (int c = 0; c < DV; c += 16) {
@@ -310,11 +316,13 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
           }
           // with a sketch each CTA's half of the columns is 64 codes, 64 signs
           const int dim = VQ ? (c & 63) + (c & 128) / 2 + (c & 64) * 2 : c;
-          if (row < r.count)
+          if (row < r.count) {
+            float* to = so + state_pos(set.rows, row, dim);
 #pragma unroll
-            for (int i = 0; i < 16; i += 4)
-              *reinterpret_cast<uint4*>(so + dim + i) =
-                  used ? make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]) : make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < 16; ++i) o[i] = used ? o[i] : 0u;
+            store8(to, o);
+            store8(to + 8, o + 8);
+          }
         }
       }
       seg += ns > 0;
