@@ -21,12 +21,13 @@
 // The product decides signs, so it has to be as good as fp32: residuals and S are each two fp16 numbers, the
 // second 2^11 times what the first leaves (22 bits together), and the three products that matter are summed in
 // fp32, the small ones apart. On the CUDA cores it took half of the instructions, and the packing on one warp a
-// plane a quarter (2200 tokens of 8 heads, 3 bits, a sketch on the keys: 52.3 us; 39.4 now, bound by
+// plane a quarter (2200 tokens of 8 heads, 3 bits, a sketch on the keys: 52.3 us; 35 now, bound by
 // issue). Small calls take TOK = 8, which spreads them over four times as many blocks as TOK = 32 (launch).
 #include <algorithm>
 
 #include <cuda_fp16.h>
 
+#include "kvq_async.cuh"
 #include "kvq_quantize_lm.cuh"
 #include "kvq_ragged.h"
 #include "kvq_tiles.cuh"
@@ -185,10 +186,10 @@ constexpr int kAppThreads = kAppWarps * 32;
 constexpr int kPadH = kHeadDim + 8;  // row stride of a half row: the 8 rows that ldmatrix reads lie in distinct banks
 constexpr float kSecond = 2048.f;
 
-template <int TOK>
+template <int TOK, bool QJL>
 struct AppSmem {
   static constexpr int kRows = TOK < 16 ? 16 : TOK;  // a matrix tile has 16; those past TOK are not looked at
-  __half rho[2][kRows][kPadH];
+  __half rho[2][QJL ? kRows : 1][kPadH];
   uint32_t planes[TOK][kMaxBits + 1][4];  // code planes, then the sign words
   float n[TOK], gamma[TOK];
   long long slot[TOK];  // -1: not written
@@ -207,18 +208,26 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], con
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
-template <int TOK>
-__global__ void __launch_bounds__(kAppThreads, 2) quantize_slots(const __grid_constant__ SlotQuantizeParams p) {
-  __shared__ __align__(16) AppSmem<TOK> sm;
-  const int side = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// Blocks an SM holds: a sketch's fragments of S take 64 registers a thread.
+template <bool QJL>
+constexpr int kAppBlocks = QJL ? 2 : 4;
+
+// QJL: the side has a sketch, or may have one. other: the call's other side is launched behind this one, to begin as soon
+// as it finds room.
+template <int TOK, bool QJL>
+__global__ void __launch_bounds__(kAppThreads, kAppBlocks<QJL>)
+quantize_slots(const __grid_constant__ SlotQuantizeParams p, int first_side, bool other) {
+  __shared__ __align__(16) AppSmem<TOK, QJL> sm;
+  if (other) grid_dep_launch();
+  const int side = first_side + blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const SideLayout& L = p.side[side];
   const int nthr = (1 << L.bits) - 1;
   const int chunks = (p.n_tokens + TOK - 1) / TOK;
   const long long total = (long long)chunks * p.heads;
-  if (blockIdx.x >= total) return;
   // this warp's rows 16 warp .. + 15 of S (columns of S^T), divided by 2^s_exp
   uint32_t frag[2][2][8][2];
-  if (L.qjl) {
+  const bool qjl = QJL && L.qjl;
+  if (qjl) {
     const float mul = exp2f((float)-p.s_exp);
 #pragma unroll
     for (int n = 0; n < 2; ++n)
@@ -272,31 +281,29 @@ __global__ void __launch_bounds__(kAppThreads, 2) quantize_slots(const __grid_co
         u[0] = a0 + a2; u[2] = a0 - a2; u[1] = a1 + a3; u[3] = a1 - a3;
 #pragma unroll
         for (int q = 0; q < 4; ++q) u[q] = (n > 0.f) ? u[q] / n : 0.f;
-        int code[4];
+        // the number of thresholds (ascending, infinite where the side has fewer) not above u, bit by bit: what a bit
+        // decides is a plane's vote (counted one by one, and the votes taken from the count, 38.8 us in place of 36.3)
+        uint32_t plane[kMaxBits];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          int c = 0;
+          const bool b2 = u[q] >= thr[3];
+          const bool b1 = u[q] >= (b2 ? thr[5] : thr[1]);
+          const bool b0 = u[q] >= (b2 ? (b1 ? thr[6] : thr[4]) : (b1 ? thr[2] : thr[0]));
+          const uint32_t w[kMaxBits] = {__ballot_sync(0xffffffffu, b0), __ballot_sync(0xffffffffu, b1), __ballot_sync(0xffffffffu, b2)};
 #pragma unroll
-          for (int j = 0; j < 7; ++j) c += (u[q] >= thr[j]) ? 1 : 0;
-          code[q] = c;
-          rho[q] = u[q] - __shfl_sync(0xffffffffu, cent_lane, c);
+          for (int pp = 0; pp < kMaxBits; ++pp) plane[pp] = q == 0 || lane == q ? w[pp] : plane[pp];
+          rho[q] = u[q] - __shfl_sync(0xffffffffu, cent_lane, (b2 ? 4 : 0) + (b1 ? 2 : 0) + (b0 ? 1 : 0));
         }
+        if (lane < 4)
 #pragma unroll
-        for (int pp = 0; pp < kMaxBits; ++pp)
-          if (pp < L.bits) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t w = __ballot_sync(0xffffffffu, (code[q] >> pp) & 1);
-              if (lane == q) sm.planes[i][pp][q] = w;
-            }
-          }
+          for (int pp = 0; pp < kMaxBits; ++pp) sm.planes[i][pp][lane] = plane[pp];
         if (lane == 0) sm.n[i] = n;
-        if (L.qjl) {
+        if (qjl) {
           const float gam = sqrtf(qlm::warp_sum(rho[0] * rho[0] + rho[1] * rho[1] + rho[2] * rho[2] + rho[3] * rho[3]));
           if (lane == 0) sm.gamma[i] = gam;
         }
       }
-      if (L.qjl)
+      if (qjl)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           sm.rho[0][i][32 * q + lane] = first_half(rho[q]);
@@ -305,9 +312,9 @@ __global__ void __launch_bounds__(kAppThreads, 2) quantize_slots(const __grid_co
     }
     __syncthreads();
 
-    if (L.qjl) {
+    if (qjl) {
 #pragma unroll 1
-      for (int m = 0; m < AppSmem<TOK>::kRows / 16; ++m) {
+      for (int m = 0; m < AppSmem<TOK, QJL>::kRows / 16; ++m) {
         float big[2][4] = {}, small[2][4] = {};
         const uint32_t a0 = (uint32_t)__cvta_generic_to_shared(&sm.rho[0][16 * m + (lane & 15)][8 * (lane >> 4)]);
 #pragma unroll
@@ -343,7 +350,7 @@ __global__ void __launch_bounds__(kAppThreads, 2) quantize_slots(const __grid_co
       __syncthreads();
     }
 
-    const int nplanes = L.bits + (L.qjl ? 1 : 0);
+    const int nplanes = L.bits + (qjl ? 1 : 0);
     auto tile_base = [&](long long slot) {
       return p.region[side] + (size_t)((slot / kPage * p.heads + h) * 2 + (slot % kPage) / kTile) * L.tile_bytes;
     };
@@ -402,18 +409,30 @@ __global__ void __launch_bounds__(kAppThreads, 2) quantize_slots(const __grid_co
       if (slot < 0) continue;
       char* tb = tile_base(slot) + (slot % kTile) * 2;
       if (i < TOK) *reinterpret_cast<__half*>(tb + L.off_norm) = __float2half_rn(sm.n[tok]);
-      else if (L.qjl) *reinterpret_cast<__half*>(tb + L.off_gamma) = __float2half_rn(sm.gamma[tok]);
+      else if (qjl) *reinterpret_cast<__half*>(tb + L.off_gamma) = __float2half_rn(sm.gamma[tok]);
     }
     __syncthreads();  // the next tokens reuse the shared buffers
   }
+  grid_dep_wait();  // the call's other launch is done when this one is
 }
 
-template <int TOK>
-cudaError_t launch_slots(const SlotQuantizeParams& p, cudaStream_t s) {
+// `sides` sides from `first` on; other: the other side follows; after: it came before.
+template <int TOK, bool QJL>
+cudaError_t launch_slots(const SlotQuantizeParams& p, int first, int sides, bool other, bool after, cudaStream_t s) {
   const long long blocks = (long long)((p.n_tokens + TOK - 1) / TOK) * p.heads;
-  // two blocks fit an SM: as many of a side, which keep their fragments of S from one group to the next
-  quantize_slots<TOK><<<dim3((unsigned)std::min<long long>(blocks, 148 * 2), 2), kAppThreads, 0, s>>>(p);
-  return launched();
+  cudaLaunchConfig_t config = {};
+  // as many blocks as fit, of a side: they keep their fragments of S from one group to the next
+  config.gridDim = dim3((unsigned)std::min<long long>(blocks, 148 * kAppBlocks<QJL>), sides);
+  config.blockDim = dim3(kAppThreads);
+  config.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  config.attrs = &attr;
+  config.numAttrs = after ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&config, quantize_slots<TOK, QJL>, p, first, other);
+  const cudaError_t counted = launched();
+  return e != cudaSuccess ? e : counted;
 }
 
 }  // namespace
@@ -441,9 +460,16 @@ cudaError_t launch_set_lengths(const LengthParams& p, cudaStream_t s) {
 
 cudaError_t launch_quantize_slots(const SlotQuantizeParams& p, cudaStream_t s) {
   // 2-bit codes and sketches, TOK 8 against 32: 8.2 / 12.7 us at 16 groups, 16.7 / 16.2 at 80, 23.6 / 20.8 at 152, 65.9 /
-  // 48.0 at 592
+  // 48.0 at 592. One bit without sketches, the kernel that may have one against the other: 10.6 / 10.5 us at 152 groups,
+  // 15.8 / 12.6 at 296, 27.0 / 20.5 at 592; 3 bits and a sketch on one side, both sides at once against a launch each: 22.9 /
+  // 24.5 at 296, 39.3 / 35.7 at 592
   const long long groups = (long long)((p.n_tokens + 31) / 32) * p.heads;
-  return groups >= 148 ? launch_slots<32>(p, s) : launch_slots<8>(p, s);
+  const bool k = p.side[0].qjl, v = p.side[1].qjl;
+  if (groups < 148) return launch_slots<8, true>(p, 0, 2, false, false, s);
+  if (!k && !v) return launch_slots<32, false>(p, 0, 2, false, false, s);
+  if (k == v || groups < 400) return launch_slots<32, true>(p, 0, 2, false, false, s);
+  const cudaError_t e = launch_slots<32, true>(p, k ? 0 : 1, 1, true, false, s);
+  return e != cudaSuccess ? e : launch_slots<32, false>(p, k ? 1 : 0, 1, false, true, s);
 }
 
 }  // namespace kvq

@@ -125,6 +125,38 @@ def test_append_by_slots_stores_what_quantize_stores(name, dtype):
     b.close()
 
 
+@pytest.mark.parametrize("tokens", [700, 1211, 1700])
+@pytest.mark.parametrize("name", ["2q2q", "3q3", "11", "23q", "22", "1q2"])
+def test_large_appends_store_what_small_ones_store(name, tokens):
+    """One call, eager and captured, against calls of 100 tokens: every kernel of the append, sketches on both sides, one
+    or none, and what follows it on the stream sees both sides."""
+    cfg = make_cfg(8, 8, *MODES[name])
+    signs, S = signs_and_sketch(4, cfg)
+    n_pages = tokens // PAGE + 3
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    K, V = (torch.randn(tokens, 8, 128, generator=gen, device="cuda").to(BF16) for _ in range(2))
+    table = cuda_ints(np.random.default_rng(5).permutation(n_pages)[None, :])
+    caches = [kvq.KvqCache(cfg, 1, 0, signs, S, block_table=table, n_pages=n_pages) for _ in range(3)]
+    for c in caches:
+        c.arena[int(c.layout()[4]):].fill_(0x5A)
+    pos = torch.arange(tokens, device="cuda")
+    slots = table[0].long()[pos // PAGE] * PAGE + pos % PAGE
+    for i in range(0, tokens, 100):
+        caches[0].quantize_slots(K[i:i + 100], V[i:i + 100], slots[i:i + 100])
+    caches[1].quantize_slots(K, V, slots)
+    seen = caches[1].arena.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        caches[2].quantize_slots(K, V, slots)
+    graph.replay()
+    first = int(caches[0].layout()[4])
+    for got in (seen, caches[1].arena, caches[2].arena):
+        assert torch.equal(got[first:], caches[0].arena[first:])
+    del graph
+    for c in caches:
+        c.close()
+
+
 def test_lengths_set_without_an_append():
     """Decode over pages filled by slots, a sequence on another's pages, and a finished sequence's place."""
     cfg = make_cfg(4, 2, 2, True, 2, True)
