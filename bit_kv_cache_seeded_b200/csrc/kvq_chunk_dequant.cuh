@@ -43,7 +43,6 @@ __device__ __forceinline__ uint32_t pick(uint32_t lo, uint32_t hi, uint32_t sel)
   return r;
 }
 __device__ __forceinline__ uint32_t half_bits(float x) { return (uint32_t)__half_as_ushort(__float2half_rn(x)); }
-__device__ __forceinline__ float half_of(uint32_t bits) { return __half2float(__ushort_as_half((unsigned short)bits)); }
 
 // The code words (one per plane) of 32 elements, element (byte i, bit s): prepared once, then the fp16 pairs of
 // bytes 0, 1 and 2, 3 for s = 0 .. 7 in turn, which shifts the words along. Two bits: the code picks one of 4

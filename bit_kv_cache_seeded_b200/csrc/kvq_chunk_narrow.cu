@@ -458,11 +458,11 @@ cudaError_t launch_rows(const ChunkParams& p, cudaStream_t s) {
   return launch_after(chunk_narrow<KQ, VQ, N>, p, p.set[kNarrow].ctas, kThreads, smem, 1, s);
 }
 // With a value sketch, tiles of 64 rows leave room for three pages of values instead of four; a call whose fullest tile has
-// 32 rows keeps the fourth. The host does not know, so both are launched, and one of them ends at once (2 us).
+// 32 rows keeps the fourth. Where the host cannot tell, both are launched, and one of them ends at once (2 us).
 // 16 requests of 32 rows over 7000 tokens, 2 bits and sketches: 134 us so, 141 on tiles of 64 rows; 64 rows 160 and 159.
 template <bool KQ, bool VQ>
 cudaError_t launch(const ChunkParams& p, cudaStream_t s) {
-  const cudaError_t e = launch_rows<KQ, VQ, 64>(p, s);
+  const cudaError_t e = VQ && (long long)p.n_tokens * p.group <= 32 ? cudaSuccess : launch_rows<KQ, VQ, 64>(p, s);
   if constexpr (VQ) return e != cudaSuccess ? e : launch_rows<KQ, VQ, 32>(p, s);
   return e;
 }
