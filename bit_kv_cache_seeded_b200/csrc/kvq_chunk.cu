@@ -582,7 +582,7 @@ __global__ void __launch_bounds__(256) chunk_f32(const __grid_constant__ ChunkPa
       if (tx == 0) *reinterpret_cast<float2*>(ml + 2 * row) = make_float2(m[i], l[i]);
 #pragma unroll
       for (int c = 0; c < C; ++c)
-        *reinterpret_cast<float4*>(so + state_pos(kF32Rows, row, 64 * c + 4 * tx)) = make_float4(o[i][c][0], o[i][c][1], o[i][c][2], o[i][c][3]);
+        *reinterpret_cast<float4*>(so + state_pos(kRowShift, kF32Rows, row, 64 * c + 4 * tx)) = make_float4(o[i][c][0], o[i][c][1], o[i][c][2], o[i][c][3]);
     }
   }
 }
@@ -613,6 +613,7 @@ __global__ void __launch_bounds__(kMergeThreads, VQ ? 2 : 3) chunk_merge(const _
     const ChunkSet& set = p.set[in];
     const int group = g - (in ? first[1] : 0), per = set.rows / kMergeRows, tiles = (int)set.head[0];
     const long long units = set.head[1], T = units * p.Hkv, G = cta_count(set, T);
+    const int shift_in = BF16 && !in ? kWideShift : kRowShift;
     const int item = group / per;
     const int hk = item / tiles, tile = item % tiles;
     // rotated, so that a block (a number of blocks that `per` may divide) meets full and empty groups in turn
@@ -656,15 +657,15 @@ __global__ void __launch_bounds__(kMergeThreads, VQ ? 2 : 3) chunk_merge(const _
 #pragma unroll(BF16 ? 2 : 4)
     for (int c = c0; c <= c1; ++c) {
       const float2* ml = reinterpret_cast<const float2*>(segment_ml(set, item, c, DV)) + row0;
-      const float* so = segment_o(set, item, c, DV) + state_pos(set.rows, row0, 4 * lane);
+      const float* so = segment_o(set, item, c, DV) + state_pos(shift_in, set.rows, row0, 4 * lane);
       float o[4][4], z[4][4], f[4];
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         f[v] = -INFINITY;
         if (row0 + v >= r.z) continue;
         f[v] = ml[v].x;
-        load4(o[v], so + v * kStateDims, false, 0);
-        if (VQ) load4(z[v], so + v * kStateDims + kHeadDim * set.rows, false, 0);
+        load4(o[v], so + (v << shift_in), false, 0);
+        if (VQ) load4(z[v], so + (v << shift_in) + kHeadDim * set.rows, false, 0);
       }
 #pragma unroll
       for (int v = 0; v < 4; ++v) {

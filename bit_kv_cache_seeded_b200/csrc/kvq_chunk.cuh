@@ -123,13 +123,13 @@ __device__ __forceinline__ float* segment_ml(const ChunkSet& s, long long item, 
 __device__ __forceinline__ float* segment_o(const ChunkSet& s, long long item, int cta, int dv) {
   return segment_ml(s, item, cta, dv) + 2 * s.rows;
 }
-// Where a row's value dim lies in o: [dim / 16][row][dim % 16], since the wide kernel's lanes hold a row each and write
-// whole sectors of neighbouring rows so, while the merge still reads 64 bytes at once. Mixed batch, wide kernel and
-// merge: rows of all dims, 16 bytes a store, 222 and 53 us; 32 bytes a store in blocks of 32 dims 210 and 58, of 16
-// 192 and 56, of 8 187 and 61.
-constexpr int kStateDims = 16;
-__device__ __forceinline__ int state_pos(int rows, int row, int dim) {
-  return (dim / kStateDims * rows + row) * kStateDims + dim % kStateDims;
+// Where a row's value dim lies in o: [dim / D][row][dim % D], D = 2^shift. The wide kernel's lanes hold a row each: D = 16,
+// so that they write whole sectors of neighbouring rows while the merge still reads 64 bytes at once. Mixed batch, wide
+// kernel and merge: rows of all dims, 16 bytes a store, 222 and 53 us; 32 bytes a store in blocks of 32 dims 210 and 58,
+// of 16 192 and 56, of 8 187 and 61. The other kernels' lanes hold a dim each, or neighbouring ones: D = 128.
+constexpr int kWideShift = 4, kRowShift = 7;
+__device__ __forceinline__ int state_pos(int shift, int rows, int row, int dim) {
+  return (((dim >> shift) * rows + row) << shift) + (dim & ((1 << shift) - 1));
 }
 
 // Where the tensor-core kernels keep coordinate 4 lane + k of a query (or of its sketch), so that the keys' order

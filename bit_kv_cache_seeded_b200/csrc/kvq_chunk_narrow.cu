@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow(const __grid_constan
           for (int c = 0; c < 8; ++c) {
             const float x = ns > 0 ? __uint_as_float(o[c]) : 0.f;
             if (block == C::kSums) l = row0 + c == lane ? x : l;
-            else if (row0 + c < count) so[state_pos(kNarrowRows, c0 + row0 + c, block * 128 + tok)] = x;
+            else if (row0 + c < count) so[state_pos(kRowShift, kNarrowRows, c0 + row0 + c, block * 128 + tok)] = x;
           }
         }
         if (quarter == 0 && lane < count) {

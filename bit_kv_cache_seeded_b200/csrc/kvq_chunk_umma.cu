@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
           // with a sketch each CTA's half of the columns is 64 codes, 64 signs
           const int dim = VQ ? (c & 63) + (c & 128) / 2 + (c & 64) * 2 : c;
           if (row < r.count) {
-            float* to = so + state_pos(set.rows, row, dim);
+            float* to = so + state_pos(kWideShift, set.rows, row, dim);
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[i] = used ? o[i] : 0u;
             store8(to, o);
