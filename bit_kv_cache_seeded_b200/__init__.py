@@ -37,7 +37,7 @@ EXPORTS = ("kvq_status_str", "kvq_cache_bytes", "kvq_packed_bytes_per_token", "k
            "kvq_step_staging_bytes", "kvq_decode_step_host", "kvq_draw_rotation_signs", "kvq_draw_qjl_matrix",
            "kvq_partial_floats", "kvq_decode_partials", "kvq_combine_partials",
            "kvq_cache_bytes_paged", "kvq_cache_init_paged", "kvq_extend_block_table", "kvq_slot_map",
-           "kvq_quantize_slots", "kvq_cache_set_lengths", "kvq_chunk_workspace_bytes", "kvq_chunk_attention")
+           "kvq_quantize_slots", "kvq_quantize_slots_rows", "kvq_cache_set_lengths", "kvq_chunk_workspace_bytes", "kvq_chunk_attention")
 KVQ_STATUS_WAIT_TIMEOUT = 1
 
 
@@ -101,6 +101,7 @@ def load() -> ctypes.CDLL:
         "kvq_extend_block_table": ([VP, VP, I32, VP, I32, VP, VP, I32, VP, VP, VP, VP], I32),
         "kvq_slot_map": ([VP, VP, VP, I32, VP, I32, I32, I32, VP, VP, VP, VP], I32),
         "kvq_quantize_slots": ([VP, VP, VP, I32, VP, I32, VP], I32),
+        "kvq_quantize_slots_rows": ([VP, VP, VP, I32, VP, I32, VP, VP], I32),
         "kvq_cache_set_lengths": ([VP, VP, VP], I32),
         "kvq_chunk_workspace_bytes": ([VP, I32, I32, P(SZ)], I32),
         "kvq_chunk_attention": ([VP, VP, I32, I32, VP, VP, VP, VP, SZ, VP], I32),
@@ -398,17 +399,23 @@ def kvq_slot_map(held: torch.Tensor, seq_start: torch.Tensor, ctx_lens: torch.Te
                                    None if positions is None else positions.data_ptr(), slots.data_ptr(), _stream(stream)))
 
 
-def kvq_quantize_slots(handle, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, stream=None):
-    """Code K, V [n_tokens, n_kv_heads, head_dim] into page slots int64 [n_tokens] (negative: skipped)."""
+def kvq_quantize_slots(handle, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, stream=None, seq_start=None):
+    """Code K, V [n_tokens, n_kv_heads, head_dim] into page slots int64 [n_tokens] (negative: skipped). With
+    seq_start (int32 [batch + 1]) only the rows of requests are written (kvq_quantize_slots_rows); without it every
+    row counts, so slots that kvq_slot_map left as they were have to be negative."""
     fn = "kvq_quantize_slots"
     if K.dtype not in DTYPES or V.dtype != K.dtype:
         raise TypeError("K and V must both be float32 or bfloat16")
     _here(fn, K=K, V=V)
     _here(fn, torch.int64, slots=slots)
+    _here(fn, torch.int32, seq_start=seq_start)
     if K.dim() != 3 or K.shape != V.shape or slots.numel() != K.shape[0]:
         raise ValueError("K and V must be [n_tokens, n_kv_heads, head_dim] and slots [n_tokens]")
-    _check(fn, load().kvq_quantize_slots(handle, K.data_ptr(), V.data_ptr(), DTYPES[K.dtype], slots.data_ptr(), K.shape[0],
-                                         _stream(stream)))
+    args = handle, K.data_ptr(), V.data_ptr(), DTYPES[K.dtype], slots.data_ptr(), K.shape[0]
+    if seq_start is None:
+        _check(fn, load().kvq_quantize_slots(*args, _stream(stream)))
+    else:
+        _check(fn, load().kvq_quantize_slots_rows(*args, seq_start.data_ptr(), _stream(stream)))
 
 
 def kvq_cache_set_lengths(handle, lens, batch: int, stream=None):
@@ -641,11 +648,14 @@ class KvqCache:
         kvq_decode_partials(self.handle, q, partials, self.workspace, stream)
         return partials
 
-    def quantize_slots(self, K, V, slots, stream=None):
-        """Code a token-major batch K, V [n_tokens, n_kv_heads, head_dim] into page slots (kvq_quantize_slots)."""
+    def quantize_slots(self, K, V, slots, stream=None, seq_start=None):
+        """Code a token-major batch K, V [n_tokens, n_kv_heads, head_dim] into page slots (kvq_quantize_slots); with
+        seq_start [batch + 1] the rows of requests alone."""
         if K.dim() != 3 or tuple(K.shape[1:]) != (self.cfg.n_kv_heads, self.cfg.head_dim) or K.shape != V.shape:
             raise ValueError(f"quantize_slots: K, V must be [n_tokens, {self.cfg.n_kv_heads}, {self.cfg.head_dim}]")
-        kvq_quantize_slots(self.handle, K, V, slots, stream)
+        if seq_start is not None and seq_start.numel() != self.batch + 1:
+            raise ValueError(f"quantize_slots: seq_start [{self.batch + 1}]")
+        kvq_quantize_slots(self.handle, K, V, slots, stream, seq_start)
 
     def set_lengths(self, lens, stream=None):
         """Set every sequence's length (kvq_cache_set_lengths)."""

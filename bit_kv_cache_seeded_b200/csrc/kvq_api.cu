@@ -1253,14 +1253,17 @@ kvq_status kvq_cache_set_lengths(kvq_cache* c, const int32_t* lens, void* stream
   return KVQ_OK;
 }
 
-kvq_status kvq_quantize_slots(kvq_cache* c, const void* K, const void* V, kvq_dtype dtype, const int64_t* slots,
-                              int32_t n_tokens, void* stream) {
+}  // extern "C"
+
+namespace {
+kvq_status quantize_slots_impl(kvq_cache* c, const void* K, const void* V, kvq_dtype dtype, const int64_t* slots,
+                               int32_t n_tokens, const int32_t* seq_start, void* stream) {
   if (!c || n_tokens < 0) return KVQ_ERR_INVALID_ARG;
   if (dtype != KVQ_F32 && dtype != KVQ_BF16) return KVQ_ERR_INVALID_ARG;
   if (!c->table || !ragged_supported(c)) return KVQ_ERR_UNSUPPORTED;
   if (n_tokens == 0) return KVQ_OK;
   if (!K || !V || !slots) return KVQ_ERR_INVALID_ARG;
-  if (!aligned16(K) || !aligned16(V) || !aligned_to(slots, 8)) return KVQ_ERR_ALIGNMENT;
+  if (!aligned16(K) || !aligned16(V) || !aligned_to(slots, 8) || !aligned_to(seq_start, 4)) return KVQ_ERR_ALIGNMENT;
   if (!on_cache_device(c)) return KVQ_ERR_INVALID_ARG;
   SlotQuantizeParams p;
   std::memset(&p, 0, sizeof(p));
@@ -1270,6 +1273,8 @@ kvq_status kvq_quantize_slots(kvq_cache* c, const void* K, const void* V, kvq_dt
   p.n_tokens = n_tokens;
   p.heads = c->cfg.n_kv_heads;
   p.slots = reinterpret_cast<const long long*>(slots);
+  p.seq_start = seq_start;
+  p.batch = c->batch;
   p.region[0] = c->d_k;
   p.region[1] = c->d_v;
   p.n_pages = c->n_pages;
@@ -1281,6 +1286,20 @@ kvq_status kvq_quantize_slots(kvq_cache* c, const void* K, const void* V, kvq_dt
   p.s_exp = sketch_exp(c);
   p.err = c->d_status;
   return launch_quantize_slots(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+}  // namespace
+
+extern "C" {
+
+kvq_status kvq_quantize_slots(kvq_cache* c, const void* K, const void* V, kvq_dtype dtype, const int64_t* slots,
+                              int32_t n_tokens, void* stream) {
+  return quantize_slots_impl(c, K, V, dtype, slots, n_tokens, nullptr, stream);
+}
+
+kvq_status kvq_quantize_slots_rows(kvq_cache* c, const void* K, const void* V, kvq_dtype dtype, const int64_t* slots,
+                                   int32_t n_tokens, const int32_t* seq_start, void* stream) {
+  if (!seq_start) return KVQ_ERR_INVALID_ARG;
+  return quantize_slots_impl(c, K, V, dtype, slots, n_tokens, seq_start, stream);
 }
 
 kvq_status kvq_chunk_workspace_bytes(const kvq_cache* c, kvq_dtype dtype, int32_t n_tokens, size_t* bytes) {

@@ -18,6 +18,8 @@ struct SlotQuantizeParams {
   int bf16;
   int n_tokens, heads;
   const long long* slots;   // 64 * page + token of the page; negative: not written
+  const int* seq_start;     // [batch + 1]: rows outside [seq_start[0], seq_start[batch]) are not written; or null: all rows count
+  int batch;
   char* region[2];
   int n_pages;
   SideLayout side[2];

@@ -224,6 +224,7 @@ quantize_slots(const __grid_constant__ SlotQuantizeParams p, int first_side, boo
   const int nthr = (1 << L.bits) - 1;
   const int chunks = (p.n_tokens + TOK - 1) / TOK;
   const long long total = (long long)chunks * p.heads;
+  const int row0 = p.seq_start ? p.seq_start[0] : 0, row1 = p.seq_start ? p.seq_start[p.batch] : p.n_tokens;
   // this warp's rows 16 warp .. + 15 of S (columns of S^T), divided by 2^s_exp
   uint32_t frag[2][2][8][2];
   const bool qjl = QJL && L.qjl;
@@ -253,7 +254,8 @@ quantize_slots(const __grid_constant__ SlotQuantizeParams p, int first_side, boo
 #pragma unroll
     for (int q = 0; q < 4; ++q) sgn[q] = p.signs[h * p.signs_stride + 32 * q + lane];
     for (int i = warp; i < TOK; i += kAppWarps) {
-      long long slot = i < count ? p.slots[first + i] : -1;
+      // rows of no request are skipped without a look: their slots may be an earlier step's
+      long long slot = i < count && first + i >= row0 && first + i < row1 ? p.slots[first + i] : -1;
       if (slot >= (long long)p.n_pages * kPage) {
         if (lane == 0) atomicOr(p.err, kStatusBadPage);
         slot = -1;

@@ -245,7 +245,8 @@ kvq_status kvq_extend_block_table(const int32_t* held, const int32_t* n_new, int
  * / 64]; the slot is -1 when the request was refused (ctx_lens[b] is not held[b] + its new tokens), or
  * when the entry is not a page of a pool of n_pages, or the position is outside the table. seq_ids and
  * positions (int32 [n_tokens]) may be NULL. Rows before seq_start[0] and from seq_start[batch] on are left as they
- * are. seq_start must not decrease. Outputs as above; n_tokens == 0 is a no-op. */
+ * are: buffers that are kept from step to step hold an earlier step's slots there, which an append must not take for
+ * this step's (kvq_quantize_slots_rows). seq_start must not decrease. Outputs as above; n_tokens == 0 is a no-op. */
 kvq_status kvq_slot_map(const int32_t* held, const int32_t* seq_start, const int32_t* ctx_lens, int32_t batch,
                         const int32_t* block_table, int32_t pages_per_seq, int32_t n_pages, int32_t n_tokens,
                         int32_t* seq_ids, int32_t* positions, int64_t* slots, void* stream);
@@ -256,9 +257,14 @@ kvq_status kvq_slot_map(const int32_t* held, const int32_t* seq_start, const int
  * skipped; one past the pool sets KVQ_STATUS_BAD_PAGE and is skipped. The slots of a call are distinct:
  * a slot named twice ends up with unspecified content (its neighbours keep theirs). The cache's lengths
  * do not change: give them to kvq_chunk_attention, or set them with kvq_cache_set_lengths. Caches that
- * are not paged, or with a window, KIVI or FP4 codes: KVQ_ERR_UNSUPPORTED. n_tokens == 0: no-op. */
+ * are not paged, or with a window, KIVI or FP4 codes: KVQ_ERR_UNSUPPORTED. n_tokens == 0: no-op.
+ * kvq_quantize_slots writes every row whose slot is not negative. kvq_quantize_slots_rows writes only the rows of
+ * requests, seq_start[0] <= t < seq_start[batch] (device int32 [batch + 1], the cache's batch), whatever slots holds
+ * elsewhere: for buffers of a fixed size that a step may fill only in part. */
 kvq_status kvq_quantize_slots(kvq_cache* c, const void* K, const void* V, kvq_dtype dtype, const int64_t* slots,
                               int32_t n_tokens, void* stream);
+kvq_status kvq_quantize_slots_rows(kvq_cache* c, const void* K, const void* V, kvq_dtype dtype, const int64_t* slots,
+                                   int32_t n_tokens, const int32_t* seq_start, void* stream);
 
 /* Set every sequence's length (host array of `batch`), on the host and, on `stream`, on the device:
  * after an append by slots, to start a sequence on pages it shares with another, or to reuse a finished

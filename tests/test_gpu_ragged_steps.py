@@ -1,0 +1,110 @@
+"""Steps of the ragged serving path one after the other on the GPU: buffers that are kept, requests that are refused,
+appends of every kernel, what calls share."""
+import numpy as np
+import pytest
+import torch
+
+import bit_kv_cache_seeded_b200 as kvq
+from tests._ragged import PAGE, Batch, assert_close, causal_attention, cuda_ints, dequantised, make_cfg, signs_and_sketch
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    kvq.load()
+
+
+class Server:
+    """The README's step, on buffers of a fixed size that are never filled between steps."""
+
+    def __init__(self, cfg, batch, pages_per_seq, n_pages, rows, dtype=BF16, seed=0):
+        self.cfg, self.n_pages = cfg, n_pages
+        self.signs, self.S = signs_and_sketch(seed, cfg)
+        self.table = torch.full((batch, pages_per_seq), -1, dtype=torch.int32, device="cuda")
+        self.cache = kvq.KvqCache(cfg, batch, 0, self.signs, self.S, block_table=self.table, n_pages=n_pages)
+        self.first = int(self.cache.layout()[4])
+        self.cache.arena[self.first:].fill_(0x5A)
+        self.free, self.cursor = cuda_ints(np.random.default_rng(seed).permutation(n_pages)), cuda_ints([0])
+        self.held, self.new = cuda_ints([0] * batch), cuda_ints([0] * batch)
+        self.start, self.ctx, self.taken = cuda_ints([0] * (batch + 1)), cuda_ints([0] * batch), cuda_ints([0, 0])
+        self.slots = torch.empty(rows, dtype=torch.int64, device="cuda")
+        self.k, self.v = (torch.zeros(rows, cfg.n_kv_heads, 128, dtype=dtype, device="cuda") for _ in range(2))
+        self.q = torch.zeros(rows, cfg.n_q_heads, 128, dtype=dtype, device="cuda")
+        self.gen = torch.Generator(device="cuda").manual_seed(seed)
+
+    def inputs(self, new):
+        self.new.copy_(torch.tensor(new, dtype=torch.int32))
+        for t in (self.k, self.v, self.q):
+            t.copy_(torch.randn(t.shape, generator=self.gen, device="cuda"))
+
+    def append(self):
+        kvq.kvq_extend_block_table(self.held, self.new, self.free, self.table, self.start, self.ctx, self.taken, self.cursor)
+        kvq.kvq_slot_map(self.held, self.start, self.ctx, self.table, self.n_pages, None, None, self.slots)
+        self.cache.quantize_slots(self.k, self.v, self.slots, seq_start=self.start)
+
+    def advance(self):
+        self.cursor.add_(self.taken[:1])
+        self.held.copy_(self.ctx)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows", [160, 1300])
+@pytest.mark.parametrize("name", [(2, True, 2, True), (1, False, 1, False), (3, True, 3, False)])
+def test_a_short_step_after_a_long_one_leaves_the_rest_of_the_pool(name, rows, dtype):
+    """The slots behind a step's tokens are still the long step's; they may also be anything else. The pool is that of an
+    append of the step's tokens alone."""
+    s = Server(make_cfg(4, 4, *name), 3, rows // PAGE + 2, rows // PAGE + 6, rows, dtype)
+    s.inputs([rows - 70, 0, 70])
+    s.append()
+    s.advance()
+    alone = kvq.KvqCache(s.cfg, 3, 0, s.signs, s.S, block_table=s.table, n_pages=s.n_pages)
+    for new, junk in (([1, 1, 0], False), ([0, 0, 0], False), ([0, 2, 3], True)):
+        alone.arena[s.first:] = s.cache.arena[s.first:]
+        s.inputs(new)
+        if junk:
+            s.slots.copy_(torch.randint(-2 ** 62, 2 ** 62, s.slots.shape, device="cuda"))
+            s.slots[-40:] = torch.arange(40, device="cuda")
+        s.append()
+        s.advance()
+        n = sum(new)
+        alone.quantize_slots(s.k[:n], s.v[:n], s.slots[:n])
+        assert torch.equal(alone.arena[s.first:], s.cache.arena[s.first:])
+    assert kvq.kvq_cache_status(s.cache.handle) == 0
+    alone.close()
+    s.cache.close()
+
+
+@pytest.mark.parametrize("name", [(2, True, 2, True), (1, False, 1, False), (3, True, 3, False)])
+@pytest.mark.parametrize("tokens", [40, 700, 1700])
+def test_rows_of_requests_alone_are_appended(name, tokens):
+    """Requests that begin behind the first row and end before the last: the pool's bytes are those of an append of
+    their rows by themselves."""
+    cfg = make_cfg(8, 8, *name)
+    signs, S = signs_and_sketch(2, cfg)
+    n_pages = tokens // PAGE + 3
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    K, V = (torch.randn(tokens, 8, 128, generator=gen, device="cuda").to(BF16) for _ in range(2))
+    slots = torch.randperm(n_pages * PAGE, generator=gen, device="cuda")[:tokens]
+    table = cuda_ints(np.full((2, n_pages), -1))
+    caches = [kvq.KvqCache(cfg, 2, 0, signs, S, block_table=table, n_pages=n_pages) for _ in range(2)]
+    for c in caches:
+        c.arena[int(c.layout()[4]):].fill_(0x5A)
+    a, b = 5, tokens - 9
+    caches[0].quantize_slots(K, V, slots, seq_start=cuda_ints([a, a + 7, b]))
+    alone = torch.full_like(slots, -1)
+    alone[a:b] = slots[a:b]
+    caches[1].quantize_slots(K, V, alone)
+    first = int(caches[0].layout()[4])
+    assert torch.equal(caches[0].arena[first:], caches[1].arena[first:])
+    for start in ([0, 0, 0], [tokens, tokens, tokens], [-5, -3, -1], [9, 9, 2]):  # no row of a request
+        caches[0].quantize_slots(K.flip(0).contiguous(), V, slots, seq_start=cuda_ints(start))
+    assert torch.equal(caches[0].arena[first:], caches[1].arena[first:])
+    caches[0].quantize_slots(K, V, slots, seq_start=cuda_ints([-3, 0, tokens + 100]))  # all of them
+    caches[1].quantize_slots(K, V, slots)
+    assert torch.equal(caches[0].arena[first:], caches[1].arena[first:])
+    for c in caches:
+        c.close()
