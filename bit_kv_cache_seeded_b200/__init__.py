@@ -37,7 +37,8 @@ EXPORTS = ("kvq_status_str", "kvq_cache_bytes", "kvq_packed_bytes_per_token", "k
            "kvq_step_staging_bytes", "kvq_decode_step_host", "kvq_draw_rotation_signs", "kvq_draw_qjl_matrix",
            "kvq_partial_floats", "kvq_decode_partials", "kvq_combine_partials",
            "kvq_cache_bytes_paged", "kvq_cache_init_paged", "kvq_extend_block_table", "kvq_slot_map",
-           "kvq_quantize_slots", "kvq_quantize_slots_rows", "kvq_cache_set_lengths", "kvq_chunk_workspace_bytes", "kvq_chunk_attention")
+           "kvq_quantize_slots", "kvq_quantize_slots_rows", "kvq_cache_set_lengths", "kvq_chunk_workspace_bytes", "kvq_chunk_attention",
+           "kvq_chunk_attention_held")
 KVQ_STATUS_WAIT_TIMEOUT = 1
 
 
@@ -105,6 +106,7 @@ def load() -> ctypes.CDLL:
         "kvq_cache_set_lengths": ([VP, VP, VP], I32),
         "kvq_chunk_workspace_bytes": ([VP, I32, I32, P(SZ)], I32),
         "kvq_chunk_attention": ([VP, VP, I32, I32, VP, VP, VP, VP, SZ, VP], I32),
+        "kvq_chunk_attention_held": ([VP, VP, I32, I32, VP, VP, VP, VP, VP, SZ, VP], I32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -435,21 +437,25 @@ def kvq_chunk_workspace_bytes(handle, dtype, n_tokens: int) -> int:
 
 
 def kvq_chunk_attention(handle, q: torch.Tensor, seq_start: torch.Tensor, ctx_lens, out: torch.Tensor,
-                        workspace: torch.Tensor, stream=None):
+                        workspace: torch.Tensor, stream=None, held=None):
     """Attention of new tokens' queries q [n_tokens, n_q_heads, head_dim], request b's in rows seq_start[b] ..
     seq_start[b + 1] - 1, over the packed cache of ctx_lens [batch] tokens (None: the cache's lengths). out is
-    like q."""
+    like q. With held [batch], the lengths before the step, requests that kvq_extend_block_table refused get zeros
+    (kvq_chunk_attention_held); without it their rows attend as if their tokens were the last of ctx_lens."""
     fn = "kvq_chunk_attention"
     if q.dtype not in DTYPES or out.dtype != q.dtype:
         raise TypeError("q and out must both be float32 or bfloat16")
     _here(fn, q=q, out=out, workspace=workspace)
-    _here(fn, torch.int32, seq_start=seq_start, ctx_lens=ctx_lens)
+    _here(fn, torch.int32, seq_start=seq_start, ctx_lens=ctx_lens, held=held)
     if q.dim() != 3 or out.shape != q.shape:
         raise ValueError("q and out must be [n_tokens, n_q_heads, head_dim]")
-    _check(fn, load().kvq_chunk_attention(handle, q.data_ptr(), DTYPES[q.dtype], q.shape[0], seq_start.data_ptr(),
-                                          None if ctx_lens is None else ctx_lens.data_ptr(), out.data_ptr(),
-                                          workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                          _stream(stream)))
+    first = (handle, q.data_ptr(), DTYPES[q.dtype], q.shape[0], seq_start.data_ptr(),
+             None if ctx_lens is None else ctx_lens.data_ptr())
+    last = out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)
+    if held is None:
+        _check(fn, load().kvq_chunk_attention(*first, *last))
+    else:
+        _check(fn, load().kvq_chunk_attention_held(*first, held.data_ptr(), *last))
 
 
 def kvq_decode_attention_static(handle, q: torch.Tensor, out: torch.Tensor, stream=None):
@@ -661,21 +667,21 @@ class KvqCache:
         """Set every sequence's length (kvq_cache_set_lengths)."""
         kvq_cache_set_lengths(self.handle, lens, self.batch, stream)
 
-    def chunk_attention(self, q, seq_start, ctx_lens=None, out=None, workspace=None, stream=None):
-        """Attention of a ragged batch of new tokens (kvq_chunk_attention); returns out, like q. Without a
-        workspace the cache keeps one per stream, grown to the largest call there; a captured call takes one
+    def chunk_attention(self, q, seq_start, ctx_lens=None, out=None, workspace=None, stream=None, held=None):
+        """Attention of a ragged batch of new tokens (kvq_chunk_attention; with held, the lengths before the step, refused
+        requests get zeros); returns out, like q. Without a workspace the cache keeps one per stream, grown to the largest call there; a captured call takes one
         from the graph's own memory, so that no two graphs share it."""
         if q.dim() != 3 or tuple(q.shape[1:]) != (self.cfg.n_q_heads, self.cfg.head_dim):
             raise ValueError(f"chunk_attention: q must be [n_tokens, {self.cfg.n_q_heads}, {self.cfg.head_dim}]")
-        if seq_start.numel() != self.batch + 1 or (ctx_lens is not None and ctx_lens.numel() != self.batch):
-            raise ValueError(f"chunk_attention: seq_start [{self.batch + 1}] and ctx_lens [{self.batch}]")
+        if seq_start.numel() != self.batch + 1 or any(t is not None and t.numel() != self.batch for t in (ctx_lens, held)):
+            raise ValueError(f"chunk_attention: seq_start [{self.batch + 1}], ctx_lens and held [{self.batch}]")
         if q.dtype not in DTYPES:
             raise TypeError("q must be float32 or bfloat16")
         if out is None:
             out = torch.empty_like(q)
         if workspace is None:
             workspace = self._chunk_workspace(kvq_chunk_workspace_bytes(self.handle, q.dtype, q.shape[0]), q.device, stream)
-        kvq_chunk_attention(self.handle, q, seq_start, ctx_lens, out, workspace, stream)
+        kvq_chunk_attention(self.handle, q, seq_start, ctx_lens, out, workspace, stream, held)
         return out
 
     def _chunk_workspace(self, need, device, stream):

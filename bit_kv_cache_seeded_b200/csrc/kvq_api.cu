@@ -1311,9 +1311,12 @@ kvq_status kvq_chunk_workspace_bytes(const kvq_cache* c, kvq_dtype dtype, int32_
   return KVQ_OK;
 }
 
-kvq_status kvq_chunk_attention(const kvq_cache* c, const void* q, kvq_dtype dtype, int32_t n_tokens,
-                               const int32_t* seq_start, const int32_t* ctx_lens, void* out, void* workspace,
-                               size_t ws_bytes, void* stream) {
+}  // extern "C"
+
+namespace {
+kvq_status chunk_attention_impl(const kvq_cache* c, const void* q, kvq_dtype dtype, int32_t n_tokens,
+                                const int32_t* seq_start, const int32_t* ctx_lens, const int32_t* held, void* out,
+                                void* workspace, size_t ws_bytes, void* stream) {
   if (!c || n_tokens < 0) return KVQ_ERR_INVALID_ARG;
   if (dtype != KVQ_F32 && dtype != KVQ_BF16) return KVQ_ERR_INVALID_ARG;
   if (!ragged_supported(c)) return KVQ_ERR_UNSUPPORTED;
@@ -1321,7 +1324,7 @@ kvq_status kvq_chunk_attention(const kvq_cache* c, const void* q, kvq_dtype dtyp
   if (!q || !seq_start || !out || !workspace) return KVQ_ERR_INVALID_ARG;
   if ((long)n_tokens * c->cfg.n_q_heads > (1l << 30)) return KVQ_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return KVQ_ERR_ALIGNMENT;
-  if (!aligned_to(seq_start, 4) || !aligned_to(ctx_lens, 4)) return KVQ_ERR_ALIGNMENT;
+  if (!aligned_to(seq_start, 4) || !aligned_to(ctx_lens, 4) || !aligned_to(held, 4)) return KVQ_ERR_ALIGNMENT;
   if (!on_cache_device(c)) return KVQ_ERR_INVALID_ARG;
   const bool bf16 = dtype == KVQ_BF16;
   const ChunkLayout L = chunk_layout_of(c, n_tokens, bf16);
@@ -1338,6 +1341,7 @@ kvq_status kvq_chunk_attention(const kvq_cache* c, const void* q, kvq_dtype dtyp
   p.group = p.Hq / p.Hkv;
   p.seq_start = seq_start;
   p.ctx_lens = ctx_lens ? ctx_lens : c->d_lens;
+  p.held = held;
   p.capacity = c->capacity;
   p.kreg = c->d_k;
   p.vreg = c->d_v;
@@ -1376,6 +1380,22 @@ kvq_status kvq_chunk_attention(const kvq_cache* c, const void* q, kvq_dtype dtyp
   p.qprep = w + L.qprep;
   p.qscale = reinterpret_cast<float*>(w + L.qscale);
   return launch_chunk_attention(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+}  // namespace
+
+extern "C" {
+
+kvq_status kvq_chunk_attention(const kvq_cache* c, const void* q, kvq_dtype dtype, int32_t n_tokens,
+                               const int32_t* seq_start, const int32_t* ctx_lens, void* out, void* workspace,
+                               size_t ws_bytes, void* stream) {
+  return chunk_attention_impl(c, q, dtype, n_tokens, seq_start, ctx_lens, nullptr, out, workspace, ws_bytes, stream);
+}
+
+kvq_status kvq_chunk_attention_held(const kvq_cache* c, const void* q, kvq_dtype dtype, int32_t n_tokens,
+                                    const int32_t* seq_start, const int32_t* ctx_lens, const int32_t* held, void* out,
+                                    void* workspace, size_t ws_bytes, void* stream) {
+  if (!held) return KVQ_ERR_INVALID_ARG;
+  return chunk_attention_impl(c, q, dtype, n_tokens, seq_start, ctx_lens, held, out, workspace, ws_bytes, stream);
 }
 
 }  // extern "C"

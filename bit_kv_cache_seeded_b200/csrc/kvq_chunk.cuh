@@ -45,7 +45,9 @@ __device__ __forceinline__ Rows tile_rows(const ChunkParams& p, const ChunkSet& 
   r.first = tile * per;
   const int tokens = min(per, n - r.first);
   r.count = tokens * p.group;
-  r.ctx = min(max(p.ctx_lens[b], 0), p.capacity);
+  const int ctx = p.ctx_lens[b];
+  // a refused request's new tokens are not in the cache: no positions, so its rows get zeros
+  r.ctx = p.held && (long long)p.held[b] + n != ctx ? 0 : min(max(ctx, 0), p.capacity);
   r.pos0 = r.ctx - n + r.first;
   r.limit = max(0, r.pos0 + tokens);
   return r;

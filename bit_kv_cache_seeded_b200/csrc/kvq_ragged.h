@@ -53,6 +53,7 @@ struct ChunkParams {
   int n_tokens, B, Hq, Hkv, group;
   const int* seq_start;     // [B + 1]
   const int* ctx_lens;      // [B]
+  const int* held;          // [B]: a request whose ctx_lens is not held + its new tokens was refused; or null
   int capacity;             // tokens a sequence can hold
   const char* kreg;
   const char* vreg;

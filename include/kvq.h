@@ -287,11 +287,19 @@ kvq_status kvq_cache_set_lengths(kvq_cache* c, const int32_t* lens, void* stream
  * LM, LM_QJL and SIGN1 caches without a window, paged or not; others KVQ_ERR_UNSUPPORTED. n_tokens * n_q_heads may not
  * exceed 2^30. A block-table entry outside the pool sets KVQ_STATUS_BAD_PAGE and reads page 0. The
  * workspace (kvq_chunk_workspace_bytes for this type and n_tokens) is in use until the call's work is
- * done: calls that may overlap, and graphs that may replay at the same time, need one each. */
+ * done: calls that may overlap, and graphs that may replay at the same time, need one each.
+ * A request that kvq_extend_block_table refused keeps its rows in seq_start, but its new tokens are not in
+ * the cache and ctx_lens is what it held before. kvq_chunk_attention cannot tell it from one whose tokens are the last
+ * of ctx_lens, and attends with its rows as if they were: a caller that does not read taken[1] uses
+ * kvq_chunk_attention_held, which is given the lengths before the step (held, device int32 [batch]) and writes zeros for
+ * every request whose ctx_lens[b] is not held[b] + its rows. */
 kvq_status kvq_chunk_workspace_bytes(const kvq_cache* c, kvq_dtype dtype, int32_t n_tokens, size_t* bytes);
 kvq_status kvq_chunk_attention(const kvq_cache* c, const void* q, kvq_dtype dtype, int32_t n_tokens,
                                const int32_t* seq_start, const int32_t* ctx_lens, void* out, void* workspace,
                                size_t ws_bytes, void* stream);
+kvq_status kvq_chunk_attention_held(const kvq_cache* c, const void* q, kvq_dtype dtype, int32_t n_tokens,
+                                    const int32_t* seq_start, const int32_t* ctx_lens, const int32_t* held, void* out,
+                                    void* workspace, size_t ws_bytes, void* stream);
 
 /* Device bytes of the staging buffer kvq_decode_step_host needs for inputs of type dtype: two
  * input slots (one step's K and V with n_new = 1 for all sequences, and q), then two output slots;

@@ -108,3 +108,46 @@ def test_rows_of_requests_alone_are_appended(name, tokens):
     assert torch.equal(caches[0].arena[first:], caches[1].arena[first:])
     for c in caches:
         c.close()
+
+
+# ---- refused requests
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("name", [(2, True, 2, True), (3, True, 3, False)])
+def test_a_refused_request_between_granted_ones(name, dtype):
+    """The four calls of a step that refuses a request of one, of a few and of many tokens: nothing of it is appended, its
+    rows get zeros, and the others get what they get without it. The next step goes on from the lengths that are left."""
+    cfg = make_cfg(4, 2, *name)
+    s = Server(cfg, 5, 6, 16, 400, dtype)
+    s.inputs([100, 40, 200, 10, 0])
+    s.append()
+    s.advance()
+    for new, over in (([20, 120, 3, 70, 1], 1), ([6, 10, 250, 0, 0], 2), ([1, 2, 4, 400, 3], 3), ([5, -1, 5, 5, 5], 1)):
+        total = sum(max(n, 0) for n in new)
+        if over == 1 and new[1] > 0:      # want of pages: the free list ends behind the request's first
+            s.free = s.free[:int(s.cursor) + 1].contiguous()
+        if total > s.slots.numel():
+            s.slots = torch.empty(total, dtype=torch.int64, device="cuda")
+            s.k, s.v = (torch.empty(total, 2, 128, dtype=dtype, device="cuda") for _ in range(2))
+            s.q = torch.empty(total, 4, 128, dtype=dtype, device="cuda")
+        s.inputs(new)
+        held = s.held.tolist()
+        s.append()
+        granted = [c == h + max(n, 0) and n >= 0 for c, h, n in zip(s.ctx.tolist(), held, new)]
+        assert not granted[over] and int(s.taken[1]) == granted.count(False)
+        out = s.cache.chunk_attention(s.q, s.start, s.ctx, out=torch.full_like(s.q, 3.0), held=s.held)
+        ref, at = np.zeros((total, 4, 128)), 0
+        for b, n in enumerate(max(n, 0) for n in new):
+            for hk in range(2 if granted[b] and n else 0):
+                K, V = dequantised(s.cache, cfg, s.table.cpu().numpy(), b, hk, held[b] + n, s.signs, s.S)
+                ref[at:at + n, 2 * hk:2 * hk + 2] = causal_attention(s.q[at:at + n, 2 * hk:2 * hk + 2].double().cpu().numpy(),
+                                                                     K, V, held[b] + n)
+            if not granted[b]:
+                assert not out[at:at + n].any()
+            at += n
+        assert_close(out[:total], ref, dtype)
+        assert (out[total:] == 3).all()
+        s.advance()
+        assert s.held.tolist() == [h + n if g else h for h, n, g in zip(held, new, granted)]
+    assert kvq.kvq_cache_status(s.cache.handle) == 0
+    s.cache.close()

@@ -34,3 +34,14 @@ def test_append_of_request_rows_refuses(lib):
     with pytest.raises(ValueError, match="seq_start"):
         bare_cache().quantize_slots(x, x, slots, seq_start=torch.zeros(3, dtype=torch.int32))
     assert kvq.kvq_kernel_launches() == n
+
+
+def test_attention_with_lengths_before_the_step_refuses(lib):
+    n = kvq.kvq_kernel_launches()
+    args = [None, ptr(0), 0, 1, ptr(1), None, ptr(2), ptr(3), ptr(4), 1 << 20, None]
+    assert lib.kvq_chunk_attention_held(*args) == INVALID
+    assert lib.kvq_chunk_attention_held(ptr(9), *args[1:6], None, *args[7:]) == INVALID
+    with pytest.raises(ValueError, match="held"):
+        bare_cache().chunk_attention(torch.zeros(5, 8, 128), torch.zeros(4, dtype=torch.int32),
+                                     held=torch.zeros(4, dtype=torch.int32))
+    assert kvq.kvq_kernel_launches() == n
