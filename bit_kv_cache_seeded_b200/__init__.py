@@ -12,6 +12,7 @@ workspace for convenience.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -137,6 +138,12 @@ def _stream(stream=None):
     if stream is None:  # torch.cuda.current_stream().cuda_stream without the object: 0.3 us instead of 3.4
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream
+
+
+def _memory_of(stream):
+    """What is allocated inside is `stream`'s memory (None: the current one's). A tensor that a call on `stream` writes
+    must not come from another stream's: its memory may be in use there by work that `stream` does not wait for."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def make_cfg(head_dim=128, n_q_heads=1, n_kv_heads=1, k_mode="lm_qjl", v_mode="lm_qjl", k_bits=2,
@@ -677,17 +684,15 @@ class KvqCache:
             raise ValueError(f"chunk_attention: seq_start [{self.batch + 1}], ctx_lens and held [{self.batch}]")
         if q.dtype not in DTYPES:
             raise TypeError("q must be float32 or bfloat16")
-        if out is None:
-            out = torch.empty_like(q)
-        if workspace is None:
-            workspace = self._chunk_workspace(kvq_chunk_workspace_bytes(self.handle, q.dtype, q.shape[0]), q.device, stream)
+        with _memory_of(stream):
+            if out is None:
+                out = torch.empty_like(q)
+            if workspace is None:
+                workspace = self._chunk_workspace(kvq_chunk_workspace_bytes(self.handle, q.dtype, q.shape[0]), q.device)
         kvq_chunk_attention(self.handle, q, seq_start, ctx_lens, out, workspace, stream, held)
         return out
 
-    def _chunk_workspace(self, need, device, stream):
-        if stream is not None:
-            with torch.cuda.stream(stream):
-                return self._chunk_workspace(need, device, None)
+    def _chunk_workspace(self, need, device):
         # memory of the current stream: a workspace it outgrows is reused in its order
         if torch.cuda.is_current_stream_capturing():
             return torch.empty(need, dtype=torch.uint8, device=device)

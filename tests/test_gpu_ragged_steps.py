@@ -151,3 +151,22 @@ def test_a_refused_request_between_granted_ones(name, dtype):
         assert s.held.tolist() == [h + n if g else h for h, n, g in zip(held, new, granted)]
     assert kvq.kvq_cache_status(s.cache.handle) == 0
     s.cache.close()
+
+
+# ---- streams and threads
+
+def test_out_on_a_stream_given_by_name():
+    """The result is the given stream's memory; what is pending on the current stream does not reach it."""
+    x = Batch(make_cfg(8, 2, 2, True, 2, True), [600, 3], [40, 2], seed=24)
+    want = x.cache.chunk_attention(x.q, x.seq_start, x.ctx_lens)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    old = torch.full_like(want, 3.0)
+    del old                                     # its memory is the next of the current stream's
+    out = x.cache.chunk_attention(x.q, x.seq_start, x.ctx_lens, stream=s)
+    of = {seg["address"]: (seg["total_size"], seg["stream"]) for seg in torch.cuda.memory_snapshot()}
+    at = [stream for base, (size, stream) in of.items() if base <= out.data_ptr() < base + size]
+    assert at == [s.cuda_stream]
+    s.synchronize()
+    assert torch.equal(out, want)
+    x.cache.close()

@@ -1,4 +1,5 @@
 """The ragged serving path's calls as far as they need no GPU: refusals, and what the Python side hands to the library."""
+import contextlib
 import ctypes
 
 import pytest
@@ -45,3 +46,46 @@ def test_attention_with_lengths_before_the_step_refuses(lib):
         bare_cache().chunk_attention(torch.zeros(5, 8, 128), torch.zeros(4, dtype=torch.int32),
                                      held=torch.zeros(4, dtype=torch.int32))
     assert kvq.kvq_kernel_launches() == n
+
+
+class Streams:
+    """Stands in for torch's streams: knows the current one, and on which every tensor was made."""
+
+    def __init__(self, monkeypatch):
+        self.current, self.made, self.calls = "current", [], []
+        for name in ("empty", "empty_like"):
+            monkeypatch.setattr(torch, name, self._recorded(getattr(torch, name)))
+        monkeypatch.setattr(torch.cuda, "stream", self._switched)
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+        monkeypatch.setattr(kvq, "_stream", lambda s=None: s or self.current)
+
+    def _recorded(self, make):
+        def made(*args, **kw):
+            t = make(*args, **kw)
+            self.made.append((t, self.current))
+            return t
+        return made
+
+    @contextlib.contextmanager
+    def _switched(self, stream):
+        before, self.current = self.current, stream
+        yield
+        self.current = before
+
+    def of(self, tensor):
+        return next(s for t, s in self.made if t is tensor)
+
+
+def test_attention_on_a_named_stream_makes_its_tensors_there(lib, monkeypatch):
+    """Memory of another stream may be in use by work that the named one does not wait for."""
+    streams, seen = Streams(monkeypatch), []
+    monkeypatch.setattr(kvq, "kvq_chunk_workspace_bytes", lambda handle, dtype, n: 64)
+    monkeypatch.setattr(kvq, "kvq_chunk_attention", lambda h, q, start, ctx, out, ws, stream, held=None: seen.append((out, ws, stream)))
+    c, q, start = bare_cache(), torch.zeros(5, 8, 128), torch.zeros(4, dtype=torch.int32)
+    for stream in ("side", None):
+        out = c.chunk_attention(q, start, stream=stream)
+        used, ws, at = seen[-1]
+        assert used is out and at == stream and streams.current == "current"
+        assert streams.of(out) == streams.of(ws) == (stream or "current")
+    mine = torch.zeros_like(q)
+    assert c.chunk_attention(q, start, out=mine, stream="side") is mine
