@@ -615,8 +615,9 @@ class KvqCache:
         self._check_kv("step", K, V, self.batch, 1)
         self._check_q_out("step", q, out)
         if out is None:
-            out = torch.empty((self.batch, self.cfg.n_q_heads, self.out_dim), dtype=torch.float32,
-                              device=q.device)
+            with _memory_of(stream):
+                out = torch.empty((self.batch, self.cfg.n_q_heads, self.out_dim), dtype=torch.float32,
+                                  device=q.device)
         kvq_decode_step(self.handle, K, V, q, out, self.workspace, stream)
         return out
 
@@ -638,15 +639,17 @@ class KvqCache:
             raise ValueError("step_host: out must be float32 [batch, n_q_heads, out_dim]")
         need = kvq_step_staging_bytes(self.handle, q.dtype)
         if getattr(self, "staging", None) is None or self.staging.numel() < need:
-            self.staging = torch.empty(need, dtype=torch.uint8, device=self.workspace.device)
+            with _memory_of(stream):
+                self.staging = torch.empty(need, dtype=torch.uint8, device=self.workspace.device)
         return kvq_decode_step_host(self.handle, K, V, q, q.dtype, out, self.staging, self.workspace, stream,
                                     out_event)
 
     def decode(self, q, out=None, stream=None):
         self._check_q_out("decode", q, out)
         if out is None:
-            out = torch.empty((self.batch, self.cfg.n_q_heads, self.out_dim), dtype=torch.float32,
-                              device=q.device)
+            with _memory_of(stream):
+                out = torch.empty((self.batch, self.cfg.n_q_heads, self.out_dim), dtype=torch.float32,
+                                  device=q.device)
         kvq_decode_attention(self.handle, q, out, self.workspace, stream)
         return out
 
@@ -655,7 +658,8 @@ class KvqCache:
         self._check_q_out("decode_partials", q, None)
         n = kvq_partial_floats(self.handle)
         if partials is None:
-            partials = torch.empty((self.batch, self.cfg.n_q_heads, n), dtype=torch.float32, device=q.device)
+            with _memory_of(stream):
+                partials = torch.empty((self.batch, self.cfg.n_q_heads, n), dtype=torch.float32, device=q.device)
         if tuple(partials.shape) != (self.batch, self.cfg.n_q_heads, n):
             raise ValueError(f"decode_partials: partials must be {(self.batch, self.cfg.n_q_heads, n)}")
         kvq_decode_partials(self.handle, q, partials, self.workspace, stream)

@@ -89,3 +89,21 @@ def test_attention_on_a_named_stream_makes_its_tensors_there(lib, monkeypatch):
         assert streams.of(out) == streams.of(ws) == (stream or "current")
     mine = torch.zeros_like(q)
     assert c.chunk_attention(q, start, out=mine, stream="side") is mine
+
+
+def test_decode_calls_on_a_named_stream_make_their_tensors_there(lib, monkeypatch):
+    streams, seen = Streams(monkeypatch), []
+    for name in ("kvq_decode_attention", "kvq_decode_step", "kvq_decode_partials", "kvq_decode_step_host"):
+        monkeypatch.setattr(kvq, name, lambda *args, name=name: seen.append((name, args)))
+    monkeypatch.setattr(kvq, "kvq_partial_floats", lambda handle: 130)
+    monkeypatch.setattr(kvq, "kvq_step_staging_bytes", lambda handle, dtype: 64)
+    monkeypatch.setattr(torch.Tensor, "pin_memory", lambda t: t)
+    c, q, kv = bare_cache(), torch.zeros(3, 8, 128), torch.zeros(3, 2, 1, 128)
+    c.out_dim, c.workspace = 128, torch.zeros(64, dtype=torch.uint8)
+    for stream in ("side", None):
+        c.staging = None
+        made = [c.decode(q, stream=stream), c.step(kv, kv, q, stream=stream), c.decode_partials(q, stream=stream)]
+        c.step_host(kv, kv, q, stream=stream)
+        assert [streams.of(t) for t in (*made, c.staging)] == [stream or "current"] * 4
+        assert streams.current == "current"
+    assert [name for name, _ in seen[:4]] == ["kvq_decode_attention", "kvq_decode_step", "kvq_decode_partials", "kvq_decode_step_host"]
