@@ -15,7 +15,7 @@ from __future__ import annotations
 import torch
 import torch.distributed as dist
 
-from . import kvq_combine_partials
+from . import _memory_of, kvq_combine_partials
 
 
 def shard_range(ctx: int, rank: int, world: int) -> tuple[int, int]:
@@ -40,9 +40,10 @@ def exchange_states(local: torch.Tensor, group=None) -> torch.Tensor:
 def context_parallel_decode(cache, q: torch.Tensor, out: torch.Tensor | None = None, group=None,
                             stream=None) -> torch.Tensor:
     """Decode attention of q over the context of all ranks' shards (every rank gets out)."""
-    local = cache.decode_partials(q, stream=stream)
-    states = exchange_states(local, group)
-    if out is None:
-        out = torch.empty((cache.batch, cache.cfg.n_q_heads, cache.out_dim), dtype=torch.float32, device=q.device)
-    kvq_combine_partials(states, out, stream=stream)
+    with _memory_of(stream):  # the exchange too runs on the stream, behind the states and before their merge
+        local = cache.decode_partials(q, stream=stream)
+        states = exchange_states(local, group)
+        if out is None:
+            out = torch.empty((cache.batch, cache.cfg.n_q_heads, cache.out_dim), dtype=torch.float32, device=q.device)
+        kvq_combine_partials(states, out, stream=stream)
     return out

@@ -107,3 +107,19 @@ def test_decode_calls_on_a_named_stream_make_their_tensors_there(lib, monkeypatc
         assert [streams.of(t) for t in (*made, c.staging)] == [stream or "current"] * 4
         assert streams.current == "current"
     assert [name for name, _ in seen[:4]] == ["kvq_decode_attention", "kvq_decode_step", "kvq_decode_partials", "kvq_decode_step_host"]
+
+
+def test_context_parallel_decode_on_a_named_stream_exchanges_there(lib, monkeypatch):
+    from bit_kv_cache_seeded_b200 import context_parallel
+    streams, seen = Streams(monkeypatch), []
+    monkeypatch.setattr(kvq, "kvq_partial_floats", lambda handle: 130)
+    monkeypatch.setattr(kvq, "kvq_decode_partials", lambda *args: seen.append(("states", args[-1])))
+    monkeypatch.setattr(context_parallel, "exchange_states", lambda t, group: seen.append(("exchange", streams.current)) or t[None])
+    monkeypatch.setattr(context_parallel, "kvq_combine_partials", lambda s, out, stream: seen.append(("merge", stream)))
+    c, q = bare_cache(), torch.zeros(3, 8, 128)
+    c.out_dim, c.workspace = 128, torch.zeros(64, dtype=torch.uint8)
+    for stream in ("side", None):
+        out = context_parallel.context_parallel_decode(c, q, stream=stream)
+        assert streams.of(out) == (stream or "current")
+    assert seen == [(n, s) for s in ("side", None) for n in ("states", "exchange", "merge")][:3] + [
+        ("states", None), ("exchange", "current"), ("merge", None)]
