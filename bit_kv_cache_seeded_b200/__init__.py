@@ -15,6 +15,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import threading
 
 import numpy as np
 import torch
@@ -581,6 +582,7 @@ class KvqCache:
             self.handle = kvq_cache_init_paged(cfg, batch, n_pages, block_table, self.arena, rot_signs, qjl_matrix)
         self.workspace = torch.empty(max(16, kvq_workspace_bytes(self.handle)), dtype=torch.uint8,
                                      device=device)
+        self.chunk_workspaces, self.chunk_lock = {}, threading.Lock()
         self.out_dim = cfg.latent_dim if cfg.k_mode == MODES["fp4"] else cfg.head_dim
 
     # Shapes the library reads and writes; it cannot see tensor extents, so they are checked here.
@@ -681,7 +683,8 @@ class KvqCache:
     def chunk_attention(self, q, seq_start, ctx_lens=None, out=None, workspace=None, stream=None, held=None):
         """Attention of a ragged batch of new tokens (kvq_chunk_attention; with held, the lengths before the step, refused
         requests get zeros); returns out, like q. Without a workspace the cache keeps one per stream, grown to the largest call there; a captured call takes one
-        from the graph's own memory, so that no two graphs share it."""
+        from the graph's own memory, so that no two graphs share it. Calls of several threads are enqueued one after
+        the other; a workspace of one's own is for one call at a time."""
         if q.dim() != 3 or tuple(q.shape[1:]) != (self.cfg.n_q_heads, self.cfg.head_dim):
             raise ValueError(f"chunk_attention: q must be [n_tokens, {self.cfg.n_q_heads}, {self.cfg.head_dim}]")
         if seq_start.numel() != self.batch + 1 or any(t is not None and t.numel() != self.batch for t in (ctx_lens, held)):
@@ -691,16 +694,21 @@ class KvqCache:
         with _memory_of(stream):
             if out is None:
                 out = torch.empty_like(q)
-            if workspace is None:
+            if workspace is not None:
+                kvq_chunk_attention(self.handle, q, seq_start, ctx_lens, out, workspace, stream, held)
+                return out
+            # a call is several launches, and the library releases the interpreter: threads that share a stream, and so
+            # a workspace, enqueue theirs one call after the other
+            with self.chunk_lock:
                 workspace = self._chunk_workspace(kvq_chunk_workspace_bytes(self.handle, q.dtype, q.shape[0]), q.device)
-        kvq_chunk_attention(self.handle, q, seq_start, ctx_lens, out, workspace, stream, held)
+                kvq_chunk_attention(self.handle, q, seq_start, ctx_lens, out, workspace, stream, held)
         return out
 
     def _chunk_workspace(self, need, device):
         # memory of the current stream: a workspace it outgrows is reused in its order
         if torch.cuda.is_current_stream_capturing():
             return torch.empty(need, dtype=torch.uint8, device=device)
-        kept, at = self.__dict__.setdefault("chunk_workspaces", {}), _stream()
+        kept, at = self.chunk_workspaces, _stream()
         have = kept.get(at)
         if have is None or have.numel() < need:
             have = kept[at] = torch.empty(need, dtype=torch.uint8, device=device)

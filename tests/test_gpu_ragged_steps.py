@@ -1,5 +1,7 @@
 """Steps of the ragged serving path one after the other on the GPU: buffers that are kept, requests that are refused,
 appends of every kernel, what calls share."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -169,4 +171,27 @@ def test_out_on_a_stream_given_by_name():
     assert at == [s.cuda_stream]
     s.synchronize()
     assert torch.equal(out, want)
+    x.cache.close()
+
+
+def test_threads_on_one_stream():
+    """Calls of four threads on the default stream, small and large, fp32 and bf16, without workspaces of their own."""
+    x = Batch(make_cfg(8, 2, 2, True, 2, True), [2000, 3, 70], [40, 2, 90], seed=25)
+    qs = [x.q, x.q.flip(0).contiguous(), x.q.float(), (0.5 * x.q).contiguous()]
+    want = [x.cache.chunk_attention(q, x.seq_start, x.ctx_lens) for q in qs]
+    torch.cuda.synchronize()
+    got = [[] for _ in qs]
+
+    def work(i):
+        for _ in range(20):
+            got[i].append(x.cache.chunk_attention(qs[i], x.seq_start, x.ctx_lens))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(qs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for outs, w in zip(got, want):
+        assert len(outs) == 20 and all(torch.equal(o, w) for o in outs)
+    assert len(x.cache.chunk_workspaces) == 1
     x.cache.close()

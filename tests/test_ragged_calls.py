@@ -2,6 +2,9 @@
 import contextlib
 import ctypes
 
+import threading
+import time
+
 import pytest
 import torch
 
@@ -24,6 +27,7 @@ def ptr(i):
 def bare_cache(batch=3, n_q_heads=8, n_kv_heads=2):
     c = object.__new__(kvq.KvqCache)
     c.batch, c.cfg, c.handle = batch, kvq.make_cfg(n_q_heads=n_q_heads, n_kv_heads=n_kv_heads), None
+    c.chunk_workspaces, c.chunk_lock = {}, threading.Lock()
     return c
 
 
@@ -123,3 +127,26 @@ def test_context_parallel_decode_on_a_named_stream_exchanges_there(lib, monkeypa
         assert streams.of(out) == (stream or "current")
     assert seen == [(n, s) for s in ("side", None) for n in ("states", "exchange", "merge")][:3] + [
         ("states", None), ("exchange", "current"), ("merge", None)]
+
+
+def test_threads_that_share_a_workspace_enqueue_in_turn(lib, monkeypatch):
+    """A call's kernels use its workspace one after the other: another thread's must not come between."""
+    Streams(monkeypatch)
+    inside, most, used = [], [], []
+
+    def enqueue(h, q, start, ctx, out, ws, stream, held=None):
+        inside.append(1)
+        used.append(ws)
+        time.sleep(0.02)
+        most.append(len(inside))
+        inside.pop()
+    monkeypatch.setattr(kvq, "kvq_chunk_workspace_bytes", lambda handle, dtype, n: 64)
+    monkeypatch.setattr(kvq, "kvq_chunk_attention", enqueue)
+    c, q, start = bare_cache(), torch.zeros(5, 8, 128), torch.zeros(4, dtype=torch.int32)
+    threads = [threading.Thread(target=lambda: [c.chunk_attention(q, start) for _ in range(3)]) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(most) == 12 and max(most) == 1
+    assert all(ws is used[0] for ws in used)
