@@ -692,6 +692,7 @@ class KvqCache:
         if q.dtype not in DTYPES:
             raise TypeError("q must be float32 or bfloat16")
         with _memory_of(stream):
+            _here("chunk_attention", q=q)  # before anything is made beside it
             if out is None:
                 out = torch.empty_like(q)
             if workspace is not None:
@@ -708,7 +709,8 @@ class KvqCache:
         # memory of the current stream: a workspace it outgrows is reused in its order
         if torch.cuda.is_current_stream_capturing():
             return torch.empty(need, dtype=torch.uint8, device=device)
-        kept, at = self.chunk_workspaces, _stream()
+        # every device's default stream has the handle 0
+        kept, at = self.chunk_workspaces, (device, _stream())
         have = kept.get(at)
         if have is None or have.numel() < need:
             have = kept[at] = torch.empty(need, dtype=torch.uint8, device=device)

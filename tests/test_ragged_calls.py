@@ -62,6 +62,7 @@ class Streams:
         monkeypatch.setattr(torch.cuda, "stream", self._switched)
         monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
         monkeypatch.setattr(kvq, "_stream", lambda s=None: s or self.current)
+        monkeypatch.setattr(kvq, "_here", lambda *args, **tensors: None)
 
     def _recorded(self, make):
         def made(*args, **kw):
@@ -150,3 +151,22 @@ def test_threads_that_share_a_workspace_enqueue_in_turn(lib, monkeypatch):
         t.join()
     assert len(most) == 12 and max(most) == 1
     assert all(ws is used[0] for ws in used)
+
+
+def test_a_workspace_is_kept_for_its_device(lib, monkeypatch):
+    """A call that is refused because its tensors are on another device than the cache leaves no workspace there for the
+    next call on the same stream handle."""
+    Streams(monkeypatch)
+    c = bare_cache()
+    wrong, right = torch.device("meta"), torch.device("cpu")
+    assert c._chunk_workspace(64, wrong).device == wrong
+    kept = c._chunk_workspace(64, right)
+    assert kept.device == right and c._chunk_workspace(32, right) is kept
+
+
+def test_attention_makes_nothing_beside_a_host_tensor(lib, monkeypatch):
+    c = bare_cache()
+    monkeypatch.setattr(kvq, "kvq_chunk_workspace_bytes", lambda handle, dtype, n: pytest.fail("asked for a workspace"))
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        c.chunk_attention(torch.zeros(5, 8, 128), torch.zeros(4, dtype=torch.int32))
+    assert not c.chunk_workspaces
