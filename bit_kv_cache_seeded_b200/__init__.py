@@ -684,7 +684,7 @@ class KvqCache:
         """Attention of a ragged batch of new tokens (kvq_chunk_attention; with held, the lengths before the step, refused
         requests get zeros); returns out, like q. Without a workspace the cache keeps one per stream, grown to the largest call there; a captured call takes one
         from the graph's own memory, so that no two graphs share it. Calls of several threads are enqueued one after
-        the other; a workspace of one's own is for one call at a time."""
+        the other; a workspace of one's own is for one call at a time. Kept workspaces go with close()."""
         if q.dim() != 3 or tuple(q.shape[1:]) != (self.cfg.n_q_heads, self.cfg.head_dim):
             raise ValueError(f"chunk_attention: q must be [n_tokens, {self.cfg.n_q_heads}, {self.cfg.head_dim}]")
         if seq_start.numel() != self.batch + 1 or any(t is not None and t.numel() != self.batch for t in (ctx_lens, held)):
@@ -726,6 +726,7 @@ class KvqCache:
         if self.handle:
             kvq_cache_destroy(self.handle)
             self.handle = None
+            self.chunk_workspaces.clear()
 
     def __del__(self):
         try:

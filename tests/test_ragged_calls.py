@@ -170,3 +170,14 @@ def test_attention_makes_nothing_beside_a_host_tensor(lib, monkeypatch):
     with pytest.raises(ValueError, match="CUDA tensor"):
         c.chunk_attention(torch.zeros(5, 8, 128), torch.zeros(4, dtype=torch.int32))
     assert not c.chunk_workspaces
+
+
+def test_close_gives_the_workspaces_back(lib, monkeypatch):
+    Streams(monkeypatch)
+    monkeypatch.setattr(kvq, "kvq_cache_destroy", lambda handle: None)
+    c = bare_cache()
+    c.handle = 1
+    c._chunk_workspace(64, torch.device("cpu"))
+    assert len(c.chunk_workspaces) == 1
+    c.close()
+    assert c.handle is None and not c.chunk_workspaces
