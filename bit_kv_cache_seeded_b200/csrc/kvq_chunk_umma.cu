@@ -34,7 +34,11 @@ using namespace chunk;
 
 constexpr int kStages = 4;
 constexpr int kTileRows = 128;        // of a CTA
-constexpr int kSlots = 16;            // of segments: values are never more than kStages pages, so segments, ahead
+// Slots of segments for the first position whose value norm is not finite. The values' first group resets a slot half a
+// round before its segment. It may be kStages + VG segments ahead of the softmax, where they are a page long: it stores
+// page n once the products have read page n - kStages, whose rows may still have their slot to read, and then walks on,
+// without a wait, to its next page, n + VG. The slot that it resets there belongs to the segment kSlots / 2 before.
+constexpr int kSlots = 32;
 constexpr float kLag = 8.f, kShift = 7.f;
 constexpr uint32_t kColS = 256, kTmemCols = 512;
 
@@ -44,6 +48,7 @@ struct Cfg {
   static constexpr int DK = KQ ? 256 : 128, DV = VQ ? 256 : 128;
   // groups of 2 warps that dequantise a side, page n on group n % G: twice as many where a sketch doubles the work
   static constexpr int KG = KQ ? 4 : 2, VG = VQ ? 4 : 2;
+  static_assert(kSlots / 2 > kStages + VG, "a slot is reset while the softmax may still read it");
   static constexpr int kWarpK = 4 * NT, kWarpV = kWarpK + 2 * KG, kWarpS = kWarpV + 2 * VG, kWarpO = kWarpS + 1;
   // With a key sketch 22 warps, and two more that only give their registers back: 80 a thread at launch, shared out
   // so that nothing spills (shared memory leaves the L1 too small to hold local memory).
@@ -387,7 +392,7 @@ __global__ void __launch_bounds__(Cfg<KQ, VQ>::kThreads, 1) chunk_umma(const __g
     while (w.next(set)) {
       const int ns = segment_pages(w), limit = w.rows.limit;
       if (ns == 0) continue;
-      if (th == 0 && grp == 0) bars.bad[(seg + kSlots / 2) % kSlots] = 0x7fffffff;  // last used half a round ago
+      if (th == 0 && grp == 0) bars.bad[(seg + kSlots / 2) % kSlots] = 0x7fffffff;  // last read before: kSlots
       const int first = (grp + C::VG - n % C::VG) % C::VG;  // this group's first page of the segment
       int page = w.k0 + first;
       if (first < ns) values.fetch(p, regs, page_tile(p, w, page, page_entry(p, w, page)));

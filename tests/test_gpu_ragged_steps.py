@@ -195,3 +195,41 @@ def test_threads_on_one_stream():
         assert len(outs) == 20 and all(torch.equal(o, w) for o in outs)
     assert len(x.cache.chunk_workspaces) == 1
     x.cache.close()
+
+
+# ---- values that are not finite, in many short segments
+
+@pytest.mark.parametrize("name", [(2, True, 2, True), (2, False, 3, True), (3, True, 3, False), (1, False, 1, False)])
+def test_values_that_are_not_finite_in_many_one_page_segments(name):
+    """More one-page segments a pair of CTAs than its ring of markers has slots, several of them with a token that is not
+    finite, at its first, a middle or its last position: the rows from that token on are NaN, and no other."""
+    B, group, heads = 700, 4, 4                    # 2800 row tiles of 72 to 256 rows on 74 pairs: 37 each
+    rng = np.random.default_rng(26)
+    new = rng.integers(18, 65, B)
+    start = np.concatenate([[0], np.cumsum(new)])
+    gen = torch.Generator(device="cuda").manual_seed(26)
+    v = torch.randn(int(start[-1]), heads, 128, generator=gen, device="cuda").to(BF16)
+    bad = {}
+    for b in rng.choice(B, 160, replace=False):
+        i, h = int(rng.choice([0, new[b] // 2, new[b] - 1])), int(rng.integers(heads))
+        v[start[b] + i, h, 5] = float(rng.choice([np.nan, np.inf]))
+        bad[b] = (i, h)
+    cfg = make_cfg(group * heads, heads, *name)
+    x = Batch(cfg, [0] * B, new, seed=26, v=v)
+    for _ in range(3):
+        out = x.cache.chunk_attention(x.q, x.seq_start, x.ctx_lens)
+        nan = torch.zeros(out.shape[:2], dtype=torch.bool, device="cuda")
+        for b, (i, h) in bad.items():
+            nan[start[b] + i:start[b + 1], h * group:(h + 1) * group] = True
+        assert torch.equal(out.isnan().all(-1), nan) and torch.equal(out.isnan().any(-1), nan)
+    # the finite ones of some requests, with and without a bad token in another head
+    table = x.table.cpu().numpy()
+    for b in [*list(bad)[:6], 0, 349, B - 1]:
+        for h in range(heads):
+            upto = bad[b][0] if b in bad and bad[b][1] == h else int(new[b])
+            K, V = dequantised(x.cache, cfg, table, b, h, int(new[b]), x.signs, x.S)
+            rows = (slice(start[b], start[b] + upto), slice(h * group, (h + 1) * group))
+            if upto:
+                assert_close(out[rows], causal_attention(x.q[rows].double().cpu().numpy(), K[:upto], V[:upto], upto), BF16)
+    assert kvq.kvq_cache_status(x.cache.handle) == 0
+    x.cache.close()
