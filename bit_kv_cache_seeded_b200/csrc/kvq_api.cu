@@ -1192,6 +1192,7 @@ kvq_status kvq_extend_block_table(const int32_t* held, const int32_t* n_new, int
                                   int32_t* seq_start, int32_t* ctx_lens, int32_t* taken, void* stream) {
   if (!held || !n_new || !block_table || !seq_start || !ctx_lens || !taken) return KVQ_ERR_INVALID_ARG;
   if (batch < 1 || pages_per_seq < 1 || n_free < 0 || (n_free > 0 && !free_pages)) return KVQ_ERR_INVALID_ARG;
+  if (batch > kMaxTableRequests) return KVQ_ERR_INVALID_ARG;
   if ((long)pages_per_seq * kTile * kTilePair > (1l << 30)) return KVQ_ERR_INVALID_ARG;
   const void* in[] = {held, n_new, free_pages, cursor};
   const void* out[] = {block_table, seq_start, ctx_lens, taken};

@@ -87,6 +87,9 @@ struct ChunkLayout {
   size_t qprep, qscale, total;
 };
 
+// Requests of one extend_block_table call: every block sums the counts of all requests before its own, work that
+// grows with the square of the batch, in 32-bit request numbers.
+constexpr int kMaxTableRequests = 1 << 20;
 cudaError_t launch_extend_block_table(const int* held, const int* n_new, int batch, const int* free_pages, int n_free,
                                       const int* cursor, int* table, int pages_per_seq, int* seq_start, int* ctx_lens,
                                       int* taken, cudaStream_t s);

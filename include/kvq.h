@@ -233,7 +233,7 @@ kvq_status kvq_combine_partials(const float* partials, int32_t n_parts, int32_t 
  * A request is refused, and gets no page, when held or n_new is negative, when held + n_new exceeds
  * 64 pages_per_seq, or when the pages of the requests up to it exceed the free ones; a request that
  * needs no page is never refused for want of them. A cursor outside [0, n_free] leaves no free page.
- * The entries of free_pages are not checked (calls that read the table check them). Outputs may be
+ * At most 2^20 requests. The entries of free_pages are not checked (calls that read the table check them). Outputs may be
  * neither inputs nor each other (KVQ_ERR_INVALID_ARG), nor overlap them. No cache needed; runs on the
  * current device. */
 kvq_status kvq_extend_block_table(const int32_t* held, const int32_t* n_new, int32_t batch, const int32_t* free_pages,

@@ -233,3 +233,30 @@ def test_values_that_are_not_finite_in_many_one_page_segments(name):
                 assert_close(out[rows], causal_attention(x.q[rows].double().cpu().numpy(), K[:upto], V[:upto], upto), BF16)
     assert kvq.kvq_cache_status(x.cache.handle) == 0
     x.cache.close()
+
+
+@pytest.mark.parametrize("n_free", [600000, 200000])
+def test_block_tables_of_the_most_requests(n_free):
+    """2^20 requests of up to 138 tokens that need 229000 pages: enough free pages, and too few."""
+    B, pps = 1 << 20, 2
+    gen = torch.Generator(device="cuda").manual_seed(27)
+    held = torch.randint(0, 100, (B,), generator=gen, device="cuda", dtype=torch.int32)
+    new = torch.randint(0, 40, (B,), generator=gen, device="cuda", dtype=torch.int32)
+    free = torch.randperm(n_free, generator=gen, device="cuda").int()
+    table, cursor = torch.full((B, pps), -7, dtype=torch.int32, device="cuda"), cuda_ints([5])
+    start, ctx, taken = cuda_ints(np.zeros(B + 1)), cuda_ints(np.zeros(B)), cuda_ints([0, 0])
+    kvq.kvq_extend_block_table(held, new, free, table, start, ctx, taken, cursor)
+    h, n = held.long(), new.long()
+    fits = h + n <= pps * PAGE
+    p0, p1 = (h + PAGE - 1) // PAGE, (h + n + PAGE - 1) // PAGE
+    need = torch.where(fits, p1 - p0, 0)
+    end = need.cumsum(0)
+    ok = fits & ((need == 0) | (end <= free.numel() - 5))
+    assert bool((~ok & fits).any()) == (n_free == 200000)
+    page = torch.arange(pps, device="cuda")
+    mine = ok[:, None] & (page >= p0[:, None]) & (page < p1[:, None])
+    at = (5 + (end - need - p0)[:, None] + page).clamp(0, free.numel() - 1)
+    assert torch.equal(table, torch.where(mine, free[at], -7))
+    assert torch.equal(start[1:].long(), n.cumsum(0)) and int(start[0]) == 0
+    assert torch.equal(ctx.long(), torch.where(ok, h + n, h))
+    assert taken.tolist() == [int((need * ok).sum()), int((~ok).sum())]

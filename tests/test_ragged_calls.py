@@ -181,3 +181,12 @@ def test_close_gives_the_workspaces_back(lib, monkeypatch):
     assert len(c.chunk_workspaces) == 1
     c.close()
     assert c.handle is None and not c.chunk_workspaces
+
+
+def test_block_tables_of_too_many_requests_are_refused(lib):
+    """A block walks all requests before its own: near 2^31 of them its counter would wrap, and long before that the call
+    would take minutes."""
+    n = kvq.kvq_kernel_launches()
+    for batch in ((1 << 20) + 1, 2 ** 31 - 8, 2 ** 31 - 1):
+        assert lib.kvq_extend_block_table(ptr(0), ptr(1), batch, ptr(2), 10, None, ptr(4), 8, ptr(5), ptr(6), ptr(7), None) == INVALID
+    assert kvq.kvq_kernel_launches() == n
