@@ -1177,6 +1177,8 @@ extern "C" kvq_status kvq_decode_attention_static(const kvq_cache* c, const void
 namespace {
 // Exponent of two that brings S's largest entry to [2^9, 2^10), kept behind the staged tables (0 without a sketch).
 int sketch_exp(const kvq_cache* c) { return c->h_tables.empty() ? 0 : (int)c->h_tables.back(); }
+// Chunk attention counts a row tile's query bytes in 32 bits: 512 / group tokens of n_q_heads rows of 512 bytes.
+constexpr int kMaxChunkHeads = 8192;
 // The cache kinds the ragged path handles: rotated codes, no bf16 window.
 bool ragged_supported(const kvq_cache* c) { return !c->is_fp4 && !has_window(c); }
 bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -1306,7 +1308,7 @@ kvq_status kvq_quantize_slots_rows(kvq_cache* c, const void* K, const void* V, k
 kvq_status kvq_chunk_workspace_bytes(const kvq_cache* c, kvq_dtype dtype, int32_t n_tokens, size_t* bytes) {
   if (!c || !bytes || n_tokens < 0) return KVQ_ERR_INVALID_ARG;
   if (dtype != KVQ_F32 && dtype != KVQ_BF16) return KVQ_ERR_INVALID_ARG;
-  if (!ragged_supported(c)) return KVQ_ERR_UNSUPPORTED;
+  if (!ragged_supported(c) || c->cfg.n_kv_heads > kMaxChunkHeads) return KVQ_ERR_UNSUPPORTED;
   if ((long)n_tokens * c->cfg.n_q_heads > (1l << 30)) return KVQ_ERR_INVALID_ARG;
   *bytes = chunk_layout_of(c, n_tokens, dtype == KVQ_BF16).total;
   return KVQ_OK;
@@ -1320,7 +1322,7 @@ kvq_status chunk_attention_impl(const kvq_cache* c, const void* q, kvq_dtype dty
                                 void* workspace, size_t ws_bytes, void* stream) {
   if (!c || n_tokens < 0) return KVQ_ERR_INVALID_ARG;
   if (dtype != KVQ_F32 && dtype != KVQ_BF16) return KVQ_ERR_INVALID_ARG;
-  if (!ragged_supported(c)) return KVQ_ERR_UNSUPPORTED;
+  if (!ragged_supported(c) || c->cfg.n_kv_heads > kMaxChunkHeads) return KVQ_ERR_UNSUPPORTED;
   if (n_tokens == 0) return KVQ_OK;
   if (!q || !seq_start || !out || !workspace) return KVQ_ERR_INVALID_ARG;
   if ((long)n_tokens * c->cfg.n_q_heads > (1l << 30)) return KVQ_ERR_INVALID_ARG;

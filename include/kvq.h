@@ -284,7 +284,8 @@ kvq_status kvq_cache_set_lengths(kvq_cache* c, const int32_t* lens, void* stream
  * kvq_decode_attention (n_new = 1 for every request computes the same attention); f32 queries are
  * computed in fp32, bf16 ones on the tensor cores in fp16 with fp32 sums and statistics (value norms under 2^-10
  * keep fewer than fp16's 11 bits there).
- * LM, LM_QJL and SIGN1 caches without a window, paged or not; others KVQ_ERR_UNSUPPORTED. n_tokens * n_q_heads may not
+ * LM, LM_QJL and SIGN1 caches without a window and of at most 8192 kv-heads, paged or not; others
+ * KVQ_ERR_UNSUPPORTED. n_tokens * n_q_heads may not
  * exceed 2^30. A block-table entry outside the pool sets KVQ_STATUS_BAD_PAGE and reads page 0. The
  * workspace (kvq_chunk_workspace_bytes for this type and n_tokens) is in use until the call's work is
  * done: calls that may overlap, and graphs that may replay at the same time, need one each. It holds a softmax state

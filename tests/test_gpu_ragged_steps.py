@@ -260,3 +260,25 @@ def test_block_tables_of_the_most_requests(n_free):
     assert torch.equal(start[1:].long(), n.cumsum(0)) and int(start[0]) == 0
     assert torch.equal(ctx.long(), torch.where(ok, h + n, h))
     assert taken.tolist() == [int((need * ok).sum()), int((~ok).sum())]
+
+
+def test_chunk_attention_of_the_most_heads():
+    """A row tile of 512 tokens and 8192 heads ends just below 2^31 bytes of queries; more heads are refused."""
+    cfg = make_cfg(8192, 8192, 3, True, 3, False)
+    x = Batch(cfg, [0], [512], seed=28)
+    out = x.cache.chunk_attention(x.q, x.seq_start, x.ctx_lens)
+    table = x.table.cpu().numpy()
+    for h in (0, 8191):
+        K, V = dequantised(x.cache, cfg, table, 0, h, 512, x.signs, x.S)
+        assert_close(out[:, h:h + 1], causal_attention(x.q[:, h:h + 1].double().cpu().numpy(), K, V, 512), BF16)
+    assert kvq.kvq_cache_status(x.cache.handle) == 0
+    x.cache.close()
+    more = kvq.KvqCache(make_cfg(8193, 8193, 3, True, 3, False), 1, 64, x.signs, x.S)
+    n = kvq.kvq_kernel_launches()
+    q, ws = torch.zeros(65, 8193, 128, dtype=BF16, device="cuda"), torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    for call in (lambda: more.chunk_attention(q, cuda_ints([0, 65])), lambda: more.chunk_attention(q, cuda_ints([0, 65]), workspace=ws)):
+        with pytest.raises(kvq.KvqError) as e:
+            call()
+        assert e.value.status == 2
+    assert kvq.kvq_kernel_launches() == n
+    more.close()
