@@ -190,3 +190,22 @@ def test_block_tables_of_too_many_requests_are_refused(lib):
     for batch in ((1 << 20) + 1, 2 ** 31 - 8, 2 ** 31 - 1):
         assert lib.kvq_extend_block_table(ptr(0), ptr(1), batch, ptr(2), 10, None, ptr(4), 8, ptr(5), ptr(6), ptr(7), None) == INVALID
     assert kvq.kvq_kernel_launches() == n
+
+
+def test_counts_of_more_than_32_bits_are_refused(lib, monkeypatch):
+    """Not cut down to their low 32 bits: 2^32 + 5 new tokens are not 5."""
+    monkeypatch.setattr(kvq, "_here", lambda *args, **tensors: None)
+    monkeypatch.setattr(kvq, "load", lambda: pytest.fail("reached the library"))
+    many = 2 ** 32 + 5
+    i32 = lambda *n: torch.empty(n, dtype=torch.int32, device="meta")  # noqa: E731
+    x = torch.empty(many, 1, 128, device="meta")
+    calls = [lambda: kvq.kvq_chunk_workspace_bytes(None, torch.float32, many),
+             lambda: kvq.kvq_extend_block_table(i32(2), i32(2), i32(many), i32(2, 3), i32(3), i32(2), i32(2)),
+             lambda: kvq.kvq_extend_block_table(i32(many), i32(many), i32(4), i32(many, 1), i32(many + 1), i32(many), i32(2)),
+             lambda: kvq.kvq_slot_map(i32(2), i32(3), i32(2), i32(2, 3), 4, None, None, i32(many)),
+             lambda: kvq.kvq_slot_map(i32(2), i32(3), i32(2), i32(2, 3), many, None, None, i32(4)),
+             lambda: kvq.kvq_quantize_slots(None, x, x, i32(many)),
+             lambda: kvq.kvq_chunk_attention(None, x, i32(2), None, x, i32(4))]
+    for call in calls:
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
