@@ -282,3 +282,42 @@ def test_chunk_attention_of_the_most_heads():
         assert e.value.status == 2
     assert kvq.kvq_kernel_launches() == n
     more.close()
+
+
+# ---- appends of blocks of 32 tokens
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("tokens", [700, 1211, 1700])
+@pytest.mark.parametrize("name", [(2, True, 2, True), (3, True, 3, False), (2, False, 3, True), (2, False, 2, False),
+                                  (1, False, 1, False), (1, True, 2, False)])
+def test_large_appends_in_any_order(name, tokens, dtype):
+    """Shuffled slots, runs that begin inside an octet, skipped tokens and slots past the pool inside a block, a zero vector,
+    a rotation per head: the bytes of calls of 100 tokens, whose kernel is compared with kvq_quantize."""
+    cfg = make_cfg(8, 8, *name, rot_per_head=1)
+    signs, S = signs_and_sketch(29, cfg)
+    n_pages = tokens // PAGE + 4
+    gen = torch.Generator(device="cuda").manual_seed(tokens)
+    K, V = (torch.randn(tokens, 8, 128, generator=gen, device="cuda").to(dtype) for _ in range(2))
+    K[33], V[tokens // 2] = 0, 0
+    table = cuda_ints(np.full((1, n_pages), -1))
+    run = 5 + torch.arange(tokens, device="cuda")
+    holes = run.clone()
+    holes[3::7] = -torch.arange(1, len(holes[3::7]) + 1, device="cuda")
+    holes[40:45] = n_pages * PAGE + torch.arange(5, device="cuda")
+    holes[tokens - 3] = 2 ** 62
+    shuffled = torch.randperm(n_pages * PAGE, generator=gen, device="cuda")[:tokens]
+    shuffled[50] = -1
+    turned = torch.where(run // 8 % 2 == 0, run ^ 7, run)  # octets backwards, every other one
+    turned[turned >= 5 + tokens] = -2
+    for slots, status in ((run, 0), (run.flip(0).contiguous(), 0), (shuffled, 0), (turned, 0), (holes, 2)):
+        large, small = (kvq.KvqCache(cfg, 1, 0, signs, S, block_table=table, n_pages=n_pages) for _ in range(2))
+        first = int(large.layout()[4])
+        for c in (large, small):
+            c.arena[first:].fill_(0x5A)
+        large.quantize_slots(K, V, slots)
+        for i in range(0, tokens, 100):
+            small.quantize_slots(K[i:i + 100], V[i:i + 100], slots[i:i + 100])
+        assert torch.equal(large.arena[first:], small.arena[first:])
+        assert kvq.kvq_cache_status(large.handle) == status
+        large.close()
+        small.close()
