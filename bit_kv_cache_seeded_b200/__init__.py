@@ -373,11 +373,13 @@ def _here(fn: str, dtype=None, **tensors):
             raise ValueError(f"{fn}: {name} is on {t.device}, not on the current device")
 
 
-def _int32(fn: str, *counts):
-    """Counts that the library takes as int32; ctypes would cut the others down to 32 bits without a word."""
-    for n in counts:
-        if not -2**31 <= n < 2**31:
-            raise ValueError(f"{fn}: {n} does not fit 32 bits")
+# Counts that the library takes as int32 are compared with this (in place: a call takes a few microseconds); ctypes would
+# cut larger ones down to 32 bits without a word.
+INT32_MAX = 2**31 - 1
+
+
+def _too_many(fn: str):
+    return ValueError(f"{fn}: a count that does not fit 32 bits")
 
 
 def kvq_extend_block_table(held: torch.Tensor, n_new: torch.Tensor, free_pages: torch.Tensor, block_table: torch.Tensor,
@@ -393,8 +395,10 @@ def kvq_extend_block_table(held: torch.Tensor, n_new: torch.Tensor, free_pages: 
             or ctx_lens.numel() != B or taken.numel() != 2 or (cursor is not None and cursor.numel() != 1):
         raise ValueError(f"{fn}: held, n_new, ctx_lens [batch], seq_start [batch + 1], block_table [batch, pages_per_seq], "
                          "taken [2], cursor [1]")
-    _int32(fn, B, free_pages.numel(), shape[1])
-    _check(fn, load().kvq_extend_block_table(held.data_ptr(), n_new.data_ptr(), B, free_pages.data_ptr(), free_pages.numel(),
+    n_free = free_pages.numel()
+    if B > INT32_MAX or n_free > INT32_MAX or shape[1] > INT32_MAX:
+        raise _too_many(fn)
+    _check(fn, load().kvq_extend_block_table(held.data_ptr(), n_new.data_ptr(), B, free_pages.data_ptr(), n_free,
                                              None if cursor is None else cursor.data_ptr(), block_table.data_ptr(), shape[1],
                                              seq_start.data_ptr(), ctx_lens.data_ptr(), taken.data_ptr(), _stream(stream)))
 
@@ -412,7 +416,8 @@ def kvq_slot_map(held: torch.Tensor, seq_start: torch.Tensor, ctx_lens: torch.Te
             or (seq_ids is not None and seq_ids.numel() != n) or (positions is not None and positions.numel() != n):
         raise ValueError(f"{fn}: held, ctx_lens [batch], seq_start [batch + 1], block_table [batch, pages_per_seq], "
                          "seq_ids, positions, slots [n_tokens]")
-    _int32(fn, B, shape[1], n_pages, n)
+    if B > INT32_MAX or shape[1] > INT32_MAX or n > INT32_MAX or not -INT32_MAX <= n_pages <= INT32_MAX:
+        raise _too_many(fn)
     _check(fn, load().kvq_slot_map(held.data_ptr(), seq_start.data_ptr(), ctx_lens.data_ptr(), B, block_table.data_ptr(),
                                    shape[1], n_pages, n, None if seq_ids is None else seq_ids.data_ptr(),
                                    None if positions is None else positions.data_ptr(), slots.data_ptr(), _stream(stream)))
@@ -427,15 +432,19 @@ def kvq_quantize_slots(handle, K: torch.Tensor, V: torch.Tensor, slots: torch.Te
         raise TypeError("K and V must both be float32 or bfloat16")
     _here(fn, K=K, V=V)
     _here(fn, torch.int64, slots=slots)
-    _here(fn, torch.int32, seq_start=seq_start)
+    if seq_start is not None:
+        _here(fn, torch.int32, seq_start=seq_start)
     if K.dim() != 3 or K.shape != V.shape or slots.numel() != K.shape[0]:
         raise ValueError("K and V must be [n_tokens, n_kv_heads, head_dim] and slots [n_tokens]")
-    _int32(fn, K.shape[0])
-    args = handle, K.data_ptr(), V.data_ptr(), DTYPES[K.dtype], slots.data_ptr(), K.shape[0]
+    n = K.shape[0]
+    if n > INT32_MAX:
+        raise _too_many(fn)
     if seq_start is None:
-        _check(fn, load().kvq_quantize_slots(*args, _stream(stream)))
+        _check(fn, load().kvq_quantize_slots(handle, K.data_ptr(), V.data_ptr(), DTYPES[K.dtype], slots.data_ptr(), n,
+                                             _stream(stream)))
     else:
-        _check(fn, load().kvq_quantize_slots_rows(*args, seq_start.data_ptr(), _stream(stream)))
+        _check(fn, load().kvq_quantize_slots_rows(handle, K.data_ptr(), V.data_ptr(), DTYPES[K.dtype], slots.data_ptr(), n,
+                                                  seq_start.data_ptr(), _stream(stream)))
 
 
 def kvq_cache_set_lengths(handle, lens, batch: int, stream=None):
@@ -449,7 +458,8 @@ def kvq_cache_set_lengths(handle, lens, batch: int, stream=None):
 
 def kvq_chunk_workspace_bytes(handle, dtype, n_tokens: int) -> int:
     out = ctypes.c_size_t()
-    _int32("kvq_chunk_workspace_bytes", n_tokens)
+    if not -INT32_MAX <= n_tokens <= INT32_MAX:
+        raise _too_many("kvq_chunk_workspace_bytes")
     _check("kvq_chunk_workspace_bytes",
            load().kvq_chunk_workspace_bytes(handle, DTYPES[dtype], n_tokens, ctypes.byref(out)))
     return out.value
@@ -468,7 +478,8 @@ def kvq_chunk_attention(handle, q: torch.Tensor, seq_start: torch.Tensor, ctx_le
     _here(fn, torch.int32, seq_start=seq_start, ctx_lens=ctx_lens, held=held)
     if q.dim() != 3 or out.shape != q.shape:
         raise ValueError("q and out must be [n_tokens, n_q_heads, head_dim]")
-    _int32(fn, q.shape[0])
+    if q.shape[0] > INT32_MAX:
+        raise _too_many(fn)
     first = (handle, q.data_ptr(), DTYPES[q.dtype], q.shape[0], seq_start.data_ptr(),
              None if ctx_lens is None else ctx_lens.data_ptr())
     last = out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)
