@@ -1288,6 +1288,7 @@ kvq_status quantize_slots_impl(kvq_cache* c, const void* K, const void* V, kvq_d
   p.St = c->d_St;
   p.s_exp = sketch_exp(c);
   p.err = c->d_status;
+  p.sms = c->sms;
   return launch_quantize_slots(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 }  // namespace

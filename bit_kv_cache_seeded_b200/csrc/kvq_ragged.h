@@ -28,6 +28,7 @@ struct SlotQuantizeParams {
   const float* St;
   int s_exp;                // S / 2^s_exp is within fp16's range
   int* err;
+  int sms;
 };
 
 // Chunk attention (kvq_chunk.cu): the workspace is laid out by chunk_layout(). The requests of one set are those

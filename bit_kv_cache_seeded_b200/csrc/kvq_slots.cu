@@ -424,7 +424,7 @@ cudaError_t launch_slots(const SlotQuantizeParams& p, int first, int sides, bool
   const long long blocks = (long long)((p.n_tokens + TOK - 1) / TOK) * p.heads;
   cudaLaunchConfig_t config = {};
   // as many blocks as fit, of a side: they keep their fragments of S from one group to the next
-  config.gridDim = dim3((unsigned)std::min<long long>(blocks, 148 * kAppBlocks<QJL>), sides);
+  config.gridDim = dim3((unsigned)std::min<long long>(blocks, p.sms * kAppBlocks<QJL>), sides);
   config.blockDim = dim3(kAppThreads);
   config.stream = s;
   cudaLaunchAttribute attr;
@@ -464,12 +464,12 @@ cudaError_t launch_quantize_slots(const SlotQuantizeParams& p, cudaStream_t s) {
   // 2-bit codes and sketches, TOK 8 against 32: 8.2 / 12.7 us at 16 groups, 16.7 / 16.2 at 80, 23.6 / 20.8 at 152, 65.9 /
   // 48.0 at 592. One bit without sketches, the kernel that may have one against the other: 10.6 / 10.5 us at 152 groups,
   // 15.8 / 12.6 at 296, 27.0 / 20.5 at 592; 3 bits and a sketch on one side, both sides at once against a launch each: 22.9 /
-  // 24.5 at 296, 39.3 / 35.7 at 592
+  // 24.5 at 296, 39.3 / 35.7 at 592. On 148 SMs: a group an SM, and 2.7 of them
   const long long groups = (long long)((p.n_tokens + 31) / 32) * p.heads;
   const bool k = p.side[0].qjl, v = p.side[1].qjl;
-  if (groups < 148) return launch_slots<8, true>(p, 0, 2, false, false, s);
+  if (groups < p.sms) return launch_slots<8, true>(p, 0, 2, false, false, s);
   if (!k && !v) return launch_slots<32, false>(p, 0, 2, false, false, s);
-  if (k == v || groups < 400) return launch_slots<32, true>(p, 0, 2, false, false, s);
+  if (k == v || 10 * groups < 27ll * p.sms) return launch_slots<32, true>(p, 0, 2, false, false, s);
   const cudaError_t e = launch_slots<32, true>(p, k ? 0 : 1, 1, true, false, s);
   return e != cudaSuccess ? e : launch_slots<32, false>(p, k ? 1 : 0, 1, false, true, s);
 }
