@@ -1,14 +1,15 @@
-// Attention of a ragged batch of new tokens over the packed LM / LM_QJL / SIGN1 cache: host plan, query
-// prep, the fp32 segment kernel, and the merge (bf16's segment kernel: kvq_chunk_umma.cu). ("TurboQuant vs OSCAR vs EpiCache", section
-// "Quantization frontiers: TurboQuant and OSCAR": rotation, Lloyd-Max codes, QJL sketch; kernels
-// compatible with paged attention.)
+// Attention of a ragged batch of new tokens over the packed LM / LM_QJL / SIGN1 cache: plan, query
+// prep, the fp32 segment kernel, and the merge (bf16's segment kernels: kvq_chunk_umma.cu, kvq_chunk_narrow.cu).
+// ("TurboQuant vs OSCAR vs EpiCache", section "Quantization frontiers: TurboQuant and OSCAR": rotation, Lloyd-Max codes,
+// QJL sketch; kernels compatible with paged attention.)
 //
 // With R = H D / sqrt(d), a key k_t is held as n_t / sqrt(d) R^T (c[code] + kappa gamma_t S^T z_t), kappa =
 // sqrt(pi/2) / m. Rotating and sketching the query once (q~ = R q, s = kappa S q~) leaves
 //   logit_t = scale n_t / sqrt(d) (<q~, c[code_t]> + gamma_t <s, z_t>),
 // and the value sum is rotated back once per row:
 //   out = D H / d (sum_t w_t c[code_t] + kappa S^T sum_t w_t gamma_t z_t) / sum_t p_t,  w_t = p_t n_t.
-// Three launches: prep (plan and queries), segments (kvq_chunk.cuh), merge.
+// Launches: prep (plan and queries), segments (kvq_chunk.cuh), merge. fp32 calls have one segment kernel, bf16 ones up to
+// three: the wide one, where the call is large enough for it, and the narrow one, with a value sketch in two instances.
 #include <algorithm>
 
 #include <cuda_bf16.h>

@@ -2,9 +2,9 @@
 // segments leave behind.
 //
 // Rows. A kv-head of request b has n_b * group query rows, row r = token r / group, head r % group. A set (ChunkSet)
-// takes the requests whose rows are within its bounds. (A pair of CTAs counts as one CTA here.) Row tiles of `rows` rows never cross a request; the tiles of
+// takes the requests whose rows are within its bounds. Row tiles of `rows` rows never cross a request; the tiles of
 // request b are tile_start[b] .. tile_start[b + 1] - 1, and tile_rows[t] describes tile t, so that a segment starts one
-// load after it knows its tile.
+// load after it knows its tile. Below, "CTA" is a pair of them in the wide set.
 //
 // Units. Tile t attends to the positions below its limit, the last row's position + 1, in units of one or two
 // 64-token pages; unit_start[t] is the prefix sum of max(1, ceil(limit / unit)). The units of all kv-heads

@@ -40,7 +40,7 @@ struct Cfg {
   // warps: softmax first, then keys, values, the two that issue; the others only give their registers back
   static constexpr int kWarpK = N / 8, kWarpV = kWarpK + 8, kWarpS = kWarpV + 8, kWarpO = kWarpS + 1;
   // Registers a thread, launched with 72. Nothing may spill where it recurs, since shared memory leaves the L1 too small to
-  // hold local memory. 8 * 88 + 16 * 72 + 4 * 40 and 4 * 104 + 16 * 72 + 8 * 56 are 28 * 72, on every quarter of the SM.
+  // hold local memory (instances with a value sketch spill one or two registers, 4 or 8 bytes). 8 * 88 + 16 * 72 + 4 * 40 and 4 * 104 + 16 * 72 + 8 * 56 are 28 * 72, on every quarter of the SM.
   static constexpr int kRegsSoftmax = N == 32 ? 104 : 88, kRegsDequant = 72, kRegsIssue = N == 32 ? 56 : 40;
   static constexpr int kPBytes = kStep * N * 2;  // P^T: [16 token groups][N / 8 row groups] of 8 tokens x 16 bytes
   static constexpr int kQBytes = N * DK * 2, kKStage = kStep * 256, kVPage = DV * 128;
