@@ -21,7 +21,7 @@ def _lib():
 
 
 class Server:
-    """The README's step, on buffers of a fixed size that are never filled between steps."""
+    """A server's step, on buffers of a fixed size that are never filled between steps."""
 
     def __init__(self, cfg, batch, pages_per_seq, n_pages, rows, dtype=BF16, seed=0):
         self.cfg, self.n_pages = cfg, n_pages
@@ -321,3 +321,108 @@ def test_large_appends_in_any_order(name, tokens, dtype):
         assert kvq.kvq_cache_status(large.handle) == status
         large.close()
         small.close()
+
+
+@pytest.mark.parametrize("name", [(2, True, 2, True), (3, True, 3, False), (1, True, 2, False)])
+@pytest.mark.parametrize("tokens", [100, 700])
+def test_a_slot_named_twice_leaves_its_neighbours(tokens, name):
+    """Within a block of tokens, and between blocks far apart; the other tokens' codes, signs and norms are those of a call
+    without the second mention."""
+    cfg = make_cfg(8, 8, *name)
+    signs, S = signs_and_sketch(30, cfg)
+    n_pages = tokens // PAGE + 2
+    gen = torch.Generator(device="cuda").manual_seed(30)
+    K, V = (torch.randn(tokens, 8, 128, generator=gen, device="cuda").to(BF16) for _ in range(2))
+    table = cuda_ints(np.arange(n_pages)[None])
+    twice, once = (kvq.KvqCache(cfg, 1, 0, signs, S, block_table=table, n_pages=n_pages) for _ in range(2))
+    for c in (twice, once):
+        c.arena[int(c.layout()[4]):].zero_()
+    slots = torch.arange(tokens, device="cuda")
+    named = slots.clone()
+    again = {4: 3, 20: 60, tokens - 1: 8, tokens - 9: 9, 33: 33 - 16}   # row: the slot it names too
+    for row, slot in again.items():
+        named[row] = slot
+        slots[row] = -1
+    twice.quantize_slots(K, V, named)
+    once.quantize_slots(K, V, slots)
+    keep = [t for t in range(tokens) if t not in again and t not in again.values()]
+    for h in (0, 7):
+        for a, b in zip(dequantised(twice, cfg, table.cpu().numpy(), 0, h, tokens, signs, S),
+                        dequantised(once, cfg, table.cpu().numpy(), 0, h, tokens, signs, S)):
+            np.testing.assert_array_equal(a[keep], b[keep])
+    assert kvq.kvq_cache_status(twice.handle) == 0
+    twice.close()
+    once.close()
+
+
+def test_pages_behind_4_gib_of_a_pool():
+    """The same tokens on the first pages of a small pool and on the last pages of one of 4.9 GB a side: the same bits."""
+    cfg = make_cfg(16, 8, 3, True, 3, True)
+    signs, S = signs_and_sketch(31, cfg)
+    held, new = [500, 70, 0], [90, 3, 200]
+    tokens = sum(held) + sum(new)
+    gen = torch.Generator(device="cuda").manual_seed(31)
+    K, V = (torch.randn(tokens, 8, 128, generator=gen, device="cuda").to(BF16) for _ in range(2))
+    q = torch.randn(sum(new), 16, 128, generator=gen, device="cuda")
+    results = []
+    for n_pages, free in ((20, np.arange(20)), (140000, 139999 - np.arange(20))):
+        table = torch.full((3, 10), -1, dtype=torch.int32, device="cuda")
+        c = kvq.KvqCache(cfg, 3, 0, signs, S, block_table=table, n_pages=n_pages)
+        info = c.layout()
+        assert n_pages == 20 or int(info[1]) * 16 * (n_pages - 20) > 2 ** 32
+        start, ctx, taken, cursor, at, got = cuda_ints([0] * 4), cuda_ints([0] * 3), cuda_ints([0, 0]), cuda_ints([0]), 0, []
+        for have, more in (([0] * 3, held), (held, new)):
+            n = sum(more)
+            slots = torch.empty(n, dtype=torch.int64, device="cuda")
+            kvq.kvq_extend_block_table(cuda_ints(have), cuda_ints(more), cuda_ints(free), table, start, ctx, taken, cursor)
+            kvq.kvq_slot_map(cuda_ints(have), start, ctx, table, n_pages, None, None, slots)
+            c.quantize_slots(K[at:at + n], V[at:at + n], slots, seq_start=start)
+            cursor += taken[:1]
+            at += n
+        assert int(taken[1]) == 0
+        for dtype in (BF16, F32):
+            got.append(c.chunk_attention(q.to(dtype), start, ctx, held=cuda_ints(held)))
+        c.set_lengths([h + n for h, n in zip(held, new)])
+        got.append(c.decode(q[:3].contiguous()))
+        assert kvq.kvq_cache_status(c.handle) == 0
+        results.append(got)
+        c.close()
+        del c
+    for a, b in zip(*results):
+        assert a.isfinite().all() and torch.equal(a, b)
+
+
+def test_captured_steps_without_a_fill_and_with_refusals():
+    """The whole step captured once and replayed with long steps, short ones, empty ones and refused requests, against the
+    same steps made eagerly: the same pools, lengths and results."""
+    cfg, rows = make_cfg(8, 2, 2, True, 2, True), 200
+    plan = [[120, 3, 0, 64], [1, 1, 1, 1], [0, 0, 0, 0], [5, 190, 1, 0], [1, 0, 130, 60], [-4, 2, 1, 1], [60, 60, 0, 70]]
+    results = []
+    for captured in (True, False):
+        s = Server(cfg, 4, 4, 9, rows, seed=32)
+        out, got = torch.zeros_like(s.q), []
+
+        def step():
+            s.append()
+            s.cache.chunk_attention(s.q, s.start, s.ctx, out=out, held=s.held)
+            s.advance()
+        if captured:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                step()
+        for new in plan:
+            s.inputs(new)
+            out.fill_(3.0)
+            g.replay() if captured else step()
+            got += [out.clone(), s.held.clone(), s.taken.clone(), s.cache.arena[s.first:].clone()]
+        assert kvq.kvq_cache_status(s.cache.handle) == 0
+        results.append(got)
+        if captured:
+            del g
+        s.cache.close()
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    refused = [int(t[1]) for t in results[0][2::4]]
+    assert refused[:3] == [0, 0, 0] and sum(refused) >= 3
+    total = [min(rows, sum(max(n, 0) for n in new)) for new in plan]
+    assert all((o[n:] == 3).all() for o, n in zip(results[0][::4], total))
